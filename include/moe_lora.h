@@ -319,6 +319,132 @@ int moe_lora_forward_timed(const moe_lora_shape* shape, const uint16_t* x, const
                            void* workspace, size_t ws_bytes, uint16_t* y, void* stream,
                            moe_lora_profiler* prof);
 
+/* ------------------------------------------------------------------------
+ * Dense blocks beside the routed experts: the gated feed-forward block with
+ * its backward pass, products and the same block on 4-bit weights, and the
+ * clipping of gradients.  The conventions above hold (caller's buffers and
+ * stream, checks before anything is launched); in addition no output and no
+ * workspace may share memory with an input or with another output
+ * (MOE_LORA_EINVAL) unless a call says so.
+ * ------------------------------------------------------------------------ */
+
+/* Gates: act(g) of h = act(g) * u. */
+#define MOE_LORA_ACT_SILU 0 /* g / (1 + exp(-g))                                  */
+#define MOE_LORA_ACT_GELU 1 /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2    */
+
+/* A gated feed-forward block (a dense layer's, or the shared expert beside
+ * the routed ones).  T may be 0. */
+typedef struct moe_lora_ffn_shape {
+  int32_t T;   /* tokens (up to 2^26)                                  */
+  int32_t H;   /* hidden size, a multiple of 8 (up to 2^20)            */
+  int32_t I;   /* intermediate size, a multiple of 8 (up to 2^20)      */
+  int32_t act; /* MOE_LORA_ACT_*                                       */
+} moe_lora_ffn_shape;
+
+/* Bytes of workspace for the forward (backward = 0), or for either call
+ * (backward != 0); 0 when the shape is invalid.  Host only, pure. */
+size_t moe_lora_ffn_workspace_bytes(const moe_lora_ffn_shape* shape, int backward);
+
+/* The block's forward:
+ *     [g u] = x W_gu^T,  h = act(g) * u,  y = h W_down^T
+ *   x       device [T][H] bf16
+ *   W_gu    device [2I][H] bf16, rows 0..I-1 = gate, rows I..2I-1 = up
+ *   W_down  device [H][I] bf16
+ *   gu      device [T][2I] fp32: g and u of every token, written for the
+ *           backward; NULL where none follows
+ *   y       device [T][H] bf16, overwritten
+ * Sums and the gate are fp32; h is rounded to bf16 once, between the two
+ * products, and y once.  The same inputs give the same bits. */
+int moe_lora_ffn_forward(const moe_lora_ffn_shape* shape, const uint16_t* x, const uint16_t* W_gu,
+                         const uint16_t* W_down, float* gu, void* workspace, size_t ws_bytes, uint16_t* y,
+                         void* stream);
+
+/* The block's backward, from dy and what the forward kept:
+ *     dh = dy W_down,  dg = dh * u * act'(g),  du = dh * act(g)
+ *     dx = [dg du] W_gu,  dW_gu = [dg du]^T x,  dW_down = dy^T h
+ *   dy, x            device [T][H] bf16
+ *   gu               device [T][2I] fp32, as the forward wrote it
+ *   dx               device [T][H] bf16 or NULL (not wanted)
+ *   dW_gu, dW_down   device, shaped as the weights, bf16 or NULL; at least
+ *                    one of the three is wanted
+ * Gradients are overwritten (with zeros for T = 0), not added to.  dg, du and
+ * h are rounded to bf16 once, before the products that take them.  The same
+ * inputs give the same bits. */
+int moe_lora_ffn_backward(const moe_lora_ffn_shape* shape, const uint16_t* dy, const uint16_t* x, const float* gu,
+                          const uint16_t* W_gu, const uint16_t* W_down, void* workspace, size_t ws_bytes,
+                          uint16_t* dx, uint16_t* dW_gu, uint16_t* dW_down, void* stream);
+
+/* A packed matrix of 4-bit weights.  Its values are
+ *     w[n][k] = s[n][k / group] * (q[n][k] - z[n][k / group])
+ * with q in 0..15, a bf16 scale and a zero point per row and group; the last
+ * group of a row is short when K is no multiple of the group. */
+typedef struct moe_lora_w4 {
+  const void* data;  /* device, as moe_lora_w4_pack wrote it, 16-byte aligned       */
+  int32_t N, K;      /* outputs; inputs, a multiple of 8 (each up to 2^24)          */
+  int32_t group;     /* 32, 64 or 128                                               */
+  int32_t has_zeros; /* 1: a zero point per row and group; 0: 8 everywhere          */
+} moe_lora_w4;
+
+/* Bytes of the packed form of w (data is not read), 0 when w is invalid. */
+size_t moe_lora_w4_bytes(const moe_lora_w4* w);
+
+/* Lays a 4-bit matrix out for the calls below, once, when it is loaded (w:
+ * its sizes; data is not read).
+ *   q       device [N][K/2] uint8, the weight of the even k in the low half
+ *   scales  device [N][ceil(K/group)] bf16
+ *   zeros   device [N][ceil(K/group)] uint8, 0..15 (larger ones count as 15);
+ *           NULL exactly when has_zeros is 0
+ *   packed  device, 16-byte aligned, packed_bytes >= moe_lora_w4_bytes(w) */
+int moe_lora_w4_pack(const moe_lora_w4* w, const uint8_t* q, const uint16_t* scales, const uint8_t* zeros,
+                     void* packed, size_t packed_bytes, void* stream);
+
+/* y = x w^T for M rows (0..65536), made for the few rows of a decode batch.
+ *   x  device [M][K] bf16, 16-byte aligned      y  device [M][N] bf16, overwritten
+ * The weights enter as integers and the scales in fp32, so y differs from
+ * the exact product by its own rounding and that of fp32 sums.  A row of x
+ * with an infinity or NaN gives a row of y that is not finite.  The same
+ * inputs give the same bits. */
+int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, uint16_t* y, void* stream);
+
+/* The gated block on 4-bit weights: h = act(x gate^T) * (x up^T), y = h
+ * down^T, h rounded to bf16.  gate and up are [I][H] alike in group and zero
+ * points, down is [H][I]; I is a multiple of 8 as well.
+ *   x, y  device [M][H] bf16   workspace  device, 16-byte aligned */
+size_t moe_lora_w4_ffn_workspace_bytes(int32_t M, int32_t I);
+int moe_lora_w4_ffn_forward(const moe_lora_w4* gate, const moe_lora_w4* up, const moe_lora_w4* down, int32_t M,
+                            int32_t act, const uint16_t* x, void* workspace, size_t ws_bytes, uint16_t* y,
+                            void* stream);
+
+/* Element types of gradients. */
+#define MOE_LORA_F32 0
+#define MOE_LORA_BF16 1
+#define MOE_LORA_F16 2
+
+/* One gradient tensor, numel elements in a row (numel may be 0). */
+typedef struct moe_lora_grad {
+  const void* g;  /* device, aligned to its element                                */
+  void* out;      /* device: the clipped gradient; may be g itself (in place)      */
+  int64_t numel;
+  int32_t dtype;  /* MOE_LORA_F32, MOE_LORA_BF16 or MOE_LORA_F16: of g and of out  */
+} moe_lora_grad;
+
+/* Bytes of workspace for n tensors (0 when n is negative).  Host only. */
+size_t moe_lora_clip_workspace_bytes(int32_t n);
+
+/* Clips n gradients by their global norm:
+ *     norm = sqrt(sum over all tensors of sum g^2)
+ *     out  = g * min(1, max_norm / (norm + 1e-6))
+ *   grads     host array of n entries, read before the call returns; no two
+ *             outputs overlap, nor an output another tensor's gradient
+ *   max_norm  >= 0; infinity leaves the gradients as they are (in place:
+ *             only the norm is computed)
+ *   norm      device [1] fp32, written
+ * Sums are fp64 in a fixed order: the same gradients give the same bits.  A
+ * gradient that is not finite shows in norm and, by the formula, in out: an
+ * infinite norm makes finite gradients 0, NaN makes all of them NaN. */
+int moe_lora_clip_grads(const moe_lora_grad* grads, int32_t n, float max_norm, float* norm, void* workspace,
+                        size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,6 +20,11 @@ MOE_LORA_EALIGN = -2
 MOE_LORA_EWORKSPACE = -3
 MOE_LORA_EUNSUPPORTED = -4
 MOE_LORA_EHIP = -5
+MOE_LORA_ACT_SILU = 0
+MOE_LORA_ACT_GELU = 1
+MOE_LORA_F32 = 0
+MOE_LORA_BF16 = 1
+MOE_LORA_F16 = 2
 MOE_LORA_NOALLOC_WORKSPACE_BYTES = 64 << 20  # the static workspace of moe_lora_forward_noalloc
 
 _lib = None
@@ -64,6 +69,20 @@ class moe_lora_align_ptrs(ctypes.Structure):
 class moe_lora_tune_entry(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("rows_per_expert", "H", "I", "E", "r", "L", "block_m")
                 + KNOBS]
+
+
+class moe_lora_ffn_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "I", "act")]
+
+
+class moe_lora_w4(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p)] + [(n, ctypes.c_int32) for n in (
+        "N", "K", "group", "has_zeros")]
+
+
+class moe_lora_grad(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
 
 
 # An entry's tuned configuration applies to shapes within this distance of
@@ -173,6 +192,22 @@ def load_library(path: str = LIB_PATH):
     lib.moe_lora_profiler_read.restype = i32
     lib.moe_lora_profiler_destroy.argtypes = [vp]
     lib.moe_lora_profiler_destroy.restype = None
+    fp, wp = ctypes.POINTER(moe_lora_ffn_shape), ctypes.POINTER(moe_lora_w4)
+    sz, c32 = ctypes.c_size_t, ctypes.c_int32
+    for name, restype, argtypes in (
+            ("moe_lora_ffn_workspace_bytes", sz, [fp, i32]),
+            ("moe_lora_ffn_forward", i32, [fp] + [vp] * 5 + [sz, vp, vp]),
+            ("moe_lora_ffn_backward", i32, [fp] + [vp] * 6 + [sz] + [vp] * 4),
+            ("moe_lora_w4_bytes", sz, [wp]),
+            ("moe_lora_w4_pack", i32, [wp, vp, vp, vp, vp, sz, vp]),
+            ("moe_lora_w4_matmul", i32, [wp, c32, vp, vp, vp]),
+            ("moe_lora_w4_ffn_workspace_bytes", sz, [c32, c32]),
+            ("moe_lora_w4_ffn_forward", i32, [wp, wp, wp, c32, c32, vp, vp, sz, vp, vp]),
+            ("moe_lora_clip_workspace_bytes", sz, [c32]),
+            ("moe_lora_clip_grads", i32,
+             [ctypes.POINTER(moe_lora_grad), c32, ctypes.c_float, vp, vp, sz, vp])):
+        f = getattr(lib, name)
+        f.restype, f.argtypes = restype, argtypes
     _lib = lib
     return lib
 
@@ -460,6 +495,261 @@ def fused_moe_lora(x, topk_ids, topk_weights, lora_ids, W_gu, W_down, A_gu, B_gu
     return y
 
 
+# ------------------------------------------------------------------ dense blocks
+
+_ACTS = {"silu": MOE_LORA_ACT_SILU, "gelu": MOE_LORA_ACT_GELU}
+_GRAD_TYPES = {"torch.float32": MOE_LORA_F32, "torch.bfloat16": MOE_LORA_BF16,
+               "torch.float16": MOE_LORA_F16}
+
+
+def _act_code(act) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act: {act!r}, expected one of {sorted(_ACTS)}")
+    return _ACTS[act]
+
+
+def _check_tensors(specs) -> None:
+    """Raise ValueError unless each (name, tensor, shape, dtype) matches, is
+    contiguous, and all tensors lie on the current HIP device.  A shape of
+    None is not compared."""
+    import torch
+    for name, t, shape, dtype in specs:
+        if t is None:
+            raise ValueError(f"{name} is required")
+        if str(t.dtype) != "torch." + dtype:
+            raise ValueError(f"{name}: dtype {str(t.dtype)[6:]}, expected {dtype}")
+        if shape is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    for name, t, _, _ in specs:
+        if not t.is_cuda:
+            raise ValueError(f"operands must be device tensors ({name} is on {t.device})")
+    dev = torch.cuda.current_device() if specs else None
+    for name, t, _, _ in specs:
+        if t.device.index != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _used_on(stream, *tensors) -> None:
+    """Tensors allocated here for the current stream and used on ``stream``:
+    their memory is not handed out again before that stream has passed them."""
+    if stream is not None:
+        import torch
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream))
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _check_workspace(workspace, need: int, what: str):
+    if str(workspace.dtype) != "torch.uint8" or workspace.dim() != 1:
+        raise ValueError(f"workspace must be a 1-D uint8 tensor ({what})")
+    if workspace.numel() < need:
+        raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} are needed")
+    return ("workspace", workspace, None, "uint8")
+
+
+def make_ffn_shape(T, H, I, act="silu") -> moe_lora_ffn_shape:
+    """Sizes of a gated feed-forward block; act: "silu" or "gelu" (tanh form)."""
+    return moe_lora_ffn_shape(int(T), int(H), int(I), _act_code(act))
+
+
+def moe_lora_ffn_workspace_bytes(shape: moe_lora_ffn_shape, backward: bool = True) -> int:
+    return int(load_library().moe_lora_ffn_workspace_bytes(ctypes.byref(shape), int(bool(backward))))
+
+
+def alloc_ffn_workspace(shape: moe_lora_ffn_shape, backward: bool = True, device="cuda"):
+    """Workspace of moe_lora_ffn_forward and (backward) moe_lora_ffn_backward."""
+    import torch
+    n = moe_lora_ffn_workspace_bytes(shape, backward)
+    if n == 0:
+        raise MoeLoraError("moe_lora_ffn_workspace_bytes", MOE_LORA_EINVAL)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_lora_ffn_forward(shape, x, W_gu, W_down, workspace, y, gu=None, stream=None) -> None:
+    """y = (act(x Wg^T) * (x Wu^T)) W_down^T; with gu ([T, 2I] fp32) the
+    pre-activations are kept there for moe_lora_ffn_backward."""
+    T, H, I = shape.T, shape.H, shape.I
+    specs = [("x", x, (T, H), "bfloat16"), ("W_gu", W_gu, (2 * I, H), "bfloat16"),
+             ("W_down", W_down, (H, I), "bfloat16"), ("y", y, (T, H), "bfloat16"),
+             _check_workspace(workspace, moe_lora_ffn_workspace_bytes(shape, False),
+                              "alloc_ffn_workspace")]
+    if gu is not None:
+        specs.append(("gu", gu, (T, 2 * I), "float32"))
+    _check_tensors(specs)
+    _check("moe_lora_ffn_forward", load_library().moe_lora_ffn_forward(
+        ctypes.byref(shape), x.data_ptr(), W_gu.data_ptr(), W_down.data_ptr(),
+        None if gu is None else gu.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        y.data_ptr(), _stream(stream)))
+
+
+def moe_lora_ffn_backward(shape, dy, x, gu, W_gu, W_down, workspace, dx=None, dW_gu=None,
+                          dW_down=None, stream=None) -> None:
+    """Gradients of the block from dy and the kept gu into those of dx, dW_gu
+    and dW_down that are given (overwritten)."""
+    T, H, I = shape.T, shape.H, shape.I
+    specs = [("dy", dy, (T, H), "bfloat16"), ("x", x, (T, H), "bfloat16"),
+             ("gu", gu, (T, 2 * I), "float32"), ("W_gu", W_gu, (2 * I, H), "bfloat16"),
+             ("W_down", W_down, (H, I), "bfloat16"),
+             _check_workspace(workspace, moe_lora_ffn_workspace_bytes(shape, True),
+                              "alloc_ffn_workspace")]
+    outs = (("dx", dx, (T, H)), ("dW_gu", dW_gu, (2 * I, H)), ("dW_down", dW_down, (H, I)))
+    specs += [(n, t, s, "bfloat16") for n, t, s in outs if t is not None]
+    _check_tensors(specs)
+    _check("moe_lora_ffn_backward", load_library().moe_lora_ffn_backward(
+        ctypes.byref(shape), dy.data_ptr(), x.data_ptr(), gu.data_ptr(), W_gu.data_ptr(),
+        W_down.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        *[None if t is None else t.data_ptr() for _, t, _ in outs], _stream(stream)))
+
+
+def gated_ffn(x, W_gu, W_down, act="silu", workspace=None, y=None, stream=None):
+    """The block's forward on the current stream; returns y [T, H] (bf16).
+    x [T,H], W_gu [2I,H], W_down [H,I], all bf16."""
+    import torch
+    for name, t in (("x", x), ("W_gu", W_gu)):
+        if t.dim() != 2:
+            raise ValueError(f"{name}: {t.dim()} dimensions, expected 2")
+    shape = make_ffn_shape(x.shape[0], x.shape[1], W_gu.shape[0] // 2, act)
+    if workspace is None:
+        workspace = alloc_ffn_workspace(shape, False, x.device)
+        _used_on(stream, workspace)
+    if y is None:
+        y = torch.empty_like(x)
+        _used_on(stream, y)
+    moe_lora_ffn_forward(shape, x, W_gu, W_down, workspace, y, stream=stream)
+    return y
+
+
+class W4Weight:
+    """A packed 4-bit matrix [N, K] (moe_lora_w4_pack): its sizes and its
+    device buffer."""
+
+    def __init__(self, N, K, group, has_zeros):
+        self.desc = moe_lora_w4(None, int(N), int(K), int(group), int(has_zeros))
+        self.packed = None
+
+    N = property(lambda self: self.desc.N)
+    K = property(lambda self: self.desc.K)
+    group = property(lambda self: self.desc.group)
+    has_zeros = property(lambda self: bool(self.desc.has_zeros))
+
+    def _spec(self, name):
+        return (name, self.packed, None, "uint8")
+
+
+def moe_lora_w4_bytes(w: W4Weight) -> int:
+    return int(load_library().moe_lora_w4_bytes(ctypes.byref(w.desc)))
+
+
+def moe_lora_w4_pack(q, scales, zeros=None, group=128, stream=None) -> W4Weight:
+    """Lays out 4-bit weights q [N, K/2] uint8 (even k in the low half) with
+    scales [N, ceil(K/group)] bf16 and zero points [N, ceil(K/group)] uint8
+    (0..15; None: 8 everywhere) for moe_lora_w4_matmul; done once per matrix."""
+    import torch
+    if q.dim() != 2:
+        raise ValueError(f"q: {q.dim()} dimensions, expected 2")
+    N, K = q.shape[0], 2 * q.shape[1]
+    w = W4Weight(N, K, group, zeros is not None)
+    n = moe_lora_w4_bytes(w)
+    if n == 0:
+        raise MoeLoraError("moe_lora_w4_bytes", MOE_LORA_EALIGN if K % 8 else MOE_LORA_EINVAL)
+    G = (K + group - 1) // group
+    specs = [("q", q, (N, K // 2), "uint8"), ("scales", scales, (N, G), "bfloat16")]
+    if zeros is not None:
+        specs.append(("zeros", zeros, (N, G), "uint8"))
+    _check_tensors(specs)
+    w.packed = torch.empty(n, dtype=torch.uint8, device=q.device)
+    _used_on(stream, w.packed)
+    w.desc.data = w.packed.data_ptr()
+    _check("moe_lora_w4_pack", load_library().moe_lora_w4_pack(
+        ctypes.byref(w.desc), q.data_ptr(), scales.data_ptr(),
+        None if zeros is None else zeros.data_ptr(), w.packed.data_ptr(), n, _stream(stream)))
+    return w
+
+
+def moe_lora_w4_matmul(x, w: W4Weight, y, stream=None) -> None:
+    """y [M, N] = x [M, K] w^T (bf16 rows, packed 4-bit weights)."""
+    M = x.shape[0] if x.dim() == 2 else -1
+    _check_tensors([("x", x, (M, w.K), "bfloat16"), ("y", y, (M, w.N), "bfloat16"), w._spec("w")])
+    _check("moe_lora_w4_matmul", load_library().moe_lora_w4_matmul(
+        ctypes.byref(w.desc), M, x.data_ptr(), y.data_ptr(), _stream(stream)))
+
+
+def moe_lora_w4_ffn_workspace_bytes(M, I) -> int:
+    return int(load_library().moe_lora_w4_ffn_workspace_bytes(int(M), int(I)))
+
+
+def alloc_w4_ffn_workspace(M, I, device="cuda"):
+    import torch
+    n = moe_lora_w4_ffn_workspace_bytes(M, I)
+    if n == 0:
+        raise MoeLoraError("moe_lora_w4_ffn_workspace_bytes", MOE_LORA_EINVAL)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_lora_w4_ffn_forward(x, gate: W4Weight, up: W4Weight, down: W4Weight, workspace, y,
+                            act="silu", stream=None) -> None:
+    """y = (act(x gate^T) * (x up^T)) down^T on packed 4-bit weights."""
+    M = x.shape[0] if x.dim() == 2 else -1
+    _check_tensors([("x", x, (M, gate.K), "bfloat16"), ("y", y, (M, down.N), "bfloat16"),
+                    gate._spec("gate"), up._spec("up"), down._spec("down"),
+                    _check_workspace(workspace, moe_lora_w4_ffn_workspace_bytes(M, gate.N),
+                                     "alloc_w4_ffn_workspace")])
+    _check("moe_lora_w4_ffn_forward", load_library().moe_lora_w4_ffn_forward(
+        ctypes.byref(gate.desc), ctypes.byref(up.desc), ctypes.byref(down.desc), M, _act_code(act),
+        x.data_ptr(), workspace.data_ptr(), workspace.numel(), y.data_ptr(), _stream(stream)))
+
+
+class GradSet:
+    """The gradients of one training program for moe_lora_clip_grads: checked
+    and listed once, kept as long as the program uses these tensors.  out:
+    where the clipped gradients go (like ``grads``); None: in place."""
+
+    def __init__(self, grads, out=None):
+        import torch
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if len(self.out) != len(self.grads):
+            raise ValueError(f"out holds {len(self.out)} tensors, grads {len(self.grads)}")
+        n = len(self.grads)
+        self._arr = (moe_lora_grad * max(1, n))()
+        specs = []
+        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            if str(g.dtype) not in _GRAD_TYPES:
+                raise ValueError(f"grads[{i}]: dtype {str(g.dtype)[6:]}, expected float32, bfloat16 or "
+                                 "float16")
+            dtype, shape = str(g.dtype)[6:], tuple(g.shape)
+            specs += [(f"grads[{i}]", g, shape, dtype), (f"out[{i}]", o, shape, dtype)]
+            self._arr[i] = moe_lora_grad(g.data_ptr(), o.data_ptr(), g.numel(), _GRAD_TYPES[str(g.dtype)])
+        _check_tensors(specs)
+        need = moe_lora_clip_workspace_bytes(n)
+        device = self.grads[0].device if n else "cuda"
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
+
+    def __len__(self):
+        return len(self.grads)
+
+
+def moe_lora_clip_workspace_bytes(n: int) -> int:
+    return int(load_library().moe_lora_clip_workspace_bytes(int(n)))
+
+
+def moe_lora_clip_grads(grads, max_norm: float, norm, stream=None) -> None:
+    """Scales the gradients (a GradSet, or a list of tensors, in place) by
+    min(1, max_norm / (norm + 1e-6)) and writes their global norm to ``norm``
+    ([1] fp32, device).  max_norm = inf: the norm only."""
+    if not isinstance(grads, GradSet):
+        grads = GradSet(grads)
+        _used_on(stream, grads.workspace)
+    _check_tensors([("norm", norm, (1,), "float32"), ("workspace", grads.workspace, None, "uint8")])
+    _check("moe_lora_clip_grads", load_library().moe_lora_clip_grads(
+        grads._arr, len(grads), float(max_norm), norm.data_ptr(), grads.workspace.data_ptr(),
+        grads.workspace.numel(), _stream(stream)))
+
+
 __all__ = [n for n in dir() if n.startswith("moe_lora") or n in (
     "make_shape", "alloc_workspace", "workspace_tensors", "fused_moe_lora", "load_library",
-    "MoeLoraError", "Profiler", "check_operands", "layer_operand_specs")]
+    "make_ffn_shape", "alloc_ffn_workspace", "gated_ffn",
+    "W4Weight", "alloc_w4_ffn_workspace", "GradSet", "MoeLoraError", "Profiler", "check_operands", "layer_operand_specs")]

@@ -1,0 +1,37 @@
+// Internal declarations of the gated feed-forward block (ffn.hip,
+// ffn_gemm.hip).  Not part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "moe_lora.h"
+
+namespace moelora {
+
+// The products of the block.  Each is C[m][n] = sum_k A(m, k) B(n, k) with
+// bf16 operands that lie either with k contiguous (A[m*lda + k]) or with the
+// output index contiguous (A[k*lda + m]), and an epilogue on the fp32 sums.
+enum FfnProduct {
+  FFN_GATE_UP,   // A = x, B = W_gu (gate and up rows interleaved): h = act(g) * u, gu kept on request
+  FFN_DOWN,      // A = h, B = W_down: y
+  FFN_DH,        // A = dy, B = W_down by its columns: dg, du and h from dh and the kept gu
+  FFN_DX,        // A = dgu, B = W_gu by its columns: dx
+  FFN_DW,        // A = dgu or dy, B = x or h, both by their columns (k = token): dW
+};
+
+struct FfnGemm {
+  const uint16_t* A;
+  const uint16_t* B;
+  int64_t lda, ldb;  // elements
+  int M, N, K;       // FFN_GATE_UP: N = I
+  uint16_t* out;     // bf16: h (GATE_UP), y, dgu (DH: [M][2N]), dx, dW
+  uint16_t* out2;    // DH: h
+  float* gu;         // GATE_UP: kept pre-activations [M][2N] or NULL; DH: read
+  int act;
+};
+
+int launch_ffn_gemm(const FfnGemm& g, FfnProduct product, hipStream_t st);
+
+}  // namespace moelora
