@@ -1,132 +1,417 @@
-// Products of the gated feed-forward block: bf16 MFMA, fp32 sums.
+// Products of the gated feed-forward block: LDS-tiled bf16 MFMA.
+//
+//   C[m][n] = sum_k A(m, k) B(n, k), fp32 sums, gate and its gradient in the
+// epilogue.  An operand lies either with k contiguous (x, h, dy, the weights
+// of a forward) or with its output index contiguous (the weights of dh and
+// dx, both sides of a weight gradient): the transposes that a backward pass
+// needs are never written out, they happen on the way from LDS to registers
+// (ds_read_b64_tr_b16).
+#include <type_traits>
+
 #include "device_util.h"
 #include "ffn.h"
+#include "internal.h"
 #include "gate_act.h"
 
 namespace moelora {
 
 namespace {
 
-// 128 x 128 outputs per workgroup of 2 x 2 wavefronts (64 x 64 each), K in
-// steps of 32 through LDS rows padded to 40 elements.
-constexpr int BM = 128, BN = 128, BK = 32, PAD = 40;
+typedef __attribute__((address_space(3))) char lds_char;
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 
-// Rows [r0, r0 + 128) x k [k0, k0 + 32) of an operand into LDS, k contiguous
-// there.  KC: k is contiguous in memory.  row(i): memory row of tile row i
-// (KC only).  What lies outside is zero.
-template <bool KC, class RowOf>
-__device__ __forceinline__ void stage(uint16_t* lds, const uint16_t* p, int64_t ld, int r0, int rows, int k0, int K,
-                                      RowOf row) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int c = (int)threadIdx.x + 256 * j;
-    if (KC) {
-      const int r = c >> 2, k = (c & 3) * 8;
-      const int64_t mr = row(r);
-      const u32x4_t v = mr >= 0 && k0 + k < K ? ld16(p + mr * ld + k0 + k) : zero4();
-      *reinterpret_cast<u32x4_t*>(lds + r * PAD + k) = v;
-    } else {
-      const int k = c >> 4, r = (c & 15) * 8;
-      const u32x4_t v = k0 + k < K && r0 + r < rows ? ld16(p + (int64_t)(k0 + k) * ld + r0 + r) : zero4();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) lds[(r + i) * PAD + k] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
-    }
+constexpr int BK = 64;  // K depth of a stage
+
+// 16 bytes per lane from the resource's base + soff + voff (zeros where voff
+// is past the resource's end) to LDS byte lds + IMM + 16 * lane.  In assembly,
+// without a register that a load in flight could write: through the builtin
+// the compiler takes every later LDS read for a read of this copy's target
+// and waits for the copy first.  Callers wait themselves.  Resource, offset
+// and m0 come from scalar arithmetic, which needs no wait states before a
+// vector memory operation, and one between m0 and a copy into LDS.
+template <int IMM>
+__device__ __forceinline__ void copy16(u32x4_t rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff), "n"(IMM)
+               : "memory", "scc");
+}
+
+__device__ __forceinline__ u32x4_t rsrc_of(const void* base, uint32_t bytes) {
+  const uint64_t b = (uint64_t)base;
+  return u32x4_t{(uint32_t)b, (uint32_t)(b >> 32), bytes, 0x00020000u};
+}
+
+template <int BM_, int BN_, int WM_, int WN_>
+struct FfnCfg {
+  static constexpr int BM = BM_, BN = BN_;            // tile
+  static constexpr int WM = WM_, WN = WN_;            // wavefronts along m and n
+  static constexpr int NW = WM * WN, NT = 64 * NW;
+  static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;  // 32 x 32 blocks of a wavefront
+  static constexpr int ABYTES = BM * BK * 2, BBYTES = BN * BK * 2, STAGE = ABYTES + BBYTES;
+  static constexpr int LDS = 2 * STAGE;
+  static constexpr int NCA = ABYTES / 1024 / NW, NCB = BBYTES / 1024 / NW;  // 1 KB copies per wavefront and stage
+};
+
+// f(0), f(1), .. with compile-time indices
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void for_each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>());
+    for_each<N, I + 1>(static_cast<F&&>(f));
   }
 }
 
-template <int PRODUCT>
-__global__ __launch_bounds__(256) void ffn_gemm_kernel(FfnGemm p) {
-  constexpr bool A_KC = PRODUCT != FFN_DW;
-  constexpr bool B_KC = PRODUCT == FFN_GATE_UP || PRODUCT == FFN_DOWN;
-  constexpr bool GATE = PRODUCT == FFN_GATE_UP;
-  __shared__ __attribute__((aligned(16))) uint16_t As[BM * PAD], Bs[BN * PAD];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave >> 1, wn = wave & 1, l16 = lane & 15, kq = lane >> 4;
-  const int m0 = blockIdx.y * BM;
-  const int n0 = blockIdx.x * (GATE ? BN / 2 : BN);
-  // gate_up: tile columns [64w, 64w + 64) are gate n0 + 32w + [0, 32), then
-  // the up columns of the same outputs
-  auto brow = [&](int c) -> int64_t {
-    if (GATE) {
-      const int n = n0 + (c >> 6) * 32 + (c & 31);
-      return n < p.N ? ((c >> 5) & 1 ? p.N + n : n) : -1;
-    }
-    return n0 + c < p.N ? n0 + c : -1;
-  };
-  auto arow = [&](int r) -> int64_t { return m0 + r < p.M ? m0 + r : -1; };
-  f32x4_t acc[4][4];
+__device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
+
+// One operand's side of a stage: ROWS x 64 (rows: the output index).
+//
+// KC, k contiguous: LDS row r holds 64 k (128 bytes) of output row r, its 16
+// byte pieces XOR-swizzled by (r / 2) % 8 so that the 32 rows of a fragment
+// read meet every bank equally.
+// Else: LDS row k holds ROWS outputs; its 64-byte quarters of every 256
+// bytes are XOR-swizzled by k % 4, the four k rows that a transposing read
+// takes side by side.
+// The swizzle is applied to the global address (a copy fills LDS in order).
+// Rows past the end get an offset past the buffer's and copy zeros.
+//
+// Stages count from the end of K: where K is no multiple of 64 the FIRST
+// stage begins before k = 0, and its lanes that lie there copy zeros; the
+// loop's copies are whole ones.
+template <bool KC, int ROWS, int NC, bool SPLIT>
+struct Operand {
+  const uint16_t* base;  // KC: row 0 of the tile at stage 0's first k; else stage 0's first k row, column 0
+  int64_t odd;           // SPLIT: elements from there to the rows of the odd 32-row blocks (gate_up's up rows)
+  int64_t ld;
+  uint32_t off[NC];
+  u32x4_t rs, rs2;       // the stage's resources, set by at()
+  uint32_t soff;
+
+  // p: the tile's first output at k = 0; rows_left: outputs from there on;
+  // kfirst: stage 0's first k, in (-64, 0]
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t odd_, int64_t ld_, int rows_left, int kfirst,
+                                       int wave) {
+    base = p + kfirst * (KC ? (int64_t)1 : ld_);
+    odd = odd_;
+    ld = ld_;
+    const int lane = lane_id();
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int k0 = 0; k0 < p.K; k0 += BK) {
-    __syncthreads();
-    stage<A_KC>(As, p.A, p.lda, m0, p.M, k0, p.K, arow);
-    stage<B_KC>(Bs, p.B, p.ldb, n0, p.N, k0, p.K, brow);
-    __syncthreads();
-    u32x4_t a[4], b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = *reinterpret_cast<const u32x4_t*>(As + (wm * 64 + i * 16 + l16) * PAD + kq * 8);
-      b[i] = *reinterpret_cast<const u32x4_t*>(Bs + (wn * 64 + i * 16 + l16) * PAD + kq * 8);
-    }
-    // B first: a lane ends with 4 neighbouring columns of one row
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = mfma_16x16x32(b[j], a[i], acc[i][j]);
-  }
-  auto pack4 = [](const float* v) {
-    uint2 o;
-    o.x = f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
-    o.y = f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16);
-    return o;
-  };
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m = m0 + wm * 64 + i * 16 + l16;
-    if (m >= p.M) continue;
-#pragma unroll
-    for (int j = 0; j < (GATE ? 2 : 4); ++j) {
-      const int n = GATE ? n0 + wn * 32 + j * 16 + kq * 4 : n0 + wn * 64 + j * 16 + kq * 4;
-      if (n >= p.N) continue;
-      float v[4], w[4], h[4];
-      if (GATE) {
-        const f32x4_t g = acc[i][j], u = acc[i][j + 2];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) h[q] = gate_act<false>(p.act, g[q], nullptr) * u[q];
-        *reinterpret_cast<uint2*>(p.out + (int64_t)m * p.N + n) = pack4(h);
-        if (p.gu) {
-          *reinterpret_cast<f32x4_t*>(p.gu + (int64_t)m * 2 * p.N + n) = g;
-          *reinterpret_cast<f32x4_t*>(p.gu + (int64_t)m * 2 * p.N + p.N + n) = u;
-        }
-      } else if (PRODUCT == FFN_DH) {
-        const f32x4_t g = *reinterpret_cast<const f32x4_t*>(p.gu + (int64_t)m * 2 * p.N + n);
-        const f32x4_t u = *reinterpret_cast<const f32x4_t*>(p.gu + (int64_t)m * 2 * p.N + p.N + n);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float da;
-          const float a = gate_act<true>(p.act, g[q], &da), dh = acc[i][j][q];
-          h[q] = a * u[q];
-          v[q] = dh * u[q] * da;
-          w[q] = dh * a;
-        }
-        *reinterpret_cast<uint2*>(p.out + (int64_t)m * 2 * p.N + n) = pack4(v);
-        *reinterpret_cast<uint2*>(p.out + (int64_t)m * 2 * p.N + p.N + n) = pack4(w);
-        *reinterpret_cast<uint2*>(p.out2 + (int64_t)m * p.N + n) = pack4(h);
+    for (int i = 0; i < NC; ++i) {
+      const int c = wave * NC + i;
+      if (KC) {
+        const int r = c * 8 + (lane >> 3);
+        const int ch = (lane & 7) ^ ((r >> 1) & 7);
+        // SPLIT: blocks of 32 alternate between the two row sets
+        const int mr = SPLIT ? (r >> 6) * 32 + (r & 31) : r;
+        off[i] = mr < rows_left ? (uint32_t)(mr * (int)ld + ch * 8) * 2u : kBufNone;
       } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = acc[i][j][q];
-        *reinterpret_cast<uint2*>(p.out + (int64_t)m * p.N + n) = pack4(v);
+        constexpr int PER = 1024 / (ROWS * 2), LPR = ROWS / 8;  // k rows per copy, lanes per row
+        const int k = c * PER + lane / LPR;
+        const int ch = (lane % LPR) ^ (4 * (k & 3));
+        off[i] = ch * 8 < rows_left ? (uint32_t)(k * (int)ld + ch * 8) * 2u : kBufNone;
       }
     }
   }
+
+  // makes stage s the one that copy() fills from; behind the last one (!real)
+  // copies bring zeros
+  __device__ __forceinline__ void at(int s, bool real) {
+    const uint32_t bytes = real ? 0x7fffffffu : 0u;
+    if (KC) {
+      rs = rsrc_of(base, bytes);
+      if (SPLIT) rs2 = rsrc_of(base + odd, bytes);
+      soff = (uint32_t)s * (BK * 2);
+    } else {
+      rs = rsrc_of(base + (int64_t)s * BK * ld, bytes);
+      soff = 0;
+    }
+  }
+
+  // copy I of the stage into the operand's part of a stage at LDS byte lds;
+  // FIRST: stage 0, whose k below 0 are zeros
+  template <int I, bool FIRST>
+  __device__ __forceinline__ void copy(uint32_t lds, int wave, int kfirst) const {
+    uint32_t o = off[I];
+    if (FIRST) {
+      const int lane = lane_id(), c = wave * NC + I;
+      int k;
+      if (KC) k = ((lane & 7) ^ (((c * 8 + (lane >> 3)) >> 1) & 7)) * 8;
+      else k = c * (1024 / (ROWS * 2)) + lane / (ROWS / 8);
+      if (kfirst + k < 0) o = kBufNone;
+    }
+    constexpr bool WIDE = NC >= 8;  // the row set alternates within a wavefront's copies, else with the wavefront
+    if (SPLIT && (WIDE ? ((I >> 2) & 1) : (wave & 1))) copy16<I * 1024>(rs2, lds + wave * (NC * 1024), o, soff);
+    else copy16<I * 1024>(rs, lds + wave * (NC * 1024), o, soff);
+  }
+
+  // fragment of 32 outputs from w0 + 32 * blk on, K slice kk of the stage:
+  // lane l holds output l % 32, k = 16 kk + 8 (l / 32) + 0..7
+  static __device__ __forceinline__ u32x4_t frag(const char* lds, int w0, int blk, int kk) {
+    const int lane = lane_id();
+    if (KC) {
+      const int r = lane & 31, ch = (2 * kk + (lane >> 5)) ^ ((r >> 1) & 7);
+      return *reinterpret_cast<const u32x4_t*>(lds + (w0 + blk * 32 + r) * 128 + ch * 16);
+    }
+    const int g = lane >> 4, s = (lane >> 2) & 3;
+    const int col = ((w0 + blk * 32 + (g & 1) * 16) * 2 + (lane & 3) * 8) ^ (64 * s);
+    const char* p = lds + (kk * 16 + 8 * (g >> 1) + s) * (ROWS * 2) + col;
+    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * ROWS * 2));
+    const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
+    return u32x4_t{a.x, a.y, b.x, b.y};
+  }
+};
+
+constexpr int wait_vm0 = (7 << 4) | (15 << 8);
+constexpr int wait_lgkm0 = 15 | (3 << 14) | (7 << 4);
+
+__device__ __forceinline__ void bare_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
+__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
+  u32x4_t o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = f32_to_bf16(v[2 * i]) | ((uint32_t)f32_to_bf16(v[2 * i + 1]) << 16);
+  *reinterpret_cast<u32x4_t*>(p) = o;
+}
+
+template <int PRODUCT, class C>
+__global__ __launch_bounds__(C::NT, 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
+                                                                                            int nrow) {
+  constexpr bool A_KC = PRODUCT != FFN_DW;
+  constexpr bool B_KC = PRODUCT == FFN_GATE_UP || PRODUCT == FFN_DOWN;
+  constexpr bool GATE = PRODUCT == FFN_GATE_UP;
+  constexpr int MI = C::MI, NI = C::NI;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+
+  // Workgroup i runs on XCD i % 8: each XCD takes a contiguous eighth of the
+  // tiles, in panels of 4 row tiles, column by column, so that the 32 tiles
+  // that an XCD works on at a time share 4 row and 8 column panels in its L2.
+  int t;
+  {
+    const int total = ncol * nrow, x = blockIdx.x & 7, j = blockIdx.x >> 3;
+    const int per = total >> 3, rest = total & 7;
+    t = x * per + min(x, rest) + j;
+  }
+  constexpr int GM = 4;
+  const int panel = t / (GM * ncol), in = t - panel * GM * ncol;
+  const int gm = min(GM, nrow - panel * GM);
+  const int tn = in / gm, tm = panel * GM + in - tn * gm;
+  const int m0 = tm * C::BM, n0 = tn * (GATE ? C::BN / 2 : C::BN);
+
+  Operand<A_KC, C::BM, C::NCA, false> A;
+  Operand<B_KC, C::BN, C::NCB, GATE> B;
+  const int nst = (p.K + BK - 1) / BK, kfirst = p.K - nst * BK;
+  A.init(A_KC ? p.A + (int64_t)m0 * p.lda : p.A + m0, 0, p.lda, p.M - m0, kfirst, wave);
+  B.init(B_KC ? p.B + (int64_t)n0 * p.ldb : p.B + n0, (int64_t)p.N * p.ldb, p.ldb, p.N - n0, kfirst, wave);
+
+  f32x16_t acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+
+  const uint32_t smem_at = (uint32_t)(uintptr_t)(lds_char*)smem;
+  u32x4_t af[2][MI], bf[2][NI];
+  auto read = [&](int slot, int kk, int set, int i) __attribute__((always_inline)) {  // fragment i of a slice
+    const char* at = smem + slot * C::STAGE;
+    // the first MFMAs' first: one of A, all of B, the rest of A
+    if (i == 0) af[set][0] = A.frag(at, wm * (C::BM / C::WM), 0, kk);
+    else if (i <= NI) bf[set][i - 1] = B.frag(at + C::ABYTES, wn * (C::BN / C::WN), i - 1, kk);
+    else af[set][i - NI] = A.frag(at, wm * (C::BM / C::WM), i - NI, kk);
+  };
+  constexpr int NM = MI * NI, NF = MI + NI, NC = C::NCA + C::NCB;
+  // MFMA n of a slice; the next slice's fragment reads go out between the
+  // first ones, so that they have landed when the slice ends, and after the
+  // stage's barrier the copies of the stage after next, one or two at a time
+  auto slice = [&](int set, int slot, int kk, auto issue_c) __attribute__((always_inline)) {
+    constexpr bool ISSUE = decltype(issue_c)::value;
+    for_each<NM>([&](auto n_c) __attribute__((always_inline)) {
+      constexpr int n = decltype(n_c)::value, i = n / NI, j = n % NI;
+      // B first: a lane ends with runs of 4 neighbouring columns of one row
+      acc[i][j] = mfma_32x32x16(bf[set][j], af[set][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (n < NF) read(slot, kk, set ^ 1, n);
+      if constexpr (ISSUE) {
+        for_each<(n + 1) * NC / NM - n * NC / NM>([&](auto q_c) __attribute__((always_inline)) {
+          constexpr int q = n * NC / NM + decltype(q_c)::value;
+          const uint32_t to = smem_at + (slot ^ 1) * C::STAGE;
+          if constexpr (q < C::NCA) A.template copy<q, false>(to, wave, 0);
+          else B.template copy<q - C::NCA, false>(to + C::ABYTES, wave, 0);
+        });
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  typedef std::integral_constant<bool, true> yes;
+  typedef std::integral_constant<bool, false> no;
+  // Every stage runs the same code: the copies behind the last stage bring
+  // zeros without touching memory, and the last reads take what is never
+  // used (or, where the number of stages is odd, zeros).
+  A.at(0, nst > 0);
+  B.at(0, nst > 0);
+  for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, true>(smem_at, wave, kfirst); });
+  for_each<C::NCB>([&](auto i) { B.template copy<decltype(i)::value, true>(smem_at + C::ABYTES, wave, kfirst); });
+  A.at(1, nst > 1);
+  B.at(1, nst > 1);
+  for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, false>(smem_at + C::STAGE, wave, 0); });
+  for_each<C::NCB>(
+      [&](auto i) { B.template copy<decltype(i)::value, false>(smem_at + C::STAGE + C::ABYTES, wave, 0); });
+  __builtin_amdgcn_s_waitcnt(wait_vm0);
+  bare_barrier();
+#pragma unroll
+  for (int i = 0; i < NF; ++i) read(0, 0, 0, i);
+  for (int s = 0; s < nst; s += 2) {
+    for_each<2>([&](auto h_c) __attribute__((always_inline)) {
+      constexpr int slot = decltype(h_c)::value;
+      slice(0, slot, 1, no());
+      slice(1, slot, 2, no());
+      A.at(s + slot + 2, s + slot + 2 < nst);
+      B.at(s + slot + 2, s + slot + 2 < nst);
+      slice(0, slot, 3, no());
+      // own copies of the next stage have landed, own reads of this one are done
+      __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);
+      bare_barrier();
+      slice(1, slot ^ 1, 0, yes());
+    });
+  }
+  __builtin_amdgcn_s_waitcnt(wait_vm0);  // no copy outlives the workgroup
+
+  // Epilogue, 32 rows of the wavefront at a time through its own part of the
+  // LDS (the ring is done with: every wavefront is past the last stage's
+  // barrier and reads, see above), so that memory sees whole lines: a lane
+  // takes 8 neighbouring outputs of one row, a row's lanes lie side by side.
+  // Straight from the accumulators a row's 16-byte pieces went to memory one
+  // by one: dh with its gate at T = 8192, H = 4096, I = 11008 took 1550 us
+  // that way and 1200 with this (four wavefronts, both).
+  constexpr int WC = C::BN / C::WN;          // the wavefront's tile columns
+  constexpr int ROWF = WC + 4;               // floats of a staged row (padded by 16 bytes against bank conflicts)
+  constexpr int OUT = GATE ? WC / 2 : WC;    // its outputs per row
+  constexpr int LPR = OUT / 8, RPI = 64 / LPR;  // lanes per row, rows per step
+  float* mine = reinterpret_cast<float*>(smem) + wave * 32 * ROWF;
+  static_assert(C::NW * 32 * ROWF * 4 <= C::LDS, "staged rows must fit the ring");
+  bare_barrier();
+  const int l32 = lane & 31, kh = lane >> 5;
+  const int oc = (lane % LPR) * 8;           // first of this lane's outputs in the wavefront's columns
+  const int n = n0 + wn * OUT + oc;
+  for_each<MI>([&](auto i_c) __attribute__((always_inline)) {
+    constexpr int i = decltype(i_c)::value;
+    const int mb = m0 + wm * (C::BM / C::WM) + i * 32 + lane / LPR;
+    f32x4_t kg[32 / RPI][2], ku[32 / RPI][2];
+    if (PRODUCT == FFN_DH) {
+#pragma unroll
+      for (int r = 0; r < 32 / RPI; ++r) {
+        const int m = mb + r * RPI;
+        if (m < p.M && n < p.N) {
+          const f32x4_t* src = reinterpret_cast<const f32x4_t*>(p.gu + (int64_t)m * 2 * p.N + n);
+          kg[r][0] = src[0];
+          kg[r][1] = src[1];
+          ku[r][0] = src[p.N / 4];
+          ku[r][1] = src[p.N / 4 + 1];
+        }
+      }
+    }
+    // element v of a 32 x 32 block: row l % 32, column 8 (v / 4) + 4 (l / 32) + v % 4
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4_t*>(mine + l32 * ROWF + j * 32 + 8 * q + 4 * kh) =
+            f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    asm volatile("" ::: "memory");  // a wavefront's LDS accesses run in order
+#pragma unroll
+    for (int r = 0; r < 32 / RPI; ++r) {
+      const int m = mb + r * RPI;
+      if (m >= p.M || n >= p.N) continue;
+      const float* row = mine + (r * RPI + lane / LPR) * ROWF;
+      float v[8], w[8], h[8];
+      if (GATE) {
+        // 32-column blocks alternate: gate, up
+        const f32x4_t* src = reinterpret_cast<const f32x4_t*>(row + (oc >> 5) * 64 + (oc & 31));
+        const f32x4_t g0 = src[0], g1 = src[1], u0 = src[8], u1 = src[9];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          h[q] = gate_act<false>(p.act, g0[q], nullptr) * u0[q];
+          h[q + 4] = gate_act<false>(p.act, g1[q], nullptr) * u1[q];
+        }
+        store8(p.out + (int64_t)m * p.N + n, h);
+        if (p.gu) {
+          f32x4_t* dst = reinterpret_cast<f32x4_t*>(p.gu + (int64_t)m * 2 * p.N + n);
+          __builtin_nontemporal_store(g0, dst);
+          __builtin_nontemporal_store(g1, dst + 1);
+          __builtin_nontemporal_store(u0, dst + p.N / 4);
+          __builtin_nontemporal_store(u1, dst + p.N / 4 + 1);
+        }
+      } else {
+        const f32x4_t* src = reinterpret_cast<const f32x4_t*>(row + oc);
+        const f32x4_t a0 = src[0], a1 = src[1];
+        if (PRODUCT == FFN_DH) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float g = kg[r][q >> 2][q & 3], u = ku[r][q >> 2][q & 3], dh = q < 4 ? a0[q & 3] : a1[q & 3];
+            float da;
+            const float a = gate_act<true>(p.act, g, &da);
+            h[q] = a * u;
+            v[q] = dh * u * da;
+            w[q] = dh * a;
+          }
+          store8(p.out + (int64_t)m * 2 * p.N + n, v);
+          store8(p.out + (int64_t)m * 2 * p.N + p.N + n, w);
+          store8(p.out2 + (int64_t)m * p.N + n, h);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v[q] = a0[q];
+            v[q + 4] = a1[q];
+          }
+          store8(p.out + (int64_t)m * p.N + n, v);
+        }
+      }
+    }
+    asm volatile("" ::: "memory");
+  });
+}
+
+template <int PRODUCT, class C>
+int launch_cfg(const FfnGemm& g, hipStream_t st) {
+  static std::atomic<uint64_t> attr_done;
+  constexpr int bn = PRODUCT == FFN_GATE_UP ? C::BN / 2 : C::BN;
+  const int64_t ncol = (g.N + bn - 1) / bn, nrow = (g.M + C::BM - 1) / C::BM;
+  if (ncol * nrow > 0x7fffffff) return MOE_LORA_EUNSUPPORTED;
+  const void* fn = reinterpret_cast<const void*>(&ffn_gemm_kernel<PRODUCT, C>);
+  const int rc = ensure_dynamic_lds(fn, C::LDS, attr_done);
+  if (rc) return rc;
+  ffn_gemm_kernel<PRODUCT, C><<<(unsigned)(ncol * nrow), C::NT, C::LDS, st>>>(g, (int)ncol, (int)nrow);
+  return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
+}
+
+// 256 x 256 tiles on 8 wavefronts of 128 x 64, one workgroup per CU (128 KB
+// of LDS).  T = 8192, H = 4096, I = 11008 (0.74 TFLOP, dx and the gate_up
+// pair 1.48), us: down 576, dx 1119, dW_down about 590, gate_up with its kept
+// gu 1200, dh with its gate 900, i.e. 1.25 to 1.32 PFLOP/s where the epilogue
+// is only a store.  What bounds them is power: at 71 % of the MFMA slots the
+// clock is 1.85 GHz of 2.4, and a copy of the loop that waits less reached
+// 87 % at 1.59 GHz and the same time within 4 %.  Four wavefronts of 128 x
+// 128 read less LDS but stall the only wavefront of a SIMD while it issues
+// its copies (dx 1250 us against 1177, alternating runs).
+typedef FfnCfg<256, 256, 2, 4> Big;
+// 128 x 128 tiles on 4 wavefronts, two workgroups per CU, where there are too
+// few large ones to fill the chip.
+typedef FfnCfg<128, 128, 2, 2> Small;
+
 template <int PRODUCT>
-void launch(const FfnGemm& g, hipStream_t st) {
-  const int bn = PRODUCT == FFN_GATE_UP ? BN / 2 : BN;
-  ffn_gemm_kernel<PRODUCT><<<dim3((g.N + bn - 1) / bn, (g.M + BM - 1) / BM), 256, 0, st>>>(g);
+int launch(const FfnGemm& g, hipStream_t st) {
+  if ((int64_t)g.M * g.N >= 256LL * 256 * 128) return launch_cfg<PRODUCT, Big>(g, st);
+  return launch_cfg<PRODUCT, Small>(g, st);
 }
 
 }  // namespace
@@ -134,13 +419,13 @@ void launch(const FfnGemm& g, hipStream_t st) {
 int launch_ffn_gemm(const FfnGemm& g, FfnProduct product, hipStream_t st) {
   if (g.M == 0 || g.N == 0) return MOE_LORA_OK;
   switch (product) {
-    case FFN_GATE_UP: launch<FFN_GATE_UP>(g, st); break;
-    case FFN_DOWN: launch<FFN_DOWN>(g, st); break;
-    case FFN_DH: launch<FFN_DH>(g, st); break;
-    case FFN_DX: launch<FFN_DX>(g, st); break;
-    case FFN_DW: launch<FFN_DW>(g, st); break;
+    case FFN_GATE_UP: return launch<FFN_GATE_UP>(g, st);
+    case FFN_DOWN: return launch<FFN_DOWN>(g, st);
+    case FFN_DH: return launch<FFN_DH>(g, st);
+    case FFN_DX: return launch<FFN_DX>(g, st);
+    case FFN_DW: return launch<FFN_DW>(g, st);
   }
-  return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
+  return MOE_LORA_EINVAL;
 }
 
 }  // namespace moelora

@@ -257,3 +257,22 @@ def test_one_call_form():
     import lora_moe_amd as lm
     x, W_gu, W_down, _ = (t.cuda() for t in ffn_inputs(20, 136, 72, 2))
     assert torch.equal(lm.gated_ffn(x, W_gu, W_down, act="gelu"), forward(lm, x, W_gu, W_down, "gelu")[2])
+
+
+# sizes at which each product takes the large tiles, ending inside them
+@pytest.mark.parametrize("T,H,I,act", [(2050, 2072, 4104, "silu"), (4200, 2056, 2008, "gelu")])
+def test_large_block(T, H, I, act):
+    """The same bounds with the 64-bit products formed on the GPU."""
+    import lora_moe_amd as lm
+    x, W_gu, W_down, dy = (t.cuda() for t in ffn_inputs(T, H, I, 17))
+    shape, ws, y, gu = forward(lm, x, W_gu, W_down, act, keep=True)
+    got = gradients(lm, shape, ws, dy, x, gu, W_gu, W_down)
+    d = [t.double() for t in (x, W_gu, W_down, dy)]
+    (gu64, _, y64), (e_gu, _, e_y) = ffn_bounds(*d[:3], act)
+    want = ffn_backward_bounds(d[3], d[0], gu.double(), d[1], d[2], act)
+    want["gu"], want["y"] = (gu64, e_gu), (y64, e_y)
+    got.update(gu=gu, y=y)
+    for n, (v, e) in want.items():
+        l2 = within(got[n], v.cpu(), e.cpu(), f"T={T} H={H} I={I} {n}")
+        if n != "gu":
+            check_l2(l2, v.numel(), T, n)
