@@ -32,6 +32,18 @@ struct FfnGemm {
   int act;
 };
 
+// Up to this many tokens a forward that keeps nothing streams the weights
+// (ffn_rows.hip); beyond it, its rows would be read more often than the
+// weights and the tiles take over.
+constexpr int kRowsMax = 64;
+// Up to this many, h goes from one product to the other as a bf16 pair hi +
+// lo, which costs nothing beside the weights.
+constexpr int kRowsPair = 16;
+
+// FFN_GATE_UP (g.gu unused) or FFN_DOWN of at most kRowsMax rows.  a_lo: the
+// remainder of A (at most kRowsPair rows), or NULL; out_lo: that of h, or NULL.
+int launch_ffn_rows(const FfnGemm& g, FfnProduct product, const uint16_t* a_lo, uint16_t* out_lo, hipStream_t st);
+
 int launch_ffn_gemm(const FfnGemm& g, FfnProduct product, hipStream_t st);
 
 }  // namespace moelora

@@ -11,9 +11,11 @@
 //   y += s * (sum x (128 + q) - (128 + z) * sum x)
 // once per group.  The cancelled part is at most ~30 times the result's size
 // (136 against a spread of 4.6), so fp32 keeps 18 bits and more of it.
+#include <type_traits>
+
 #include "abi_util.h"
 #include "device_util.h"
-#include "gate_act.h"
+#include "rows.h"
 #include "w4.h"
 
 namespace moelora {
@@ -58,86 +60,94 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(W4Layout L, const uint8_t*
   }
 }
 
-struct W4Args {
-  const uint16_t* x;  // [M][K]
-  const char* w[2];   // packed; w[1]: the up weights (gated)
-  W4Layout L;
-  uint16_t* out;      // [M][N]
-  int M, act;
-};
+// The stream's policy for packed weights (rows.h): a chunk of a tile is one
+// contiguous KB.  SPG: 32-deep steps per group.
+template <int SPG, bool ZEROS>
+struct PackedWeights {
+  struct Args {
+    const char* w[2];  // w[1]: the up weights (gate)
+    W4Layout L;
+  };
+  static constexpr int GPC = 4 / SPG;  // groups of a chunk
+  struct Tile {
+    const char* q;      // this lane's piece of chunk 0
+    const uint16_t* s;  // the scale and zero point of this lane's row, group 0
+    const uint8_t* z;
+  };
+  struct Buf {
+    u32x4_t q;
+    uint16_t s[GPC];
+    uint8_t z[GPC];
+  };
+  Args a;
+  int lane;
+  __device__ __forceinline__ PackedWeights(const Args& a_, const RowsArgs&, int lane_) : a(a_), lane(lane_) {}
+  __device__ __forceinline__ Tile tile(int t, int half) const {
+    const int64_t i = min(t, a.L.tiles - 1);
+    const char* w = a.w[half];
+    Tile r;
+    r.q = w + i * a.L.chunks * 1024 + lane * 16;
+    r.s = reinterpret_cast<const uint16_t*>(w + a.L.off_scales) + i * a.L.G * 16 + (lane & 15);
+    r.z = reinterpret_cast<const uint8_t*>(w + a.L.off_zeros) + i * a.L.G * 16 + (lane & 15);
+    return r;
+  }
+  __device__ __forceinline__ void load(Buf& b, const Tile& t, int c, bool masked) const {
+    b.q = ld16_stream(t.q + (int64_t)c * 1024);
+#pragma unroll
+    for (int g = 0; g < GPC; ++g) {
+      // a masked chunk's groups past the last one met zeros of x only
+      const int at = masked ? min(c * GPC + g, a.L.G - 1) : c * GPC + g;
+      b.s[g] = t.s[at * 16];
+      if (ZEROS) b.z[g] = t.z[at * 16];
+    }
+  }
+  // the weights of step j as bf16 128 + q
+  __device__ __forceinline__ u32x4_t operand(const Buf& b, int j) const {
+    u32x4_t v;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) v[h] = ((b.q[j] >> (4 * h)) & 0x000f000fu) | 0x43004300u;
+    return v;
+  }
 
-// One workgroup: 16 rows x 16 columns; its four wavefronts take every fourth
-// chunk of K and add up through LDS.
-template <bool GATED>
-__global__ __launch_bounds__(256) void w4_kernel(W4Args p) {
-  constexpr int NW = 4, NP = GATED ? 2 : 1;
-  __shared__ f32x4_t part[NW][NP][64];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l16 = lane & 15, kq = lane >> 4;
-  const int tile = blockIdx.x, m0 = blockIdx.y * 16;
-  const W4Layout& L = p.L;
-  const int mr = min(m0 + l16, p.M - 1);  // rows past M repeat the last one; their results are dropped
-  const uint16_t* xr = p.x + (int64_t)mr * L.K;
-  const u32x4_t ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-  f32x4_t tot[NP];
+  template <int RF, int CT>
+  struct Acc {
+    f32x4_t tot[RF][CT], a[RF][CT], xs[RF];
+    __device__ __forceinline__ void clear() {
+      const f32x4_t z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < NP; ++i) tot[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int spg = L.group / 32;  // MFMA steps per group
-  for (int c = wave; c < L.chunks; c += NW) {
-    u32x4_t q[NP];
+      for (int f = 0; f < RF; ++f) {
+        xs[f] = z;
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
-      q[i] = ld16_stream(p.w[i] + ((int64_t)tile * L.chunks + c) * 1024 + lane * 16);
-    f32x4_t acc[NP], xs = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < NP; ++i) acc[i] = xs;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = c * 128 + j * 32 + kq * 8;
-      const u32x4_t a = k < L.K ? ld16(xr + k) : zero4();
-      xs = mfma_16x16x32(a, ones, xs);
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        u32x4_t b;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) b[h] = ((q[i][j] >> (4 * h)) & 0x000f000fu) | 0x43004300u;
-        acc[i] = mfma_16x16x32(a, b, acc[i]);
+        for (int t = 0; t < CT; ++t) tot[f][t] = a[f][t] = z;
       }
-      if ((j + 1) % spg == 0) {  // the group ends (the last one of K may be short: the rest met zeros)
-        const int g = min((c * 128 + j * 32) / L.group, L.G - 1);
+    }
+    // the rows' sums, in every column
+    __device__ __forceinline__ void rows(int f, const u32x4_t& x) {
+      const u32x4_t ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+      xs[f] = mfma_16x16x32(x, ones, xs[f]);
+    }
+    __device__ __forceinline__ void mul(int f, int t, u32x4_t x, u32x4_t w) { a[f][t] = mfma_16x16x32(x, w, a[f][t]); }
+    __device__ __forceinline__ void step(const PackedWeights&, const Tile*, const Buf* b, int, int j) {
+      if ((j + 1) % SPG) return;
+      const int g = j / SPG;
+      const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const int64_t at = ((int64_t)tile * L.G + g) * 16 + l16;
-          const float s = bf16_to_f32(reinterpret_cast<const uint16_t*>(p.w[i] + L.off_scales)[at]);
-          const float z =
-              128.f + (L.has_zeros ? (float)reinterpret_cast<const uint8_t*>(p.w[i] + L.off_zeros)[at] : 8.f);
+      for (int t = 0; t < CT; ++t) {
+        const float s = bf16_to_f32(b[t].s[g]);
+        const float z = ZEROS ? 128.f + (float)b[t].z[g] : 136.f;
 #pragma unroll
-          for (int v = 0; v < 4; ++v) tot[i][v] += s * (acc[i][v] - z * xs[v]);
-          acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int f = 0; f < RF; ++f) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) tot[f][t][v] += s * (a[f][t][v] - z * xs[f][v]);
+          a[f][t] = zero;
         }
-        xs = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
+#pragma unroll
+      for (int f = 0; f < RF; ++f) xs[f] = zero;
     }
-  }
-#pragma unroll
-  for (int i = 0; i < NP; ++i) part[wave][i][lane] = tot[i];
-  __syncthreads();
-  if (wave) return;
-  const int n = tile * 16 + l16;
-#pragma unroll
-  for (int i = 0; i < NP; ++i)
-#pragma unroll
-    for (int w = 1; w < NW; ++w) tot[i] += part[w][i][lane];
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const int m = m0 + kq * 4 + v;
-    if (m < p.M && n < L.N) {
-      const float o = GATED ? gate_act<false>(p.act, tot[0][v], nullptr) * tot[NP - 1][v] : tot[0][v];
-      p.out[(int64_t)m * L.N + n] = f32_to_bf16(o);
-    }
-  }
-}
+    __device__ __forceinline__ f32x4_t sum(int f, int t) const { return tot[f][t]; }
+  };
+};
 
 int check_matrix(const moe_lora_w4* w, W4Layout* L) {
   if (!w || w->N <= 0 || w->K <= 0) return MOE_LORA_EINVAL;
@@ -158,12 +168,41 @@ int check_matrix(const moe_lora_w4* w, W4Layout* L) {
   return MOE_LORA_OK;
 }
 
-void launch_product(const W4Args& a, bool gated, hipStream_t st) {
-  const dim3 grid(a.L.tiles, (a.M + 15) / 16);
-  if (gated) w4_kernel<true><<<grid, 256, 0, st>>>(a);
-  else w4_kernel<false><<<grid, 256, 0, st>>>(a);
+template <class W>
+void launch_format(const RowsArgs& a, const typename W::Args& wa, bool gated, hipStream_t st) {
+  if (gated) {
+    if (a.M <= 16) launch_rows_cfg<W, 1, 2, true, false>(a, wa, st);
+    else if (a.M <= 32) launch_rows_cfg<W, 2, 2, true, false>(a, wa, st);
+    else launch_rows_cfg<W, 4, 2, true, false>(a, wa, st);
+  } else if (a.x_lo) {
+    launch_rows_cfg<W, 1, 1, false, true>(a, wa, st);
+  } else {
+    if (a.M <= 16) launch_rows_cfg<W, 1, 1, false, false>(a, wa, st);
+    else if (a.M <= 32) launch_rows_cfg<W, 2, 2, false, false>(a, wa, st);
+    else launch_rows_cfg<W, 4, 2, false, false>(a, wa, st);
+  }
 }
 
+// up: the second matrix of a gated product, or NULL
+void launch_product(const RowsArgs& a, const W4Layout& L, const void* w, const void* up, hipStream_t st) {
+  auto go = [&](auto spg, auto zeros) {
+    typedef PackedWeights<decltype(spg)::value, decltype(zeros)::value> W;
+    typename W::Args wa;
+    wa.w[0] = (const char*)w;
+    wa.w[1] = (const char*)up;
+    wa.L = L;
+    launch_format<W>(a, wa, up != nullptr, st);
+  };
+  auto with = [&](auto spg) {
+    if (L.has_zeros) go(spg, std::true_type());
+    else go(spg, std::false_type());
+  };
+  if (L.group == 32) with(std::integral_constant<int, 1>());
+  else if (L.group == 64) with(std::integral_constant<int, 2>());
+  else with(std::integral_constant<int, 4>());
+}
+
+constexpr int32_t kPairRows = 16;  // up to here h goes on as a bf16 pair, which costs nothing beside the weights
 constexpr int32_t kMaxRows = 1 << 16;
 
 }  // namespace
@@ -196,69 +235,55 @@ int moe_lora_w4_pack(const moe_lora_w4* w, const uint8_t* q, const uint16_t* sca
 }
 
 int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, uint16_t* y, void* stream) {
-  W4Args a = {};
-  const int rc = check_matrix(w, &a.L);
+  W4Layout L;
+  const int rc = check_matrix(w, &L);
   if (rc) return rc;
   if (M < 0) return MOE_LORA_EINVAL;
   if (M > kMaxRows) return MOE_LORA_EUNSUPPORTED;
   if (M == 0) return MOE_LORA_OK;
   if (!x || !y || !w->data) return MOE_LORA_EINVAL;
   if (!aligned16(x) || (uintptr_t)y % 2 || !aligned16(w->data)) return MOE_LORA_EALIGN;
-  const Range in[] = {{x, (size_t)M * a.L.K * 2}, {w->data, a.L.total}};
-  const Range out[] = {{y, (size_t)M * a.L.N * 2}};
+  const Range in[] = {{x, (size_t)M * L.K * 2}, {w->data, L.total}};
+  const Range out[] = {{y, (size_t)M * L.N * 2}};
   if (any_overlap(in, 2, out, 1)) return MOE_LORA_EINVAL;
-  a.x = x;
-  a.w[0] = (const char*)w->data;
-  a.out = y;
-  a.M = M;
-  launch_product(a, false, (hipStream_t)stream);
+  launch_product(RowsArgs{x, nullptr, y, nullptr, M, L.N, L.K, 0}, L, w->data, nullptr, (hipStream_t)stream);
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
 size_t moe_lora_w4_ffn_workspace_bytes(int32_t M, int32_t I) {
   if (M < 0 || I <= 0 || M > kMaxRows) return 0;
-  const size_t n = round256((size_t)M * I * 2);
+  const size_t n = round256((size_t)M * I * 2) * (M <= kPairRows ? 2 : 1);
   return n ? n : 256;
 }
 
 int moe_lora_w4_ffn_forward(const moe_lora_w4* gate, const moe_lora_w4* up, const moe_lora_w4* down, int32_t M,
                             int32_t act, const uint16_t* x, void* workspace, size_t ws_bytes, uint16_t* y,
                             void* stream) {
-  W4Args a = {};
-  W4Layout Lu, Ld;
+  W4Layout Lg, Lu, Ld;
   int rc;
-  if ((rc = check_matrix(gate, &a.L)) || (rc = check_matrix(up, &Lu)) || (rc = check_matrix(down, &Ld))) return rc;
+  if ((rc = check_matrix(gate, &Lg)) || (rc = check_matrix(up, &Lu)) || (rc = check_matrix(down, &Ld))) return rc;
   // the two halves of gate_up walk together
-  if (Lu.N != a.L.N || Lu.K != a.L.K || Lu.group != a.L.group || Lu.has_zeros != a.L.has_zeros ||
-      Ld.N != a.L.K || Ld.K != a.L.N || M < 0)
+  if (Lu.N != Lg.N || Lu.K != Lg.K || Lu.group != Lg.group || Lu.has_zeros != Lg.has_zeros || Ld.N != Lg.K ||
+      Ld.K != Lg.N || M < 0)
     return MOE_LORA_EINVAL;
   if (act != MOE_LORA_ACT_SILU && act != MOE_LORA_ACT_GELU) return MOE_LORA_EINVAL;
   if (M > kMaxRows) return MOE_LORA_EUNSUPPORTED;
   if (M == 0) return MOE_LORA_OK;
   if (!x || !y || !gate->data || !up->data || !down->data) return MOE_LORA_EINVAL;
-  const size_t h_bytes = (size_t)M * Ld.K * 2;
-  if (!workspace || ws_bytes < h_bytes) return MOE_LORA_EWORKSPACE;
+  const size_t need = moe_lora_w4_ffn_workspace_bytes(M, Ld.K);
+  if (!workspace || ws_bytes < need) return MOE_LORA_EWORKSPACE;
   if (!aligned16(x) || (uintptr_t)y % 2 || !aligned16(workspace) || !aligned16(gate->data) || !aligned16(up->data) ||
       !aligned16(down->data))
     return MOE_LORA_EALIGN;
   const Range in[] = {
-      {x, (size_t)M * a.L.K * 2}, {gate->data, a.L.total}, {up->data, Lu.total}, {down->data, Ld.total}};
-  const Range out[] = {{y, (size_t)M * Ld.N * 2}, {workspace, h_bytes}};
+      {x, (size_t)M * Lg.K * 2}, {gate->data, Lg.total}, {up->data, Lu.total}, {down->data, Ld.total}};
+  const Range out[] = {{y, (size_t)M * Ld.N * 2}, {workspace, need}};
   if (any_overlap(in, 4, out, 2)) return MOE_LORA_EINVAL;
   hipStream_t st = (hipStream_t)stream;
-  a.x = x;
-  a.w[0] = (const char*)gate->data;
-  a.w[1] = (const char*)up->data;
-  a.out = (uint16_t*)workspace;
-  a.M = M;
-  a.act = act;
-  launch_product(a, true, st);
-  a.x = (const uint16_t*)workspace;
-  a.w[0] = (const char*)down->data;
-  a.w[1] = nullptr;
-  a.L = Ld;
-  a.out = y;
-  launch_product(a, false, st);
+  uint16_t* h = (uint16_t*)workspace;
+  uint16_t* h_lo = M <= kPairRows ? (uint16_t*)((char*)workspace + round256((size_t)M * Ld.K * 2)) : nullptr;
+  launch_product(RowsArgs{x, nullptr, h, h_lo, M, Lg.N, Lg.K, act}, Lg, gate->data, up->data, st);
+  launch_product(RowsArgs{h, h_lo, y, nullptr, M, Ld.N, Ld.K, 0}, Ld, down->data, nullptr, st);
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
