@@ -380,7 +380,7 @@ int moe_lora_ffn_backward(const moe_lora_ffn_shape* shape, const uint16_t* dy, c
  * group of a row is short when K is no multiple of the group. */
 typedef struct moe_lora_w4 {
   const void* data;  /* device, as moe_lora_w4_pack wrote it, 16-byte aligned       */
-  int32_t N, K;      /* outputs; inputs, a multiple of 8 (each up to 2^24)          */
+  int32_t N, K;      /* outputs; inputs, a multiple of 8 (each up to 2^22)          */
   int32_t group;     /* 32, 64 or 128                                               */
   int32_t has_zeros; /* 1: a zero point per row and group; 0: 8 everywhere          */
 } moe_lora_w4;
@@ -399,12 +399,19 @@ int moe_lora_w4_pack(const moe_lora_w4* w, const uint8_t* q, const uint16_t* sca
                      void* packed, size_t packed_bytes, void* stream);
 
 /* y = x w^T for M rows (0..65536), made for the few rows of a decode batch.
- *   x  device [M][K] bf16, 16-byte aligned      y  device [M][N] bf16, overwritten
+ *   x          device [M][K] bf16, 16-byte aligned
+ *   y          device [M][N] bf16, overwritten
+ *   workspace  device, 16-byte aligned, ws_bytes >= moe_lora_w4_workspace_bytes(w, M)
  * The weights enter as integers and the scales in fp32, so y differs from
  * the exact product by its own rounding and that of fp32 sums.  A row of x
  * with an infinity or NaN gives a row of y that is not finite.  The same
  * inputs give the same bits. */
-int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, uint16_t* y, void* stream);
+int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, void* workspace, size_t ws_bytes,
+                       uint16_t* y, void* stream);
+
+/* Bytes of workspace that moe_lora_w4_matmul needs for M rows (0 when w or M
+ * is invalid).  Host only, pure. */
+size_t moe_lora_w4_workspace_bytes(const moe_lora_w4* w, int32_t M);
 
 /* The gated block on 4-bit weights: h = act(x gate^T) * (x up^T), y = h
  * down^T, h rounded to bf16.  gate and up are [I][H] alike in group and zero

@@ -200,7 +200,8 @@ def load_library(path: str = LIB_PATH):
             ("moe_lora_ffn_backward", i32, [fp] + [vp] * 6 + [sz] + [vp] * 4),
             ("moe_lora_w4_bytes", sz, [wp]),
             ("moe_lora_w4_pack", i32, [wp, vp, vp, vp, vp, sz, vp]),
-            ("moe_lora_w4_matmul", i32, [wp, c32, vp, vp, vp]),
+            ("moe_lora_w4_workspace_bytes", sz, [wp, c32]),
+            ("moe_lora_w4_matmul", i32, [wp, c32, vp, vp, sz, vp, vp]),
             ("moe_lora_w4_ffn_workspace_bytes", sz, [c32, c32]),
             ("moe_lora_w4_ffn_forward", i32, [wp, wp, wp, c32, c32, vp, vp, sz, vp, vp]),
             ("moe_lora_clip_workspace_bytes", sz, [c32]),
@@ -669,12 +670,26 @@ def moe_lora_w4_pack(q, scales, zeros=None, group=128, stream=None) -> W4Weight:
     return w
 
 
-def moe_lora_w4_matmul(x, w: W4Weight, y, stream=None) -> None:
-    """y [M, N] = x [M, K] w^T (bf16 rows, packed 4-bit weights)."""
+def moe_lora_w4_workspace_bytes(w: W4Weight, M: int) -> int:
+    return int(load_library().moe_lora_w4_workspace_bytes(ctypes.byref(w.desc), int(M)))
+
+
+def moe_lora_w4_matmul(x, w: W4Weight, y, workspace=None, stream=None) -> None:
+    """y [M, N] = x [M, K] w^T (bf16 rows, packed 4-bit weights).  workspace:
+    moe_lora_w4_workspace_bytes(w, M) bytes (uint8); None: allocated here."""
+    import torch
     M = x.shape[0] if x.dim() == 2 else -1
-    _check_tensors([("x", x, (M, w.K), "bfloat16"), ("y", y, (M, w.N), "bfloat16"), w._spec("w")])
+    specs = [("x", x, (M, w.K), "bfloat16"), ("y", y, (M, w.N), "bfloat16"), w._spec("w")]
+    need = moe_lora_w4_workspace_bytes(w, M)
+    if workspace is not None:
+        specs.append(_check_workspace(workspace, need, "moe_lora_w4_workspace_bytes"))
+    _check_tensors(specs)
+    if workspace is None and need > 256:  # 256: nothing is written
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        _used_on(stream, workspace)
     _check("moe_lora_w4_matmul", load_library().moe_lora_w4_matmul(
-        ctypes.byref(w.desc), M, x.data_ptr(), y.data_ptr(), _stream(stream)))
+        ctypes.byref(w.desc), M, x.data_ptr(), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel(), y.data_ptr(), _stream(stream)))
 
 
 def moe_lora_w4_ffn_workspace_bytes(M, I) -> int:

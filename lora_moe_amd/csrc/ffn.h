@@ -41,8 +41,11 @@ constexpr int kRowsMax = 64;
 constexpr int kRowsPair = 16;
 
 // FFN_GATE_UP (g.gu unused) or FFN_DOWN of at most kRowsMax rows.  a_lo: the
-// remainder of A (at most kRowsPair rows), or NULL; out_lo: that of h, or NULL.
-int launch_ffn_rows(const FfnGemm& g, FfnProduct product, const uint16_t* a_lo, uint16_t* out_lo, hipStream_t st);
+// remainder of A (at most kRowsPair rows), or NULL; out_lo: that of h, or
+// NULL; slabs: ffn_rows_slab_bytes of scratch.
+int launch_ffn_rows(const FfnGemm& g, FfnProduct product, const uint16_t* a_lo, uint16_t* out_lo, float* slabs,
+                    hipStream_t st);
+size_t ffn_rows_slab_bytes(int T, int H, int I);
 
 int launch_ffn_gemm(const FfnGemm& g, FfnProduct product, hipStream_t st);
 

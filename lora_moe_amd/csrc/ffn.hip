@@ -38,7 +38,8 @@ struct Sizes {  // bytes
 
 size_t ws_bytes_of(const moe_lora_ffn_shape& s, bool backward) {
   const Sizes z(s);
-  const size_t forward = round256(z.h) * (s.T <= kRowsPair ? 2 : 1);
+  size_t forward = round256(z.h) * (s.T <= kRowsPair ? 2 : 1);
+  if (s.T <= kRowsMax) forward += round256(ffn_rows_slab_bytes(s.T, s.H, s.I));
   return backward ? std::max(forward, round256(z.h) + round256(z.dgu)) : forward;
 }
 
@@ -77,10 +78,11 @@ int moe_lora_ffn_forward(const moe_lora_ffn_shape* shape, const uint16_t* x, con
   g.A = x, g.lda = H, g.B = W_gu, g.ldb = H, g.M = T, g.N = I, g.K = H, g.out = h, g.gu = gu;
   if (!gu && T <= kRowsMax) {
     uint16_t* h_lo = T <= kRowsPair ? (uint16_t*)((char*)workspace + round256(z.h)) : nullptr;
-    const int r = launch_ffn_rows(g, FFN_GATE_UP, nullptr, h_lo, st);
+    float* slabs = (float*)((char*)workspace + round256(z.h) * (h_lo ? 2 : 1));
+    const int r = launch_ffn_rows(g, FFN_GATE_UP, nullptr, h_lo, slabs, st);
     if (r) return r;
     g.A = h, g.lda = I, g.B = W_down, g.ldb = I, g.N = H, g.K = I, g.out = y;
-    return launch_ffn_rows(g, FFN_DOWN, h_lo, nullptr, st);
+    return launch_ffn_rows(g, FFN_DOWN, h_lo, nullptr, slabs, st);
   }
   const int r1 = launch_ffn_gemm(g, FFN_GATE_UP, st);
   if (r1) return r1;

@@ -1,182 +1,374 @@
 // Products of a few rows with a large weight matrix: the weight stream.
 //
-//   out[m][n] = sum_k x[m][k] w(n, k),  m < 16 RF,  or the gated pair
+//   out[m][n] = sum_k x[m][k] w(n, k),   or the gated pair
 //   out[m][n] = act(sum x w_gate) * sum x w_up
 //
 // Every weight is read once and meets all rows at once (MFMA 16 x 16 x 32,
-// rows on one side, 16 weight rows on the other), so the kernel is bound by
-// how many bytes of weights are in flight.  A workgroup owns CT tiles of 16
-// weight rows (gate: half of them gate rows, half the matching up rows) and
-// its wavefronts split K, each taking every KS-th chunk of 128 k: the more
-// wavefronts the fewer columns there are, up to 8 (the host picks KS), and
-// their sums meet once, through LDS, in a fixed order.  Two chunks' loads
-// are in flight per wavefront, in registers; the rows' fragments come from
-// the L2 with them (rows past M repeat the last one, their sums are dropped).
+// rows on one side, a tile of 16 weight rows on the other).  What bounds such
+// a kernel is the rate at which a CU has lines fetched to it, about 30 GB/s,
+// and the bytes in flight that sustain it; the rows' fragments come on top of
+// the weights, so the two kernels differ in how they get those:
 //
-// The weights' format is a policy W:
-//   Tile  what a lane keeps of a tile between chunks
-//   Buf   a chunk of a tile in registers
-//   load(buf, tile, chunk, masked), and per 32-deep step j either operand
-//   form, see the two policies (ffn_rows.hip, w4.hip)
+//   rows_direct_kernel, up to kRowsDirect rows: a workgroup owns one tile
+//     (gated: a gate tile and its up tile), its wavefronts split K, each
+//     taking every KS-th chunk of 128 k and fetching the rows' pieces itself.
+//   rows_shared_kernel: the 8 wavefronts of a workgroup own different tiles
+//     and walk K together, the rows' chunk comes once for all of them,
+//     through LDS.  Where that leaves too few workgroups K is split over
+//     the grid into fp32 slabs, which rows_join_kernel adds up.
+//
+// Loads are buffer loads, so that rows, k and chunks past the end are zeros
+// without traffic or branches: the loops are straight-line code in which each
+// wait names the loads it needs.
+//
+// The weights' format is a policy W (ffn_rows.hip, w4.hip): Tile, where a
+// tile lies; Buf, a chunk of it in registers; load(); operand(), the 32-deep
+// step j of a chunk as bf16; Acc, the sums.  W::DEPTH chunks are in flight.
 #pragma once
+
+#include <algorithm>
+#include <type_traits>
 
 #include "device_util.h"
 #include "gate_act.h"
+#include "moe_lora.h"
 
 namespace moelora {
+
+constexpr int kRowsDirect = 4;
+constexpr int kRowsJoinMax = 16;  // slabs at most
 
 struct RowsArgs {
   const uint16_t* x;     // [M][K]
   const uint16_t* x_lo;  // PAIR: the rows' remainders, the product takes x + x_lo
   uint16_t* out;         // [M][N]
-  uint16_t* out_lo;      // gate: the remainder of out's rounding, or NULL
+  uint16_t* out_lo;      // gated: the remainder of out's rounding, or NULL
   int M, N, K;
   int act;
+  float* slabs;          // K split over the grid: [split][M][N] (gated: [split][2][M][N]), or NULL
+  int splits;
 };
 
-template <class W, int RF, int CT, bool GATE, bool PAIR>
-__global__ __launch_bounds__(512, 2) void rows_kernel(RowsArgs p, typename W::Args wa) {
-  static_assert(!GATE || CT == 2, "one gate and one up tile");
-  constexpr int NX = PAIR ? 2 : 1;
+__device__ __forceinline__ void rows_store(const RowsArgs& p, bool gated, int m, int n, float a, float u) {
+  const float r = gated ? gate_act<false>(p.act, a, nullptr) * u : a;
+  const uint16_t hi = f32_to_bf16(r);
+  p.out[(int64_t)m * p.N + n] = hi;
+  if (gated && p.out_lo) p.out_lo[(int64_t)m * p.N + n] = f32_to_bf16(r - bf16_to_f32(hi));
+}
+
+__device__ __forceinline__ u32x4_t rows_load(const void* base, uint32_t bytes, uint32_t voff, uint32_t soff) {
+  return __builtin_bit_cast(u32x4_t,
+                            __builtin_amdgcn_raw_buffer_load_b128(make_rsrc(base, bytes), (int)voff, (int)soff, 0));
+}
+
+// n chunks through a ring of D register buffers that hold the first D of them:
+// mul(u) takes buffer u, load(u, i) brings chunk i into it.  Whole rounds,
+// then the rest without loads: one way through the loop, so that its waits
+// count the loads in flight exactly.
+template <int D, int U = 0, class M>
+__device__ __forceinline__ void rows_rest(int left, M&& mul) {
+  if constexpr (U < D) {
+    if (left > U) {
+      mul(std::integral_constant<int, U>());
+      rows_rest<D, U + 1>(left, static_cast<M&&>(mul));
+    }
+  }
+}
+template <int U, int D, class M, class F>
+__device__ __forceinline__ void rows_round(int i, M&& mul, F&& load) {
+  if constexpr (U < D) {
+    mul(std::integral_constant<int, U>());
+    load(std::integral_constant<int, U>(), i + U + D);
+    rows_round<U + 1, D>(i, static_cast<M&&>(mul), static_cast<F&&>(load));
+  }
+}
+template <int D, class M, class F>
+__device__ __forceinline__ void rows_ring(int n, M&& mul, F&& load) {
+  int i = 0;
+  for (; i + D <= n; i += D) rows_round<0, D>(i, mul, load);
+  rows_rest<D>(n - i, mul);
+}
+
+template <class W, bool GATE, bool PAIR>
+__global__ __launch_bounds__(512, 2) void rows_direct_kernel(RowsArgs p, typename W::Args wa) {
+  constexpr int CT = GATE ? 2 : 1, NX = PAIR ? 2 : 1, D = W::DEPTH * 2 / CT;
+  // a chunk of the rows (PAIR: then one of their remainders, which meet the
+  // weights as further rows), 16 bytes of padding per row against bank conflicts
+  constexpr int XROW = 256 + 16, XBYTES = kRowsDirect * XROW;
   extern __shared__ __attribute__((aligned(16))) char rows_smem[];
   const int lane = threadIdx.x & 63, ks = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, kq = lane >> 4;
-  const int m0 = blockIdx.y * (16 * RF);
-  const int tile0 = blockIdx.x * (GATE ? 1 : CT);  // first 16-column tile of the output
+  const int tile0 = blockIdx.x;
 
-  W w(wa, p, lane);
+  const W w(wa, p.N, p.K, lane);
   typename W::Tile tiles[CT];
 #pragma unroll
-  for (int t = 0; t < CT; ++t) tiles[t] = GATE ? w.tile(tile0, t) : w.tile(tile0 + t, 0);
-  const uint16_t* xr[RF];
-#pragma unroll
-  for (int f = 0; f < RF; ++f) xr[f] = p.x + (int64_t)min(m0 + f * 16 + l16, p.M - 1) * p.K + kq * 8;
-  const int64_t lo = PAIR ? p.x_lo - p.x : 0;
+  for (int t = 0; t < CT; ++t) tiles[t] = w.tile(tile0, t);
+  // lane l brings piece l % 16 of row l / 16 (rows past M: zeros) and reads
+  // the fragment of row l % 4 (PAIR: l % 8), further rows repeat them and their
+  // sums are dropped
+  const uint32_t xbytes = (uint32_t)p.M * (uint32_t)p.K * 2u;
+  const uint32_t xoff = ((uint32_t)kq * (uint32_t)p.K + (uint32_t)l16 * 8u) * 2u;
+  char* xl = rows_smem + wave * (NX * XBYTES);
 
-  struct Chunk {
-    typename W::Buf q[CT];
-    u32x4_t x[NX][RF][4];
-  } b0, b1;
-  auto load = [&](Chunk& b, int c, bool masked) __attribute__((always_inline)) {
+  typename W::Buf q[D][CT];
+  u32x4_t x[D][NX];
+  const int chunks = (p.K + 127) >> 7;
+  // workgroups start at different chunks: in step they would all ask for the
+  // same memory channels (rows lie a fixed distance apart)
+  const int rot = (int)((blockIdx.x * 5u) % (unsigned)chunks);
+  auto load = [&](int u, int i) __attribute__((always_inline)) {
+    const bool real = i < chunks;
+    const int c = i + rot < chunks ? i + rot : i + rot - chunks;
+    const uint32_t o = l16 * 8 < (real ? p.K - c * 128 : 0) ? xoff : kBufNone;
+    x[u][0] = rows_load(p.x, xbytes, o, (uint32_t)c * 256u);
+    if (PAIR) x[u][NX - 1] = rows_load(p.x_lo, xbytes, o, (uint32_t)c * 256u);
 #pragma unroll
-    for (int t = 0; t < CT; ++t) w.load(b.q[t], tiles[t], c, masked);
+    for (int t = 0; t < CT; ++t) w.load(q[u][t], tiles[t], c, real);
+    // loads return in order: kept in the order of their use
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  typename W::template Acc<1, CT> acc;
+  acc.clear();
+  const int n = wave < chunks ? (chunks - wave + ks - 1) / ks : 0;
 #pragma unroll
-    for (int f = 0; f < RF; ++f)
+  for (int u = 0; u < D; ++u) load(u, wave + u * ks);
+  auto mul = [&](auto u_c) __attribute__((always_inline)) {
+    constexpr int u = decltype(u_c)::value;
+    // (a wavefront's LDS accesses run in order)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = c * 128 + j * 32;
-        const bool ok = !masked || k + kq * 8 < p.K;
-        b.x[0][f][j] = ok ? ld16(xr[f] + k) : zero4();
-        if (PAIR) b.x[NX - 1][f][j] = ok ? ld16(xr[f] + lo + k) : zero4();
-      }
+    for (int v = 0; v < NX; ++v)
+      *reinterpret_cast<u32x4_t*>(xl + v * XBYTES + kq * XROW + l16 * 16) = x[u][v];
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const u32x4_t a =
+          *reinterpret_cast<const u32x4_t*>(xl + (l16 & (4 * NX - 1)) * XROW + j * 64 + kq * 16);
+      acc.begin(w, q[u], j);
+#pragma unroll
+      for (int t = 0; t < CT; ++t) acc.mul(0, t, a, w.operand(q[u][t], j));
+      acc.end(w, q[u], j);
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  rows_ring<D>(n, mul, [&](auto u_c, int i) __attribute__((always_inline)) {
+    load(decltype(u_c)::value, wave + i * ks);
+  });
+
+  __syncthreads();  // the rows' parts of the LDS become the sums'
+  // the wavefronts' sums, added in their order
+  f32x4_t* part = reinterpret_cast<f32x4_t*>(rows_smem);
+#pragma unroll
+  for (int t = 0; t < CT; ++t) part[(wave * CT + t) * 64 + lane] = acc.sum(0, t);
+  __syncthreads();
+  if (wave) return;
+  f32x4_t s[CT];
+#pragma unroll
+  for (int t = 0; t < CT; ++t) {
+    s[t] = part[t * 64 + lane];
+    for (int v = 1; v < ks; ++v) s[t] += part[(v * CT + t) * 64 + lane];
+    if (PAIR) {  // row m's remainder is row 4 + m, 16 lanes on
+#pragma unroll
+      for (int v = 0; v < 4; ++v) s[t][v] += __shfl_down(s[t][v], 16, 64);
+    }
+  }
+  const int no = tile0 * 16 + l16;
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (kq * 4 + v < p.M && no < p.N) rows_store(p, GATE, kq * 4 + v, no, s[0][v], s[CT - 1][v]);
+}
+
+// RF: fragments of 16 rows.  Grid: groups of 8 tiles, row tiles, K splits.
+template <class W, int RF, bool GATE, bool PAIR>
+__global__ __launch_bounds__(512, 2) void rows_shared_kernel(RowsArgs p, typename W::Args wa) {
+  constexpr int CT = GATE ? 2 : 1, NX = PAIR ? 2 : 1, D = std::min(W::DEPTH * 2 / CT, RF == 1 ? 8 : 4);
+  constexpr int PIECES = RF * 256 * NX;           // 16-byte pieces of a chunk of rows
+  constexpr int XPT = (PIECES + 511) / 512;       // per thread
+  __shared__ __attribute__((aligned(16))) u32x4_t xl[2][PIECES];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, kq = lane >> 4;
+  const int m0 = blockIdx.y * (16 * RF), rows = min(16 * RF, p.M - m0);
+  const int tile0 = blockIdx.x * 8 + wave;
+
+  const W w(wa, p.N, p.K, lane);
+  typename W::Tile tiles[CT];
+#pragma unroll
+  for (int t = 0; t < CT; ++t) tiles[t] = w.tile(tile0, t);
+
+  // this workgroup's chunks
+  const int chunks = (p.K + 127) >> 7, z = blockIdx.z;
+  const int c0 = (int)((int64_t)chunks * z / p.splits), c1 = (int)((int64_t)chunks * (z + 1) / p.splits);
+
+  // pieces: thread t brings piece t % 16 of rows t / 16, t / 16 + 32, ..
+  // (whole lines), into the order in which a fragment reads them
+  const uint32_t xbytes = (uint32_t)rows * (uint32_t)p.K * 2u;
+  const uint16_t* xbase[NX];
+  xbase[0] = p.x + (int64_t)m0 * p.K;
+  if (PAIR) xbase[NX - 1] = p.x_lo + (int64_t)m0 * p.K;
+  const int piece = tid & 15;
+  // workgroups start at different chunks, as above
+  const int n = c1 - c0, rot = n > 0 ? (int)((blockIdx.x * 5u) % (unsigned)n) : 0;
+  auto chunk = [&](int i) { return c0 + (i + rot < n ? i + rot : i + rot - n); };
+  u32x4_t xr[D][XPT];
+  auto load_x = [&](int u, int i) __attribute__((always_inline)) {
+    const int c = chunk(i);
+    const bool ok = i < n && c * 128 + piece * 8 < p.K;
+#pragma unroll
+    for (int e = 0; e < XPT; ++e) {
+      const int r = (tid >> 4) + e * 32;  // row of the NX * 16 RF stacked ones
+      const int rr = r & (16 * RF - 1);
+      const uint32_t o = ok && rr < rows && r < NX * 16 * RF
+                             ? ((uint32_t)rr * (uint32_t)p.K + (uint32_t)piece * 8u) * 2u
+                             : kBufNone;
+      // a wavefront's 4 rows are all of one half of the pair
+      xr[u][e] = rows_load(PAIR && __builtin_amdgcn_readfirstlane(r) >= 16 * RF ? xbase[NX - 1] : xbase[0], xbytes, o,
+                        (uint32_t)c * 256u);
+    }
+  };
+  auto put_x = [&](int b, int u) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < XPT; ++i) {
+      const int r = (tid >> 4) + i * 32;
+      if (PIECES >= 512 || r < NX * 16 * RF)
+        xl[b][((r >> 4) * 4 + (piece >> 2)) * 64 + (piece & 3) * 16 + (r & 15)] = xr[u][i];
+    }
+  };
+  typename W::Buf q[D][CT];
+  auto load_w = [&](int u, int i) __attribute__((always_inline)) {
+    const int c = chunk(i);
+#pragma unroll
+    for (int t = 0; t < CT; ++t) w.load(q[u][t], tiles[t], c, i < n);
   };
   typename W::template Acc<RF, CT> acc;
   acc.clear();
-  auto mul = [&](const Chunk& b, int c) __attribute__((always_inline)) {
+#pragma unroll
+  for (int u = 0; u < D; ++u) {
+    load_x(u, u);
+    load_w(u, u);
+    __builtin_amdgcn_sched_barrier(0);  // loads return in order: kept in the order of their use
+  }
+  auto mul = [&](auto u_c) __attribute__((always_inline)) {
+    constexpr int u = decltype(u_c)::value;
+    // the buffer written here was last read two chunks ago, before the
+    // previous barrier
+    put_x(u & 1, u);
+    lds_barrier();
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      u32x4_t a[NX][RF];
 #pragma unroll
       for (int v = 0; v < NX; ++v)
 #pragma unroll
-        for (int f = 0; f < RF; ++f) acc.rows(f, b.x[v][f][j]);
+        for (int f = 0; f < RF; ++f) a[v][f] = xl[u & 1][((v * RF + f) * 4 + j) * 64 + lane];
+      acc.begin(w, q[u], j);
 #pragma unroll
       for (int t = 0; t < CT; ++t) {
-        const u32x4_t bw = w.operand(b.q[t], j);
+        const u32x4_t bw = w.operand(q[u][t], j);
 #pragma unroll
         for (int v = 0; v < NX; ++v)
 #pragma unroll
-          for (int f = 0; f < RF; ++f) acc.mul(f, t, b.x[v][f][j], bw);
+          for (int f = 0; f < RF; ++f) acc.mul(f, t, a[v][f], bw);
       }
-      acc.step(w, tiles, b.q, c, j);
+      acc.end(w, q[u], j);
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
-  // this wavefront's whole chunks, two in flight; straight-line code, so that
-  // each wait names the loads it needs
-  const int full = p.K >> 7;
-  const int n = wave < full ? (full - wave + ks - 1) / ks : 0;
-  auto at = [&](int i) { return wave + i * ks; };
-  if (n >= 2) {
-    load(b0, at(0), false);
-    load(b1, at(1), false);
-    int i = 0;
-    for (; i + 4 <= n; i += 2) {
-      mul(b0, at(i));
-      load(b0, at(i + 2), false);
-      mul(b1, at(i + 1));
-      load(b1, at(i + 3), false);
-    }
-    mul(b0, at(i));
-    if (n - i == 3) {
-      load(b0, at(i + 2), false);
-      mul(b1, at(i + 1));
-      mul(b0, at(i + 2));
-    } else {
-      mul(b1, at(i + 1));
-    }
-  } else if (n == 1) {
-    load(b0, at(0), false);
-    mul(b0, at(0));
-  }
-  if ((p.K & 127) && full % ks == wave) {  // the rest of K, lanes past its end zero
-    load(b0, full, true);
-    mul(b0, full);
-  }
-
-  // the wavefronts' sums, added in their order
-  f32x4_t* part = reinterpret_cast<f32x4_t*>(rows_smem);
-  if (ks > 1) {
+  rows_ring<D>(n, mul, [&](auto u_c, int i) __attribute__((always_inline)) {
+    load_x(decltype(u_c)::value, i);
+    load_w(decltype(u_c)::value, i);
+    __builtin_amdgcn_sched_barrier(0);
+  });
+  const int no = tile0 * 16 + l16;
+  if (no >= p.N) return;
 #pragma unroll
-    for (int t = 0; t < CT; ++t)
-#pragma unroll
-      for (int f = 0; f < RF; ++f) part[((wave * CT + t) * RF + f) * 64 + lane] = acc.sum(f, t);
-    __syncthreads();
-  }
-  constexpr int OT = GATE ? 1 : CT;
-  for (int o = wave; o < OT * RF; o += ks) {
-    const int t = o / RF, f = o % RF;
-    f32x4_t s[GATE ? 2 : 1];
-    if (ks > 1) {
-#pragma unroll
-      for (int h = 0; h < (GATE ? 2 : 1); ++h) {
-        s[h] = part[((t + h) * RF + f) * 64 + lane];
-        for (int v = 1; v < ks; ++v) s[h] += part[((v * CT + t + h) * RF + f) * 64 + lane];
-      }
-    } else {
-#pragma unroll
-      for (int tt = 0; tt < CT; ++tt)
-#pragma unroll
-        for (int ff = 0; ff < RF; ++ff)
-          if (ff == f && (GATE || tt == t)) s[GATE ? tt : 0] = acc.sum(ff, tt);
-    }
-    const int n_out = (tile0 + t) * 16 + l16;
+  for (int f = 0; f < RF; ++f)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int m = m0 + f * 16 + kq * 4 + v;
-      if (m >= p.M || n_out >= p.N) continue;
-      const float r = GATE ? gate_act<false>(p.act, s[0][v], nullptr) * s[GATE ? 1 : 0][v] : s[0][v];
-      const uint16_t hi = f32_to_bf16(r);
-      p.out[(int64_t)m * p.N + n_out] = hi;
-      if (GATE && p.out_lo) p.out_lo[(int64_t)m * p.N + n_out] = f32_to_bf16(r - bf16_to_f32(hi));
+      if (m >= p.M) continue;
+      if (p.splits == 1) {
+        rows_store(p, GATE, m, no, acc.sum(f, 0)[v], acc.sum(f, CT - 1)[v]);
+      } else {
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+          p.slabs[((int64_t)(z * CT + t) * p.M + m) * p.N + no] = acc.sum(f, t)[v];
+      }
     }
-  }
 }
 
-// Wavefronts that split K: enough for about 2048 of them over the chip's 256
-// CUs (8 each, which have 64 KB of weights in flight), of at least two chunks
-// each.
+// Adds the slabs in their order.
+template <bool GATE>
+__global__ __launch_bounds__(256) void rows_join_kernel(RowsArgs p) {
+  constexpr int CT = GATE ? 2 : 1;
+  const int64_t size = (int64_t)p.M * p.N;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= size) return;
+  float s[CT];
+#pragma unroll
+  for (int t = 0; t < CT; ++t) s[t] = p.slabs[t * size + i];
+  for (int z = 1; z < p.splits; ++z)
+#pragma unroll
+    for (int t = 0; t < CT; ++t) s[t] += p.slabs[(z * CT + t) * size + i];
+  rows_store(p, GATE, (int)(i / p.N), (int)(i % p.N), s[0], s[CT - 1]);
+}
+
+inline int rows_fragments(int M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
+
+// K splits of the shared form: one workgroup per CU (256), of at least 4
+// chunks each.
+inline int rows_splits(int M, int N, int K) {
+  if (M <= kRowsDirect) return 1;
+  const int rt = 16 * rows_fragments(M);
+  const int64_t wgs = (int64_t)((N + 127) / 128) * ((M + rt - 1) / rt);
+  const int64_t s = std::min<int64_t>((256 + wgs / 2) / wgs, (K + 511) / 512);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(s, kRowsJoinMax));
+}
+
+// Bytes of slabs that a product needs.
+inline size_t rows_slab_bytes(int M, int N, int K, bool gated) {
+  const int s = rows_splits(M, N, K);
+  return s > 1 ? (size_t)s * (gated ? 2 : 1) * M * N * sizeof(float) : 0;
+}
+
+// The most that any product of M rows needs: K is split only while the split
+// groups number at most 256 + groups / 2 <= 341, each of 128 columns (gated:
+// pairs) and up to 16 RF rows.
+inline size_t rows_slab_bound(int M) {
+  return M <= kRowsDirect ? 0 : (size_t)341 * 128 * 16 * rows_fragments(M) * 2 * sizeof(float);
+}
+
+// Wavefronts that split K in the direct form: about 2048 of them over the
+// chip, at least two chunks each.
 inline int rows_ksplit(int64_t workgroups, int K) {
   int ks = 8;
   while (ks > 1 && (workgroups * ks > 3072 || K / 128 < 2 * ks)) ks >>= 1;
   return ks;
 }
 
-template <class W, int RF, int CT, bool GATE, bool PAIR>
-void launch_rows_cfg(const RowsArgs& a, const typename W::Args& wa, hipStream_t st) {
-  const int tiles = (a.N + 15) / 16, per = GATE ? 1 : CT;
-  const dim3 grid((tiles + per - 1) / per, (a.M + 16 * RF - 1) / (16 * RF));
-  const int ks = rows_ksplit((int64_t)grid.x * grid.y, a.K);
-  rows_kernel<W, RF, CT, GATE, PAIR><<<grid, 64 * ks, ks > 1 ? ks * CT * RF * 1024 : 0, st>>>(a, wa);
+template <class W, bool GATE, bool PAIR>
+void launch_rows(RowsArgs a, const typename W::Args& wa, hipStream_t st) {
+  const int tiles = (a.N + 15) / 16;
+  a.splits = rows_splits(a.M, a.N, a.K);
+  if (a.M <= kRowsDirect) {
+    const int ks = rows_ksplit(tiles, a.K);
+    constexpr int lds = std::max((GATE ? 2 : 1) * 1024, (PAIR ? 2 : 1) * kRowsDirect * (256 + 16));
+    rows_direct_kernel<W, GATE, PAIR><<<tiles, 64 * ks, ks * lds, st>>>(a, wa);
+    return;
+  }
+  const int rf = rows_fragments(a.M);
+  const dim3 grid((tiles + 7) / 8, (a.M + 16 * rf - 1) / (16 * rf), a.splits);
+  if (rf == 1) rows_shared_kernel<W, 1, GATE, PAIR><<<grid, 512, 0, st>>>(a, wa);
+  if constexpr (!PAIR) {
+    if (rf == 2) rows_shared_kernel<W, 2, GATE, false><<<grid, 512, 0, st>>>(a, wa);
+    if (rf == 4) rows_shared_kernel<W, 4, GATE, false><<<grid, 512, 0, st>>>(a, wa);
+  }
+  if (a.splits > 1) {
+    const int64_t n = (int64_t)a.M * a.N;
+    rows_join_kernel<GATE><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
+  }
 }
 
 }  // namespace moelora

@@ -5,12 +5,11 @@
 //
 // The weights meet the matrix cores as integers, so nothing of them is
 // rounded: a nibble q put into the low mantissa bits of bf16 128 is exactly
-// 128 + q (one AND and one OR for two weights), the MFMAs sum x (128 + q)
-// per group in fp32, a further MFMA against ones gives the group's sum of x
-// per row, and
-//   y += s * (sum x (128 + q) - (128 + z) * sum x)
-// once per group.  The cancelled part is at most ~30 times the result's size
-// (136 against a spread of 4.6), so fp32 keeps 18 bits and more of it.
+// 128 + q (one AND-OR for two weights), 128 + z is exact in bf16 as well, and
+// the MFMAs sum x (128 + q) and -x (128 + z) into the same fp32 accumulator,
+// once per 32-deep step each.  A group's sum, sum x (q - z), is then scaled
+// and added to the row's.  What cancels is at most ~30 times the result's
+// size (136 against a spread of 4.6), so fp32 keeps 18 bits and more of it.
 #include <type_traits>
 
 #include "abi_util.h"
@@ -26,14 +25,16 @@ namespace {
 // chunks of 1 KB, 16 bytes for each lane of a wavefront: lane l holds row
 // l % 16, and in word j the weights k = 128c + 32j + 8 (l / 16) + 0..7, even
 // ones in the low half (k 2i at bits 4i) and odd ones in the high half (k
-// 2i + 1 at bits 16 + 4i).  Then the scales [tile][group][16] bf16 and the
-// zero points [tile][group][16] uint8 where the matrix has them.  Rows past N
-// have scale 0, weights past K meet zeros of x.
+// 2i + 1 at bits 16 + 4i).  Then the scales [tile][chunk][16][groups of a
+// chunk] bf16 and, where the matrix has them, the zero points in the same
+// order, uint8: a lane has a chunk's in one load.  Rows past N and groups
+// past the last have scale 0, weights past K meet zeros of x.
 __global__ __launch_bounds__(256) void w4_pack_kernel(W4Layout L, const uint8_t* __restrict__ q,
                                                       const uint16_t* __restrict__ scales,
                                                       const uint8_t* __restrict__ zeros, char* __restrict__ packed) {
   const int64_t words = (int64_t)L.tiles * L.chunks * 256;
-  const int64_t groups = (int64_t)L.tiles * L.G * 16;
+  const int gpc = 128 / L.group;
+  const int64_t groups = (int64_t)L.tiles * L.chunks * 16 * gpc;
   const int64_t step = (int64_t)gridDim.x * 256;
   uint32_t* w = reinterpret_cast<uint32_t*>(packed);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words; i += step) {
@@ -51,10 +52,12 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(W4Layout L, const uint8_t*
   uint16_t* s = reinterpret_cast<uint16_t*>(packed + L.off_scales);
   uint8_t* z = reinterpret_cast<uint8_t*>(packed + L.off_zeros);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < groups; i += step) {
-    const int64_t g = (i >> 4) % L.G, n = (i >> 4) / L.G * 16 + (i & 15);
-    s[i] = n < L.N ? scales[n * L.G + g] : (uint16_t)0;
+    const int64_t tc = i / (16 * gpc);  // tile, chunk
+    const int64_t g = tc % L.chunks * gpc + i % gpc, n = tc / L.chunks * 16 + i / gpc % 16;
+    const bool ok = n < L.N && g < L.G;
+    s[i] = ok ? scales[n * L.G + g] : (uint16_t)0;
     if (L.has_zeros) {
-      const uint8_t v = n < L.N ? zeros[n * L.G + g] : (uint8_t)0;
+      const uint8_t v = ok ? zeros[n * L.G + g] : (uint8_t)0;
       z[i] = v < 15 ? v : (uint8_t)15;
     }
   }
@@ -69,81 +72,103 @@ struct PackedWeights {
     W4Layout L;
   };
   static constexpr int GPC = 4 / SPG;  // groups of a chunk
-  struct Tile {
-    const char* q;      // this lane's piece of chunk 0
-    const uint16_t* s;  // the scale and zero point of this lane's row, group 0
-    const uint8_t* z;
+  static constexpr int DEPTH = SPG == 1 ? 2 : 4;
+  struct Tile {  // chunk 0 of the tile's weights, scales and zero points
+    const char* q;
+    const char* s;
+    const char* z;
   };
   struct Buf {
     u32x4_t q;
-    uint16_t s[GPC];
-    uint8_t z[GPC];
+    uint32_t s[2], z;  // the words with the chunk's scales and zero points of this lane's row
   };
-  Args a;
+  const Args& a;
   int lane;
-  __device__ __forceinline__ PackedWeights(const Args& a_, const RowsArgs&, int lane_) : a(a_), lane(lane_) {}
-  __device__ __forceinline__ Tile tile(int t, int half) const {
-    const int64_t i = min(t, a.L.tiles - 1);
-    const char* w = a.w[half];
-    Tile r;
-    r.q = w + i * a.L.chunks * 1024 + lane * 16;
-    r.s = reinterpret_cast<const uint16_t*>(w + a.L.off_scales) + i * a.L.G * 16 + (lane & 15);
-    r.z = reinterpret_cast<const uint8_t*>(w + a.L.off_zeros) + i * a.L.G * 16 + (lane & 15);
-    return r;
+  uint32_t mask = 0x000f000fu, magic = 0x43004300u;
+  __device__ __forceinline__ PackedWeights(const Args& a_, int, int, int lane_) : a(a_), lane(lane_) {
+    // in registers, so that AND and OR are one instruction
+    asm("" : "+s"(mask));
+    asm("" : "+v"(magic));
   }
-  __device__ __forceinline__ void load(Buf& b, const Tile& t, int c, bool masked) const {
-    b.q = ld16_stream(t.q + (int64_t)c * 1024);
-#pragma unroll
-    for (int g = 0; g < GPC; ++g) {
-      // a masked chunk's groups past the last one met zeros of x only
-      const int at = masked ? min(c * GPC + g, a.L.G - 1) : c * GPC + g;
-      b.s[g] = t.s[at * 16];
-      if (ZEROS) b.z[g] = t.z[at * 16];
+  // tiles past the last repeat it, their sums are dropped
+  __device__ __forceinline__ Tile tile(int t, int half) const {
+    const int64_t i = (int64_t)min(t, a.L.tiles - 1) * a.L.chunks;
+    const char* w = a.w[half];
+    return Tile{w + i * 1024, w + a.L.off_scales + i * (32 * GPC), w + a.L.off_zeros + i * (16 * GPC)};
+  }
+  __device__ __forceinline__ void load(Buf& b, const Tile& t, int c, bool real) const {
+    const uint32_t n = real ? (uint32_t)a.L.chunks : 0u;
+    const buf_rsrc_t q = make_rsrc(t.q, n * 1024u);
+    b.q = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(q, lane * 16, c * 1024, 2));
+    // whole words, of which a lane picks its part when it uses them
+    const buf_rsrc_t s = make_rsrc(t.s, n * (32u * GPC));
+    const int row = lane & 15, sc = c * (32 * GPC);
+    if (GPC == 4) {
+      const uint2 v = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(s, row * 8, sc, 0));
+      b.s[0] = v.x;
+      b.s[1] = v.y;
+    } else {
+      b.s[0] = __builtin_amdgcn_raw_buffer_load_b32(s, (row * GPC >> 1) * 4, sc, 0);
     }
+    if (ZEROS) b.z = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(t.z, n * (16u * GPC)), (row * GPC >> 2) * 4,
+                                                          c * (16 * GPC), 0);
+  }
+  __device__ __forceinline__ float scale(const Buf& b, int g) const {
+    uint32_t v = b.s[GPC == 4 ? g >> 1 : 0];
+    if (GPC == 1) v <<= lane & 1 ? 0 : 16;
+    return (GPC == 1 || g & 1) ? bf16_hi(v) : bf16_lo(v);
+  }
+  // -(128 + z) as bf16, twice
+  __device__ __forceinline__ uint32_t zero(const Buf& b, int g) const {
+    if (!ZEROS) return 0xc308c308u;
+    const int shift = 8 * ((lane * GPC & 3) + g);
+    const uint32_t z = (b.z >> shift) & 255u;
+    return 0xc300c300u + z * 0x00010001u;
   }
   // the weights of step j as bf16 128 + q
   __device__ __forceinline__ u32x4_t operand(const Buf& b, int j) const {
     u32x4_t v;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) v[h] = ((b.q[j] >> (4 * h)) & 0x000f000fu) | 0x43004300u;
+    for (int h = 0; h < 4; ++h) v[h] = ((b.q[j] >> (4 * h)) & mask) | magic;
     return v;
   }
 
   template <int RF, int CT>
   struct Acc {
-    f32x4_t tot[RF][CT], a[RF][CT], xs[RF];
+    f32x4_t tot[RF][CT], a[RF][CT];
+    u32x4_t z[CT];
     __device__ __forceinline__ void clear() {
-      const f32x4_t z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int f = 0; f < RF; ++f) {
-        xs[f] = z;
+      for (int f = 0; f < RF; ++f)
 #pragma unroll
-        for (int t = 0; t < CT; ++t) tot[f][t] = a[f][t] = z;
-      }
+        for (int t = 0; t < CT; ++t) tot[f][t] = a[f][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-    // the rows' sums, in every column
-    __device__ __forceinline__ void rows(int f, const u32x4_t& x) {
-      const u32x4_t ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-      xs[f] = mfma_16x16x32(x, ones, xs[f]);
-    }
-    __device__ __forceinline__ void mul(int f, int t, u32x4_t x, u32x4_t w) { a[f][t] = mfma_16x16x32(x, w, a[f][t]); }
-    __device__ __forceinline__ void step(const PackedWeights&, const Tile*, const Buf* b, int, int j) {
-      if ((j + 1) % SPG) return;
-      const int g = j / SPG;
-      const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    // before step j: the zero points of its group
+    __device__ __forceinline__ void begin(const PackedWeights& w, const Buf* b, int j) {
+      if (j % SPG) return;
 #pragma unroll
       for (int t = 0; t < CT; ++t) {
-        const float s = bf16_to_f32(b[t].s[g]);
-        const float z = ZEROS ? 128.f + (float)b[t].z[g] : 136.f;
+        const uint32_t v = w.zero(b[t], j / SPG);
+        z[t] = u32x4_t{v, v, v, v};
+      }
+    }
+    __device__ __forceinline__ void mul(int f, int t, u32x4_t x, u32x4_t w) {
+      a[f][t] = mfma_16x16x32(x, z[t], a[f][t]);
+      a[f][t] = mfma_16x16x32(x, w, a[f][t]);
+    }
+    // after step j: a group's sum is scaled where it ends
+    __device__ __forceinline__ void end(const PackedWeights& w, const Buf* b, int j) {
+      if ((j + 1) % SPG) return;
+#pragma unroll
+      for (int t = 0; t < CT; ++t) {
+        const float s = w.scale(b[t], j / SPG);
 #pragma unroll
         for (int f = 0; f < RF; ++f) {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) tot[f][t][v] += s * (a[f][t][v] - z * xs[f][v]);
-          a[f][t] = zero;
+          for (int v = 0; v < 4; ++v) tot[f][t][v] += s * a[f][t][v];
+          a[f][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
       }
-#pragma unroll
-      for (int f = 0; f < RF; ++f) xs[f] = zero;
     }
     __device__ __forceinline__ f32x4_t sum(int f, int t) const { return tot[f][t]; }
   };
@@ -154,7 +179,7 @@ int check_matrix(const moe_lora_w4* w, W4Layout* L) {
   if (w->group != 32 && w->group != 64 && w->group != 128) return MOE_LORA_EINVAL;
   if (w->has_zeros != 0 && w->has_zeros != 1) return MOE_LORA_EINVAL;
   if (w->K % 8) return MOE_LORA_EALIGN;
-  if (w->N > (1 << 24) || w->K > (1 << 24)) return MOE_LORA_EUNSUPPORTED;
+  if (w->N > (1 << 22) || w->K > (1 << 22)) return MOE_LORA_EUNSUPPORTED;
   L->N = w->N;
   L->K = w->K;
   L->group = w->group;
@@ -163,24 +188,10 @@ int check_matrix(const moe_lora_w4* w, W4Layout* L) {
   L->chunks = (w->K + 127) / 128;
   L->G = (w->K + w->group - 1) / w->group;
   L->off_scales = (size_t)L->tiles * L->chunks * 1024;
-  L->off_zeros = L->off_scales + round256((size_t)L->tiles * L->G * 32);
-  L->total = L->off_zeros + (w->has_zeros ? round256((size_t)L->tiles * L->G * 16) : 0);
+  const size_t groups = (size_t)L->tiles * L->chunks * 16 * (128 / w->group);
+  L->off_zeros = L->off_scales + round256(groups * 2);
+  L->total = L->off_zeros + (w->has_zeros ? round256(groups) : 0);
   return MOE_LORA_OK;
-}
-
-template <class W>
-void launch_format(const RowsArgs& a, const typename W::Args& wa, bool gated, hipStream_t st) {
-  if (gated) {
-    if (a.M <= 16) launch_rows_cfg<W, 1, 2, true, false>(a, wa, st);
-    else if (a.M <= 32) launch_rows_cfg<W, 2, 2, true, false>(a, wa, st);
-    else launch_rows_cfg<W, 4, 2, true, false>(a, wa, st);
-  } else if (a.x_lo) {
-    launch_rows_cfg<W, 1, 1, false, true>(a, wa, st);
-  } else {
-    if (a.M <= 16) launch_rows_cfg<W, 1, 1, false, false>(a, wa, st);
-    else if (a.M <= 32) launch_rows_cfg<W, 2, 2, false, false>(a, wa, st);
-    else launch_rows_cfg<W, 4, 2, false, false>(a, wa, st);
-  }
 }
 
 // up: the second matrix of a gated product, or NULL
@@ -191,7 +202,9 @@ void launch_product(const RowsArgs& a, const W4Layout& L, const void* w, const v
     wa.w[0] = (const char*)w;
     wa.w[1] = (const char*)up;
     wa.L = L;
-    launch_format<W>(a, wa, up != nullptr, st);
+    if (up) launch_rows<W, true, false>(a, wa, st);
+    else if (a.x_lo) launch_rows<W, false, true>(a, wa, st);
+    else launch_rows<W, false, false>(a, wa, st);
   };
   auto with = [&](auto spg) {
     if (L.has_zeros) go(spg, std::true_type());
@@ -234,7 +247,15 @@ int moe_lora_w4_pack(const moe_lora_w4* w, const uint8_t* q, const uint16_t* sca
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
-int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, uint16_t* y, void* stream) {
+size_t moe_lora_w4_workspace_bytes(const moe_lora_w4* w, int32_t M) {
+  W4Layout L;
+  if (check_matrix(w, &L) || M < 0 || M > kMaxRows) return 0;
+  const size_t n = M ? round256(rows_slab_bytes(M, L.N, L.K, false)) : 0;
+  return n ? n : 256;
+}
+
+int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, void* workspace, size_t ws_bytes,
+                       uint16_t* y, void* stream) {
   W4Layout L;
   const int rc = check_matrix(w, &L);
   if (rc) return rc;
@@ -242,18 +263,23 @@ int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, uint1
   if (M > kMaxRows) return MOE_LORA_EUNSUPPORTED;
   if (M == 0) return MOE_LORA_OK;
   if (!x || !y || !w->data) return MOE_LORA_EINVAL;
-  if (!aligned16(x) || (uintptr_t)y % 2 || !aligned16(w->data)) return MOE_LORA_EALIGN;
+  const size_t need = rows_slab_bytes(M, L.N, L.K, false);
+  if (need && (!workspace || ws_bytes < need)) return MOE_LORA_EWORKSPACE;
+  if (!aligned16(x) || (uintptr_t)y % 2 || !aligned16(w->data) || (need && !aligned16(workspace)))
+    return MOE_LORA_EALIGN;
   const Range in[] = {{x, (size_t)M * L.K * 2}, {w->data, L.total}};
-  const Range out[] = {{y, (size_t)M * L.N * 2}};
-  if (any_overlap(in, 2, out, 1)) return MOE_LORA_EINVAL;
-  launch_product(RowsArgs{x, nullptr, y, nullptr, M, L.N, L.K, 0}, L, w->data, nullptr, (hipStream_t)stream);
+  const Range out[] = {{y, (size_t)M * L.N * 2}, {workspace, need}};
+  if (any_overlap(in, 2, out, 2)) return MOE_LORA_EINVAL;
+  launch_product(RowsArgs{x, nullptr, y, nullptr, M, L.N, L.K, 0, (float*)workspace, 1}, L, w->data, nullptr, (hipStream_t)stream);
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
+// h (and its remainder), then the slabs of either product
+static size_t ffn_h_bytes(int32_t M, int32_t I) { return round256((size_t)M * I * 2) * (M <= kPairRows ? 2 : 1); }
+
 size_t moe_lora_w4_ffn_workspace_bytes(int32_t M, int32_t I) {
-  if (M < 0 || I <= 0 || M > kMaxRows) return 0;
-  const size_t n = round256((size_t)M * I * 2) * (M <= kPairRows ? 2 : 1);
-  return n ? n : 256;
+  if (M < 0 || I <= 0 || M > kMaxRows || I > (1 << 22)) return 0;
+  return M ? ffn_h_bytes(M, I) + rows_slab_bound(M) : 256;
 }
 
 int moe_lora_w4_ffn_forward(const moe_lora_w4* gate, const moe_lora_w4* up, const moe_lora_w4* down, int32_t M,
@@ -282,8 +308,9 @@ int moe_lora_w4_ffn_forward(const moe_lora_w4* gate, const moe_lora_w4* up, cons
   hipStream_t st = (hipStream_t)stream;
   uint16_t* h = (uint16_t*)workspace;
   uint16_t* h_lo = M <= kPairRows ? (uint16_t*)((char*)workspace + round256((size_t)M * Ld.K * 2)) : nullptr;
-  launch_product(RowsArgs{x, nullptr, h, h_lo, M, Lg.N, Lg.K, act}, Lg, gate->data, up->data, st);
-  launch_product(RowsArgs{h, h_lo, y, nullptr, M, Ld.N, Ld.K, 0}, Ld, down->data, nullptr, st);
+  float* slabs = (float*)((char*)workspace + ffn_h_bytes(M, Ld.K));
+  launch_product(RowsArgs{x, nullptr, h, h_lo, M, Lg.N, Lg.K, act, slabs, 1}, Lg, gate->data, up->data, st);
+  launch_product(RowsArgs{h, h_lo, y, nullptr, M, Ld.N, Ld.K, 0, slabs, 1}, Ld, down->data, nullptr, st);
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 

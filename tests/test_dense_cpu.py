@@ -121,22 +121,31 @@ def w4_bytes(lib, d):
 
 def test_w4_matrices(lib):
     for d, code in ((w4(N=0), EINVAL), (w4(K=-8), EINVAL), (w4(group=16), EINVAL), (w4(group=0), EINVAL),
-                    (w4(zeros=2), EINVAL), (w4(K=60), EALIGN), (w4(N=(1 << 24) + 1), EUNSUP),
-                    (w4(K=(1 << 24) + 8), EUNSUP)):
+                    (w4(zeros=2), EINVAL), (w4(K=60), EALIGN), (w4(N=(1 << 22) + 1), EUNSUP),
+                    (w4(K=(1 << 22) + 8), EUNSUP)):
         assert w4_bytes(lib, d) == 0
-        assert lib.moe_lora_w4_matmul(ctypes.byref(d), 1, at(1), at(2), None) == code
+        assert lib.moe_lora_w4_matmul(ctypes.byref(d), 1, at(1), None, 0, at(2), None) == code
         z = at(4) if d.has_zeros else None
         assert lib.moe_lora_w4_pack(ctypes.byref(d), at(1), at(2), z, at(3), 1 << 40, None) == code
     # at least the weights, the scales and the zero points of whole tiles
     assert w4_bytes(lib, w4(17, 136, 32)) >= 32 * 256 // 2 + 32 * 5 * 2
     assert w4_bytes(lib, w4(17, 136, 32, 1)) >= w4_bytes(lib, w4(17, 136, 32)) + 32 * 5
-    assert lib.moe_lora_w4_matmul(None, 1, at(1), at(2), None) == EINVAL
+    assert lib.moe_lora_w4_matmul(None, 1, at(1), None, 0, at(2), None) == EINVAL
 
 
 def test_w4_arguments(lib):
     d, dz = w4(), w4(zeros=1)
     n = w4_bytes(lib, d)
-    mm = lambda M=2, x=at(1), y=at(2), d=d: lib.moe_lora_w4_matmul(ctypes.byref(d), M, x, y, None)  # noqa: E731
+    mm = lambda M=2, x=at(1), y=at(2), d=d, ws=at(9), n=1 << 30: lib.moe_lora_w4_matmul(  # noqa: E731
+        ctypes.byref(d), M, x, ws, n, y, None)
+    big = w4(128, 4096, 32)  # rows enough to split K
+    need = lib.moe_lora_w4_workspace_bytes(ctypes.byref(big), 32)
+    assert need > 256
+    assert mm(M=32, d=big, n=need - 256) == EWS and mm(M=32, d=big, ws=None) == EWS
+    assert mm(M=32, d=big, ws=at(9, 8)) == EALIGN and mm(M=32, d=big, ws=at(1)) == EINVAL
+    assert mm(M=32, d=big, ws=at(2)) == EINVAL
+    assert lib.moe_lora_w4_workspace_bytes(ctypes.byref(w4(K=60)), 1) == 0
+    assert lib.moe_lora_w4_workspace_bytes(ctypes.byref(d), -1) == 0
     assert mm(M=-1) == EINVAL and mm(M=65537) == EUNSUP and mm(M=0, x=None, y=None) == lm.MOE_LORA_OK
     assert mm(x=None) == EINVAL and mm(y=None) == EINVAL and mm(d=w4(data=None)) == EINVAL
     assert mm(x=at(1, 8)) == EALIGN and mm(y=at(2, 1)) == EALIGN and mm(d=w4(data=at(0, 8))) == EALIGN
@@ -151,7 +160,7 @@ def test_w4_arguments(lib):
 
 def test_w4_block_arguments(lib):
     g, u, d = w4(64, 32, data=at(0)), w4(64, 32, data=at(1)), w4(32, 64, data=at(2))
-    def call(g=g, u=u, d=d, M=2, act=0, x=at(3), ws=at(4), n=1 << 20, y=at(5)):
+    def call(g=g, u=u, d=d, M=2, act=0, x=at(3), ws=at(4), n=1 << 26, y=at(5)):
         return lib.moe_lora_w4_ffn_forward(*(None if t is None else ctypes.byref(t) for t in (g, u, d)), M, act, x,
                                            ws, n, y, None)
     assert call(M=0, x=None, y=None, ws=None) == lm.MOE_LORA_OK
