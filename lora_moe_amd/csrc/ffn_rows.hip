@@ -13,6 +13,7 @@ struct Bf16Weights {
     const uint16_t* w;  // gate: [2N][K], gate rows then up rows
   };
   static constexpr int DEPTH = 2;
+  static constexpr int LINES = 32;  // of 128 bytes, per chunk of a tile
   struct Tile {
     const uint16_t* base;
     uint32_t bytes;
@@ -61,7 +62,7 @@ struct Bf16Weights {
 
 int launch_ffn_rows(const FfnGemm& g, FfnProduct product, const uint16_t* a_lo, uint16_t* out_lo, float* slabs,
                     hipStream_t st) {
-  const RowsArgs a{g.A, a_lo, g.out, out_lo, g.M, g.N, g.K, g.act, slabs, 1};
+  const RowsArgs a{g.A, a_lo, g.out, out_lo, g.M, g.N, g.K, g.act, slabs, 1, 0};
   const Bf16Weights::Args wa{g.B};
   if (product == FFN_GATE_UP) launch_rows<Bf16Weights, true, false>(a, wa, st);
   else if (a_lo) launch_rows<Bf16Weights, false, true>(a, wa, st);
@@ -70,7 +71,9 @@ int launch_ffn_rows(const FfnGemm& g, FfnProduct product, const uint16_t* a_lo, 
 }
 
 size_t ffn_rows_slab_bytes(int T, int H, int I) {
-  return std::max(rows_slab_bytes(T, I, H, true), rows_slab_bytes(T, H, I, false));
+  const int lines = Bf16Weights::LINES;
+  return std::max(rows_slab_bytes(rows_plan(T, I, H, lines), T, I, true),
+                  rows_slab_bytes(rows_plan(T, H, I, lines), T, H, false));
 }
 
 }  // namespace moelora

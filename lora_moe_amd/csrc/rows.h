@@ -9,10 +9,10 @@
 // and the bytes in flight that sustain it; the rows' fragments come on top of
 // the weights, so the two kernels differ in how they get those:
 //
-//   rows_direct_kernel, up to kRowsDirect rows: a workgroup owns one tile
-//     (gated: a gate tile and its up tile), its wavefronts split K, each
-//     taking every KS-th chunk of 128 k and fetching the rows' pieces itself.
-//   rows_shared_kernel: the 8 wavefronts of a workgroup own different tiles
+//   rows_direct_kernel, up to 8 rows: a workgroup owns one tile (gated: a
+//     gate tile and its up tile), its wavefronts split K, each taking every
+//     KS-th chunk of 128 k and fetching the rows' pieces itself.
+//   rows_shared_kernel: up to 8 wavefronts of a workgroup own different tiles
 //     and walk K together, the rows' chunk comes once for all of them,
 //     through LDS.  Where that leaves too few workgroups K is split over
 //     the grid into fp32 slabs, which rows_join_kernel adds up.
@@ -35,7 +35,6 @@
 
 namespace moelora {
 
-constexpr int kRowsDirect = 4;
 constexpr int kRowsJoinMax = 16;  // slabs at most
 
 struct RowsArgs {
@@ -47,6 +46,7 @@ struct RowsArgs {
   int act;
   float* slabs;          // K split over the grid: [split][M][N] (gated: [split][2][M][N]), or NULL
   int splits;
+  int groups;            // shared form: workgroups along the columns
 };
 
 __device__ __forceinline__ void rows_store(const RowsArgs& p, bool gated, int m, int n, float a, float u) {
@@ -89,12 +89,13 @@ __device__ __forceinline__ void rows_ring(int n, M&& mul, F&& load) {
   rows_rest<D>(n - i, mul);
 }
 
-template <class W, bool GATE, bool PAIR>
+// Up to R = 4 or 8 rows.
+template <class W, int R, bool GATE, bool PAIR>
 __global__ __launch_bounds__(512, 2) void rows_direct_kernel(RowsArgs p, typename W::Args wa) {
   constexpr int CT = GATE ? 2 : 1, NX = PAIR ? 2 : 1, D = W::DEPTH * 2 / CT;
   // a chunk of the rows (PAIR: then one of their remainders, which meet the
   // weights as further rows), 16 bytes of padding per row against bank conflicts
-  constexpr int XROW = 256 + 16, XBYTES = kRowsDirect * XROW;
+  constexpr int XROW = 256 + 16, XBYTES = R * XROW, XPL = R / 4;
   extern __shared__ __attribute__((aligned(16))) char rows_smem[];
   const int lane = threadIdx.x & 63, ks = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -105,15 +106,15 @@ __global__ __launch_bounds__(512, 2) void rows_direct_kernel(RowsArgs p, typenam
   typename W::Tile tiles[CT];
 #pragma unroll
   for (int t = 0; t < CT; ++t) tiles[t] = w.tile(tile0, t);
-  // lane l brings piece l % 16 of row l / 16 (rows past M: zeros) and reads
-  // the fragment of row l % 4 (PAIR: l % 8), further rows repeat them and their
-  // sums are dropped
+  // lane l brings piece l % 16 of rows l / 16 and l / 16 + 4 (rows past M:
+  // zeros) and reads the fragment of row l % R (PAIR: l % 2R), further rows
+  // repeat them and their sums are dropped
   const uint32_t xbytes = (uint32_t)p.M * (uint32_t)p.K * 2u;
   const uint32_t xoff = ((uint32_t)kq * (uint32_t)p.K + (uint32_t)l16 * 8u) * 2u;
   char* xl = rows_smem + wave * (NX * XBYTES);
 
   typename W::Buf q[D][CT];
-  u32x4_t x[D][NX];
+  u32x4_t x[D][NX][XPL];
   const int chunks = (p.K + 127) >> 7;
   // workgroups start at different chunks: in step they would all ask for the
   // same memory channels (rows lie a fixed distance apart)
@@ -122,8 +123,12 @@ __global__ __launch_bounds__(512, 2) void rows_direct_kernel(RowsArgs p, typenam
     const bool real = i < chunks;
     const int c = i + rot < chunks ? i + rot : i + rot - chunks;
     const uint32_t o = l16 * 8 < (real ? p.K - c * 128 : 0) ? xoff : kBufNone;
-    x[u][0] = rows_load(p.x, xbytes, o, (uint32_t)c * 256u);
-    if (PAIR) x[u][NX - 1] = rows_load(p.x_lo, xbytes, o, (uint32_t)c * 256u);
+#pragma unroll
+    for (int h = 0; h < XPL; ++h) {
+      const uint32_t oh = o == kBufNone ? o : o + h * 8u * (uint32_t)p.K;  // 4 rows on
+      x[u][0][h] = rows_load(p.x, xbytes, oh, (uint32_t)c * 256u);
+      if (PAIR) x[u][NX - 1][h] = rows_load(p.x_lo, xbytes, oh, (uint32_t)c * 256u);
+    }
 #pragma unroll
     for (int t = 0; t < CT; ++t) w.load(q[u][t], tiles[t], c, real);
     // loads return in order: kept in the order of their use
@@ -139,12 +144,14 @@ __global__ __launch_bounds__(512, 2) void rows_direct_kernel(RowsArgs p, typenam
     // (a wavefront's LDS accesses run in order)
 #pragma unroll
     for (int v = 0; v < NX; ++v)
-      *reinterpret_cast<u32x4_t*>(xl + v * XBYTES + kq * XROW + l16 * 16) = x[u][v];
+#pragma unroll
+      for (int h = 0; h < XPL; ++h)
+        *reinterpret_cast<u32x4_t*>(xl + v * XBYTES + (kq + 4 * h) * XROW + l16 * 16) = x[u][v][h];
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const u32x4_t a =
-          *reinterpret_cast<const u32x4_t*>(xl + (l16 & (4 * NX - 1)) * XROW + j * 64 + kq * 16);
+          *reinterpret_cast<const u32x4_t*>(xl + (l16 & (R * NX - 1)) * XROW + j * 64 + kq * 16);
       acc.begin(w, q[u], j);
 #pragma unroll
       for (int t = 0; t < CT; ++t) acc.mul(0, t, a, w.operand(q[u][t], j));
@@ -169,9 +176,9 @@ __global__ __launch_bounds__(512, 2) void rows_direct_kernel(RowsArgs p, typenam
   for (int t = 0; t < CT; ++t) {
     s[t] = part[t * 64 + lane];
     for (int v = 1; v < ks; ++v) s[t] += part[(v * CT + t) * 64 + lane];
-    if (PAIR) {  // row m's remainder is row 4 + m, 16 lanes on
+    if (PAIR) {  // row m's remainder is row R + m, 4 R lanes on
 #pragma unroll
-      for (int v = 0; v < 4; ++v) s[t][v] += __shfl_down(s[t][v], 16, 64);
+      for (int v = 0; v < 4; ++v) s[t][v] += __shfl_down(s[t][v], 4 * R, 64);
     }
   }
   const int no = tile0 * 16 + l16;
@@ -180,10 +187,11 @@ __global__ __launch_bounds__(512, 2) void rows_direct_kernel(RowsArgs p, typenam
     if (kq * 4 + v < p.M && no < p.N) rows_store(p, GATE, kq * 4 + v, no, s[0][v], s[CT - 1][v]);
 }
 
-// RF: fragments of 16 rows.  Grid: groups of 8 tiles, row tiles, K splits.
+// RF: fragments of 16 rows.  Grid: groups of up to 8 tiles (an even share
+// each), row tiles, K splits.
 template <class W, int RF, bool GATE, bool PAIR>
 __global__ __launch_bounds__(512, 2) void rows_shared_kernel(RowsArgs p, typename W::Args wa) {
-  constexpr int CT = GATE ? 2 : 1, NX = PAIR ? 2 : 1, D = std::min(W::DEPTH * 2 / CT, RF == 1 ? 8 : 4);
+  constexpr int CT = GATE ? 2 : 1, NX = PAIR ? 2 : 1, D = RF <= 2 ? W::DEPTH * 2 / CT : std::min(W::DEPTH * 2 / CT, 4);
   constexpr int PIECES = RF * 256 * NX;           // 16-byte pieces of a chunk of rows
   constexpr int XPT = (PIECES + 511) / 512;       // per thread
   __shared__ __attribute__((aligned(16))) u32x4_t xl[2][PIECES];
@@ -191,12 +199,16 @@ __global__ __launch_bounds__(512, 2) void rows_shared_kernel(RowsArgs p, typenam
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, kq = lane >> 4;
   const int m0 = blockIdx.y * (16 * RF), rows = min(16 * RF, p.M - m0);
-  const int tile0 = blockIdx.x * 8 + wave;
+  // wavefronts past the group's tiles only bring rows
+  const int all = (p.N + 15) >> 4;
+  const int first = (int)((int64_t)all * blockIdx.x / p.groups), last = (int)((int64_t)all * (blockIdx.x + 1) / p.groups);
+  const int tile0 = first + wave;
+  const bool active = tile0 < last;
 
   const W w(wa, p.N, p.K, lane);
   typename W::Tile tiles[CT];
 #pragma unroll
-  for (int t = 0; t < CT; ++t) tiles[t] = w.tile(tile0, t);
+  for (int t = 0; t < CT; ++t) tiles[t] = w.tile(active ? tile0 : first, t);
 
   // this workgroup's chunks
   const int chunks = (p.K + 127) >> 7, z = blockIdx.z;
@@ -244,18 +256,13 @@ __global__ __launch_bounds__(512, 2) void rows_shared_kernel(RowsArgs p, typenam
   };
   typename W::template Acc<RF, CT> acc;
   acc.clear();
-#pragma unroll
-  for (int u = 0; u < D; ++u) {
-    load_x(u, u);
-    load_w(u, u);
-    __builtin_amdgcn_sched_barrier(0);  // loads return in order: kept in the order of their use
-  }
-  auto mul = [&](auto u_c) __attribute__((always_inline)) {
+  auto mul = [&](auto u_c, auto act_c) __attribute__((always_inline)) {
     constexpr int u = decltype(u_c)::value;
     // the buffer written here was last read two chunks ago, before the
     // previous barrier
     put_x(u & 1, u);
     lds_barrier();
+    if constexpr (!decltype(act_c)::value) return;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       u32x4_t a[NX][RF];
@@ -276,11 +283,26 @@ __global__ __launch_bounds__(512, 2) void rows_shared_kernel(RowsArgs p, typenam
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  rows_ring<D>(n, mul, [&](auto u_c, int i) __attribute__((always_inline)) {
-    load_x(decltype(u_c)::value, i);
-    load_w(decltype(u_c)::value, i);
-    __builtin_amdgcn_sched_barrier(0);
-  });
+  auto run = [&](auto act_c) __attribute__((always_inline)) {
+    constexpr bool ACT = decltype(act_c)::value;
+#pragma unroll
+    for (int u = 0; u < D; ++u) {
+      load_x(u, u);
+      if (ACT) load_w(u, u);
+      __builtin_amdgcn_sched_barrier(0);  // loads return in order: kept in the order of their use
+    }
+    rows_ring<D>(n, [&](auto u_c) __attribute__((always_inline)) { mul(u_c, act_c); },
+                 [&](auto u_c, int i) __attribute__((always_inline)) {
+                   load_x(decltype(u_c)::value, i);
+                   if (ACT) load_w(decltype(u_c)::value, i);
+                   __builtin_amdgcn_sched_barrier(0);
+                 });
+  };
+  if (!active) {
+    run(std::false_type());
+    return;
+  }
+  run(std::true_type());
   const int no = tile0 * 16 + l16;
   if (no >= p.N) return;
 #pragma unroll
@@ -315,29 +337,43 @@ __global__ __launch_bounds__(256) void rows_join_kernel(RowsArgs p) {
   rows_store(p, GATE, (int)(i / p.N), (int)(i % p.N), s[0], s[CT - 1]);
 }
 
+// ---- host side: which form, with how many workgroups
+
 inline int rows_fragments(int M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
 
-// K splits of the shared form: one workgroup per CU (256), of at least 4
-// chunks each.
-inline int rows_splits(int M, int N, int K) {
-  if (M <= kRowsDirect) return 1;
-  const int rt = 16 * rows_fragments(M);
-  const int64_t wgs = (int64_t)((N + 127) / 128) * ((M + rt - 1) / rt);
-  const int64_t s = std::min<int64_t>((256 + wgs / 2) / wgs, (K + 511) / 512);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(s, kRowsJoinMax));
+struct RowsPlan {
+  bool direct;
+  int groups, splits;  // shared form
+};
+
+// The direct form fetches the rows anew for every tile: 2 M lines of 128
+// bytes per chunk beside the weights' (lines_per_chunk of them), at about 7
+// TB/s over all CUs.  The shared form costs about 5 us more than its weights:
+// another launch and the slabs.  (M = 5, 11008 x 2880, 4 bits: 10 us direct
+// against 15; M = 32, 4096 x 11008: 30 against 14.)
+inline RowsPlan rows_plan(int M, int N, int K, int lines_per_chunk) {
+  RowsPlan r{false, 0, 1};
+  const int64_t tiles = (N + 15) / 16, chunks = (K + 127) / 128;
+  r.direct = M <= 8 && (2 * M <= lines_per_chunk / 2 || tiles * chunks * 2 * M * 128 < 5 * 7000000LL);
+  if (r.direct) return r;
+  // at most one workgroup per CU (256) where K is split, since a second round
+  // of a few would take as long as the first; 4 chunks each at least
+  const int64_t rt = 16 * rows_fragments(M), row_tiles = (M + rt - 1) / rt, least = (tiles + 7) / 8;
+  const int64_t s = std::min<int64_t>(256 / (least * row_tiles), (chunks + 3) / 4);
+  r.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, kRowsJoinMax));
+  r.groups = (int)std::max<int64_t>(least, std::min<int64_t>(tiles, 256 / (r.splits * row_tiles)));
+  return r;
 }
 
 // Bytes of slabs that a product needs.
-inline size_t rows_slab_bytes(int M, int N, int K, bool gated) {
-  const int s = rows_splits(M, N, K);
-  return s > 1 ? (size_t)s * (gated ? 2 : 1) * M * N * sizeof(float) : 0;
+inline size_t rows_slab_bytes(const RowsPlan& r, int M, int N, bool gated) {
+  return r.splits > 1 ? (size_t)r.splits * (gated ? 2 : 1) * M * N * sizeof(float) : 0;
 }
 
-// The most that any product of M rows needs: K is split only while the split
-// groups number at most 256 + groups / 2 <= 341, each of 128 columns (gated:
-// pairs) and up to 16 RF rows.
+// The most that any product of M rows needs: with all splits the groups, of
+// 128 columns (gated: pairs) and up to 16 RF rows, number at most 256.
 inline size_t rows_slab_bound(int M) {
-  return M <= kRowsDirect ? 0 : (size_t)341 * 128 * 16 * rows_fragments(M) * 2 * sizeof(float);
+  return (size_t)256 * 128 * 16 * rows_fragments(M) * 2 * sizeof(float);
 }
 
 // Wavefronts that split K in the direct form: about 2048 of them over the
@@ -348,18 +384,25 @@ inline int rows_ksplit(int64_t workgroups, int K) {
   return ks;
 }
 
+template <class W, int R, bool GATE, bool PAIR>
+void launch_rows_direct(const RowsArgs& a, const typename W::Args& wa, hipStream_t st) {
+  const int tiles = (a.N + 15) / 16, ks = rows_ksplit(tiles, a.K);
+  constexpr int lds = std::max((GATE ? 2 : 1) * 1024, (PAIR ? 2 : 1) * R * (256 + 16));
+  rows_direct_kernel<W, R, GATE, PAIR><<<tiles, 64 * ks, ks * lds, st>>>(a, wa);
+}
+
 template <class W, bool GATE, bool PAIR>
 void launch_rows(RowsArgs a, const typename W::Args& wa, hipStream_t st) {
-  const int tiles = (a.N + 15) / 16;
-  a.splits = rows_splits(a.M, a.N, a.K);
-  if (a.M <= kRowsDirect) {
-    const int ks = rows_ksplit(tiles, a.K);
-    constexpr int lds = std::max((GATE ? 2 : 1) * 1024, (PAIR ? 2 : 1) * kRowsDirect * (256 + 16));
-    rows_direct_kernel<W, GATE, PAIR><<<tiles, 64 * ks, ks * lds, st>>>(a, wa);
+  const RowsPlan r = rows_plan(a.M, a.N, a.K, W::LINES);
+  if (r.direct) {
+    if (a.M <= 4) launch_rows_direct<W, 4, GATE, PAIR>(a, wa, st);
+    else launch_rows_direct<W, 8, GATE, PAIR>(a, wa, st);
     return;
   }
+  a.splits = r.splits;
+  a.groups = r.groups;
   const int rf = rows_fragments(a.M);
-  const dim3 grid((tiles + 7) / 8, (a.M + 16 * rf - 1) / (16 * rf), a.splits);
+  const dim3 grid(r.groups, (a.M + 16 * rf - 1) / (16 * rf), r.splits);
   if (rf == 1) rows_shared_kernel<W, 1, GATE, PAIR><<<grid, 512, 0, st>>>(a, wa);
   if constexpr (!PAIR) {
     if (rf == 2) rows_shared_kernel<W, 2, GATE, false><<<grid, 512, 0, st>>>(a, wa);

@@ -72,6 +72,7 @@ struct PackedWeights {
     W4Layout L;
   };
   static constexpr int GPC = 4 / SPG;  // groups of a chunk
+  static constexpr int LINES = 8;
   static constexpr int DEPTH = SPG == 1 ? 2 : 4;
   struct Tile {  // chunk 0 of the tile's weights, scales and zero points
     const char* q;
@@ -215,6 +216,8 @@ void launch_product(const RowsArgs& a, const W4Layout& L, const void* w, const v
   else with(std::integral_constant<int, 4>());
 }
 
+size_t slab_bytes(const W4Layout& L, int M) { return rows_slab_bytes(rows_plan(M, L.N, L.K, 8), M, L.N, false); }
+
 constexpr int32_t kPairRows = 16;  // up to here h goes on as a bf16 pair, which costs nothing beside the weights
 constexpr int32_t kMaxRows = 1 << 16;
 
@@ -250,7 +253,7 @@ int moe_lora_w4_pack(const moe_lora_w4* w, const uint8_t* q, const uint16_t* sca
 size_t moe_lora_w4_workspace_bytes(const moe_lora_w4* w, int32_t M) {
   W4Layout L;
   if (check_matrix(w, &L) || M < 0 || M > kMaxRows) return 0;
-  const size_t n = M ? round256(rows_slab_bytes(M, L.N, L.K, false)) : 0;
+  const size_t n = M ? round256(slab_bytes(L, M)) : 0;
   return n ? n : 256;
 }
 
@@ -263,14 +266,14 @@ int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, void*
   if (M > kMaxRows) return MOE_LORA_EUNSUPPORTED;
   if (M == 0) return MOE_LORA_OK;
   if (!x || !y || !w->data) return MOE_LORA_EINVAL;
-  const size_t need = rows_slab_bytes(M, L.N, L.K, false);
+  const size_t need = slab_bytes(L, M);
   if (need && (!workspace || ws_bytes < need)) return MOE_LORA_EWORKSPACE;
   if (!aligned16(x) || (uintptr_t)y % 2 || !aligned16(w->data) || (need && !aligned16(workspace)))
     return MOE_LORA_EALIGN;
   const Range in[] = {{x, (size_t)M * L.K * 2}, {w->data, L.total}};
   const Range out[] = {{y, (size_t)M * L.N * 2}, {workspace, need}};
   if (any_overlap(in, 2, out, 2)) return MOE_LORA_EINVAL;
-  launch_product(RowsArgs{x, nullptr, y, nullptr, M, L.N, L.K, 0, (float*)workspace, 1}, L, w->data, nullptr, (hipStream_t)stream);
+  launch_product(RowsArgs{x, nullptr, y, nullptr, M, L.N, L.K, 0, (float*)workspace, 1, 0}, L, w->data, nullptr, (hipStream_t)stream);
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
@@ -309,8 +312,8 @@ int moe_lora_w4_ffn_forward(const moe_lora_w4* gate, const moe_lora_w4* up, cons
   uint16_t* h = (uint16_t*)workspace;
   uint16_t* h_lo = M <= kPairRows ? (uint16_t*)((char*)workspace + round256((size_t)M * Ld.K * 2)) : nullptr;
   float* slabs = (float*)((char*)workspace + ffn_h_bytes(M, Ld.K));
-  launch_product(RowsArgs{x, nullptr, h, h_lo, M, Lg.N, Lg.K, act, slabs, 1}, Lg, gate->data, up->data, st);
-  launch_product(RowsArgs{h, h_lo, y, nullptr, M, Ld.N, Ld.K, 0, slabs, 1}, Ld, down->data, nullptr, st);
+  launch_product(RowsArgs{x, nullptr, h, h_lo, M, Lg.N, Lg.K, act, slabs, 1, 0}, Lg, gate->data, up->data, st);
+  launch_product(RowsArgs{h, h_lo, y, nullptr, M, Ld.N, Ld.K, 0, slabs, 1, 0}, Ld, down->data, nullptr, st);
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
