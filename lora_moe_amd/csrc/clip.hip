@@ -6,9 +6,11 @@
 // Two passes, since no gradient can be scaled before the norm is known: the
 // first writes one partial sum per workgroup, the second adds them up in
 // every workgroup (in the same order, so c is the same everywhere and from
-// run to run) and scales.  Sums are fp64: squares of fp32 gradients cannot
-// overflow and the order of addition does not show in fp32.  Both passes are
-// bound by memory.
+// run to run) and scales.  Both are bound by memory; the second goes through
+// the chunks backwards, so that what the first read last is still in the 256
+// MB cache beside the HBM.  Sums are fp64 of fp32 sums of one 16-byte piece,
+// redone in fp64 where that leaves fp32's range: squares cannot overflow or
+// vanish, and the order of addition does not show in fp32.
 //
 // The tensors' table travels in the kernel arguments, kTensors at a time, so
 // nothing is kept between calls and a captured call holds its own copy.
@@ -27,7 +29,7 @@ namespace {
 
 constexpr int kTensors = 112;      // per launch: 3.2 KB of kernel arguments
 constexpr int kChunk = 16384;      // elements one workgroup takes at a time
-constexpr int kMaxParts = 1024;    // partial sums of one call, beyond one per launch
+constexpr int kMaxParts = 2048;    // partial sums of one call, beyond one per launch
 constexpr float kEps = 1e-6f;
 
 struct Table {
@@ -55,17 +57,78 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
   else static_cast<uint16_t*>(p)[i] = DT == MOE_LORA_BF16 ? f32_to_bf16(v) : f32_to_f16(v);
 }
 
-// the tensor that holds chunk c: the last whose first chunk is <= c (empty
-// tensors share their first chunk with the next one)
-__device__ __forceinline__ int tensor_of(const Table& t, int c) {
-  int lo = 0, hi = t.n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (t.first[mid] <= c) lo = mid;
-    else hi = mid;
+// 16 bytes of gradients as fp32
+template <int DT>
+struct Piece {
+  static constexpr int N = DT == MOE_LORA_F32 ? 4 : 8;
+  float v[N];
+  __device__ __forceinline__ explicit Piece(u32x4_t q) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (DT == MOE_LORA_F32) {
+        v[i] = __uint_as_float(q[i]);
+      } else {
+        v[2 * i % N] = DT == MOE_LORA_BF16 ? bf16_lo(q[i]) : f16_to_f32((uint16_t)q[i]);
+        v[(2 * i + 1) % N] = DT == MOE_LORA_BF16 ? bf16_hi(q[i]) : f16_to_f32((uint16_t)(q[i] >> 16));
+      }
+    }
   }
-  return lo;
-}
+  __device__ __forceinline__ double squares() const {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s += v[i] * v[i];
+    // in fp32's range, no square that matters beside the others was lost
+    if (s > 1e-30f && s < 1e38f) return (double)s;
+    double d = 0.;
+#pragma unroll
+    for (int i = 0; i < N; ++i) d += (double)v[i] * (double)v[i];
+    return d;
+  }
+  __device__ __forceinline__ u32x4_t scaled(float c) const {
+    u32x4_t q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (DT == MOE_LORA_F32) {
+        q[i] = __float_as_uint(v[i] * c);
+      } else {
+        const float a = v[2 * i % N] * c, b = v[(2 * i + 1) % N] * c;
+        q[i] = DT == MOE_LORA_BF16 ? f32_to_bf16(a) | (uint32_t)f32_to_bf16(b) << 16
+                                   : f32_to_f16(a) | (uint32_t)f32_to_f16(b) << 16;
+      }
+    }
+    return q;
+  }
+};
+
+// A walk over a workgroup's contiguous share of the chunks, forwards or
+// backwards: the tensor is searched once and then followed.
+struct Walk {
+  const Table& t;
+  int c, k;
+  __device__ Walk(const Table& t_, int c_) : t(t_), c(c_) {
+    // the last tensor whose first chunk is <= c (empty tensors share their
+    // first chunk with the next one)
+    int lo = 0, hi = t.n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (t.first[mid] <= c) lo = mid;
+      else hi = mid;
+    }
+    k = lo;
+  }
+  __device__ void forward() {
+    ++c;
+    while (k + 1 < t.n && t.first[k + 1] <= c) ++k;
+  }
+  __device__ void backward() {
+    --c;
+    while (k > 0 && t.first[k] > c) --k;
+  }
+  __device__ int64_t begin() const { return (int64_t)(c - t.first[k]) * kChunk; }
+  __device__ int64_t end() const { return min(begin() + kChunk, t.numel[k]); }
+};
+
+__device__ __forceinline__ int share(int chunks, int i, int of) { return (int)((int64_t)chunks * i / of); }
 
 __device__ __forceinline__ double block_sum(double v, double* lds) {
 #pragma unroll
@@ -76,10 +139,28 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   return lds[0] + lds[1] + lds[2] + lds[3];
 }
 
+constexpr int kAhead = 8;  // 16-byte loads in flight per thread
+
 template <int DT>
 __device__ __forceinline__ double chunk_squares(const void* g, int64_t i0, int64_t i1) {
+  typedef Piece<DT> P;
   double s = 0.;
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += 256) {
+  int64_t done = i0;
+  if (((uintptr_t)g & 15u) == 0) {
+    const u32x4_t* p = static_cast<const u32x4_t*>(g) + i0 / P::N;
+    const int pieces = (int)((i1 - i0) / P::N);
+    int i = threadIdx.x;
+    for (; i + (kAhead - 1) * 256 < pieces; i += kAhead * 256) {
+      u32x4_t q[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) q[j] = p[i + j * 256];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) s += P(q[j]).squares();
+    }
+    for (; i < pieces; i += 256) s += P(p[i]).squares();
+    done = i0 + (int64_t)pieces * P::N;
+  }
+  for (int64_t i = done + threadIdx.x; i < i1; i += 256) {
     const double v = (double)load1<DT>(g, i);
     s += v * v;
   }
@@ -89,13 +170,16 @@ __device__ __forceinline__ double chunk_squares(const void* g, int64_t i0, int64
 __global__ __launch_bounds__(256) void norm_kernel(Table t, double* __restrict__ parts) {
   __shared__ double lds[4];
   double s = 0.;
-  for (int c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
-    const int k = tensor_of(t, c);
-    const int64_t i0 = (int64_t)(c - t.first[k]) * kChunk;
-    const int64_t i1 = min(i0 + kChunk, t.numel[k]);
-    if (t.dtype[k] == MOE_LORA_F32) s += chunk_squares<MOE_LORA_F32>(t.g[k], i0, i1);
-    else if (t.dtype[k] == MOE_LORA_BF16) s += chunk_squares<MOE_LORA_BF16>(t.g[k], i0, i1);
-    else s += chunk_squares<MOE_LORA_F16>(t.g[k], i0, i1);
+  const int chunks = t.first[t.n];
+  const int c0 = share(chunks, blockIdx.x, gridDim.x), c1 = share(chunks, blockIdx.x + 1, gridDim.x);
+  if (c0 < c1) {
+    for (Walk w(t, c0); w.c < c1; w.forward()) {
+      const int dt = t.dtype[w.k];
+      const void* g = t.g[w.k];
+      if (dt == MOE_LORA_F32) s += chunk_squares<MOE_LORA_F32>(g, w.begin(), w.end());
+      else if (dt == MOE_LORA_BF16) s += chunk_squares<MOE_LORA_BF16>(g, w.begin(), w.end());
+      else s += chunk_squares<MOE_LORA_F16>(g, w.begin(), w.end());
+    }
   }
   s = block_sum(s, lds);
   if (threadIdx.x == 0) parts[blockIdx.x] = s;
@@ -103,7 +187,24 @@ __global__ __launch_bounds__(256) void norm_kernel(Table t, double* __restrict__
 
 template <int DT>
 __device__ __forceinline__ void chunk_scale(const void* g, void* o, int64_t i0, int64_t i1, float c) {
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += 256) store1<DT>(o, i, load1<DT>(g, i) * c);
+  typedef Piece<DT> P;
+  int64_t done = i0;
+  if ((((uintptr_t)g | (uintptr_t)o) & 15u) == 0) {
+    const u32x4_t* p = static_cast<const u32x4_t*>(g) + i0 / P::N;
+    u32x4_t* d = static_cast<u32x4_t*>(o) + i0 / P::N;
+    const int pieces = (int)((i1 - i0) / P::N);
+    int i = threadIdx.x;
+    for (; i + (kAhead - 1) * 256 < pieces; i += kAhead * 256) {
+      u32x4_t q[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) q[j] = __builtin_nontemporal_load(p + i + j * 256);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) __builtin_nontemporal_store(P(q[j]).scaled(c), d + i + j * 256);
+    }
+    for (; i < pieces; i += 256) d[i] = P(p[i]).scaled(c);
+    done = i0 + (int64_t)pieces * P::N;
+  }
+  for (int64_t i = done + threadIdx.x; i < i1; i += 256) store1<DT>(o, i, load1<DT>(g, i) * c);
 }
 
 __global__ __launch_bounds__(256) void scale_kernel(Table t, const double* __restrict__ parts, int nparts,
@@ -115,14 +216,17 @@ __global__ __launch_bounds__(256) void scale_kernel(Table t, const double* __res
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)s;
   const double cd = (double)max_norm / (s + (double)kEps);
   const float c = cd > 1. ? 1.f : (float)cd;  // NaN stays NaN
-  for (int k0 = blockIdx.x; k0 < t.first[t.n]; k0 += gridDim.x) {
-    const int k = tensor_of(t, k0);
-    if (c == 1.f && t.g[k] == t.out[k]) continue;  // in place and nothing to scale
-    const int64_t i0 = (int64_t)(k0 - t.first[k]) * kChunk;
-    const int64_t i1 = min(i0 + kChunk, t.numel[k]);
-    if (t.dtype[k] == MOE_LORA_F32) chunk_scale<MOE_LORA_F32>(t.g[k], t.out[k], i0, i1, c);
-    else if (t.dtype[k] == MOE_LORA_BF16) chunk_scale<MOE_LORA_BF16>(t.g[k], t.out[k], i0, i1, c);
-    else chunk_scale<MOE_LORA_F16>(t.g[k], t.out[k], i0, i1, c);
+  const int chunks = t.first[t.n], block = (int)gridDim.x - 1 - (int)blockIdx.x;
+  const int c0 = share(chunks, block, gridDim.x), c1 = share(chunks, block + 1, gridDim.x);
+  if (c0 >= c1) return;
+  for (Walk w(t, c1 - 1); w.c >= c0; w.backward()) {
+    const void* g = t.g[w.k];
+    void* o = t.out[w.k];
+    if (c == 1.f && g == o) continue;  // in place and nothing to scale
+    const int dt = t.dtype[w.k];
+    if (dt == MOE_LORA_F32) chunk_scale<MOE_LORA_F32>(g, o, w.begin(), w.end(), c);
+    else if (dt == MOE_LORA_BF16) chunk_scale<MOE_LORA_BF16>(g, o, w.begin(), w.end(), c);
+    else chunk_scale<MOE_LORA_F16>(g, o, w.begin(), w.end(), c);
   }
 }
 
@@ -191,9 +295,11 @@ int moe_lora_clip_grads(const moe_lora_grad* grads, int32_t n, float max_norm, f
   hipStream_t st = (hipStream_t)stream;
   double* parts = (double*)workspace;
   int nparts = 0;
+  const int32_t launches = std::max<int32_t>(1, (n + kTensors - 1) / kTensors);
   for (int pass = 0; pass < 2; ++pass) {
-    int32_t i0 = 0;
-    do {
+    for (int32_t l = 0; l < launches; ++l) {
+      // backwards in the second pass
+      const int32_t i0 = (pass ? launches - 1 - l : l) * kTensors;
       Table t = {};
       int64_t c = 0;
       while (t.n < kTensors && i0 + t.n < n) {
@@ -206,18 +312,17 @@ int moe_lora_clip_grads(const moe_lora_grad* grads, int32_t n, float max_norm, f
         c += chunks_of(e.numel);
       }
       t.first[t.n] = (int)c;
-      i0 += t.n;
       if (pass == 0) {
         // this launch's share of the partial sums, one at least
         const int blocks = (int)std::max<int64_t>(1, std::min(c, kMaxParts * c / std::max<int64_t>(1, total)));
         norm_kernel<<<blocks, 256, 0, st>>>(t, parts + nparts);
         nparts += blocks;
       } else {
-        const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(c, 2048));
-        scale_kernel<<<blocks, 256, 0, st>>>(t, parts, nparts, max_norm, i0 == t.n ? norm : nullptr);
+        const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(c, kMaxParts));
+        scale_kernel<<<blocks, 256, 0, st>>>(t, parts, nparts, max_norm, i0 == 0 ? norm : nullptr);
       }
       if (hipGetLastError() != hipSuccess) return MOE_LORA_EHIP;
-    } while (i0 < n);
+    }
   }
   return MOE_LORA_OK;
 }
