@@ -27,8 +27,11 @@ namespace moelora {
 
 namespace {
 
-constexpr int kTensors = 112;      // per launch: 3.2 KB of kernel arguments
-constexpr int kChunk = 16384;      // elements one workgroup takes at a time
+constexpr int kTensors = 256;      // per launch: 7.4 KB of kernel arguments
+// elements one workgroup takes at a time: enough chunks to go round in a small
+// call, whole batches of loads in a large one (540 M gradients: 577 us with
+// 16384, 608 with 8192)
+constexpr int kChunkMin = 2048, kChunkMax = 16384;
 constexpr int kMaxParts = 2048;    // partial sums of one call, beyond one per launch
 constexpr float kEps = 1e-6f;
 
@@ -38,7 +41,7 @@ struct Table {
   int64_t numel[kTensors];
   int first[kTensors + 1];  // first chunk of each tensor
   uint8_t dtype[kTensors];
-  int n;
+  int n, chunk;
 };
 
 __device__ __forceinline__ float f16_to_f32(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
@@ -100,35 +103,17 @@ struct Piece {
   }
 };
 
-// A walk over a workgroup's contiguous share of the chunks, forwards or
-// backwards: the tensor is searched once and then followed.
-struct Walk {
-  const Table& t;
-  int c, k;
-  __device__ Walk(const Table& t_, int c_) : t(t_), c(c_) {
-    // the last tensor whose first chunk is <= c (empty tensors share their
-    // first chunk with the next one)
-    int lo = 0, hi = t.n;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (t.first[mid] <= c) lo = mid;
-      else hi = mid;
-    }
-    k = lo;
+// the tensor that holds chunk c: the last whose first chunk is <= c (empty
+// tensors share their first chunk with the next one)
+__device__ __forceinline__ int tensor_of(const Table& t, int c) {
+  int lo = 0, hi = t.n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.first[mid] <= c) lo = mid;
+    else hi = mid;
   }
-  __device__ void forward() {
-    ++c;
-    while (k + 1 < t.n && t.first[k + 1] <= c) ++k;
-  }
-  __device__ void backward() {
-    --c;
-    while (k > 0 && t.first[k] > c) --k;
-  }
-  __device__ int64_t begin() const { return (int64_t)(c - t.first[k]) * kChunk; }
-  __device__ int64_t end() const { return min(begin() + kChunk, t.numel[k]); }
-};
-
-__device__ __forceinline__ int share(int chunks, int i, int of) { return (int)((int64_t)chunks * i / of); }
+  return lo;
+}
 
 __device__ __forceinline__ double block_sum(double v, double* lds) {
 #pragma unroll
@@ -149,15 +134,15 @@ __device__ __forceinline__ double chunk_squares(const void* g, int64_t i0, int64
   if (((uintptr_t)g & 15u) == 0) {
     const u32x4_t* p = static_cast<const u32x4_t*>(g) + i0 / P::N;
     const int pieces = (int)((i1 - i0) / P::N);
-    int i = threadIdx.x;
-    for (; i + (kAhead - 1) * 256 < pieces; i += kAhead * 256) {
+    for (int i = threadIdx.x; i < pieces; i += kAhead * 256) {
       u32x4_t q[kAhead];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) q[j] = p[i + j * 256];
+      for (int j = 0; j < kAhead; ++j)
+        if (i + j * 256 < pieces) q[j] = p[i + j * 256];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) s += P(q[j]).squares();
+      for (int j = 0; j < kAhead; ++j)
+        if (i + j * 256 < pieces) s += P(q[j]).squares();
     }
-    for (; i < pieces; i += 256) s += P(p[i]).squares();
     done = i0 + (int64_t)pieces * P::N;
   }
   for (int64_t i = done + threadIdx.x; i < i1; i += 256) {
@@ -170,16 +155,13 @@ __device__ __forceinline__ double chunk_squares(const void* g, int64_t i0, int64
 __global__ __launch_bounds__(256) void norm_kernel(Table t, double* __restrict__ parts) {
   __shared__ double lds[4];
   double s = 0.;
-  const int chunks = t.first[t.n];
-  const int c0 = share(chunks, blockIdx.x, gridDim.x), c1 = share(chunks, blockIdx.x + 1, gridDim.x);
-  if (c0 < c1) {
-    for (Walk w(t, c0); w.c < c1; w.forward()) {
-      const int dt = t.dtype[w.k];
-      const void* g = t.g[w.k];
-      if (dt == MOE_LORA_F32) s += chunk_squares<MOE_LORA_F32>(g, w.begin(), w.end());
-      else if (dt == MOE_LORA_BF16) s += chunk_squares<MOE_LORA_BF16>(g, w.begin(), w.end());
-      else s += chunk_squares<MOE_LORA_F16>(g, w.begin(), w.end());
-    }
+  for (int c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
+    const int k = tensor_of(t, c), dt = t.dtype[k];
+    const void* g = t.g[k];
+    const int64_t i0 = (int64_t)(c - t.first[k]) * t.chunk, i1 = min(i0 + t.chunk, t.numel[k]);
+    if (dt == MOE_LORA_F32) s += chunk_squares<MOE_LORA_F32>(g, i0, i1);
+    else if (dt == MOE_LORA_BF16) s += chunk_squares<MOE_LORA_BF16>(g, i0, i1);
+    else s += chunk_squares<MOE_LORA_F16>(g, i0, i1);
   }
   s = block_sum(s, lds);
   if (threadIdx.x == 0) parts[blockIdx.x] = s;
@@ -193,15 +175,15 @@ __device__ __forceinline__ void chunk_scale(const void* g, void* o, int64_t i0, 
     const u32x4_t* p = static_cast<const u32x4_t*>(g) + i0 / P::N;
     u32x4_t* d = static_cast<u32x4_t*>(o) + i0 / P::N;
     const int pieces = (int)((i1 - i0) / P::N);
-    int i = threadIdx.x;
-    for (; i + (kAhead - 1) * 256 < pieces; i += kAhead * 256) {
+    for (int i = threadIdx.x; i < pieces; i += kAhead * 256) {
       u32x4_t q[kAhead];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) q[j] = __builtin_nontemporal_load(p + i + j * 256);
+      for (int j = 0; j < kAhead; ++j)
+        if (i + j * 256 < pieces) q[j] = __builtin_nontemporal_load(p + i + j * 256);
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) __builtin_nontemporal_store(P(q[j]).scaled(c), d + i + j * 256);
+      for (int j = 0; j < kAhead; ++j)
+        if (i + j * 256 < pieces) __builtin_nontemporal_store(P(q[j]).scaled(c), d + i + j * 256);
     }
-    for (; i < pieces; i += 256) d[i] = P(p[i]).scaled(c);
     done = i0 + (int64_t)pieces * P::N;
   }
   for (int64_t i = done + threadIdx.x; i < i1; i += 256) store1<DT>(o, i, load1<DT>(g, i) * c);
@@ -216,23 +198,27 @@ __global__ __launch_bounds__(256) void scale_kernel(Table t, const double* __res
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)s;
   const double cd = (double)max_norm / (s + (double)kEps);
   const float c = cd > 1. ? 1.f : (float)cd;  // NaN stays NaN
-  const int chunks = t.first[t.n], block = (int)gridDim.x - 1 - (int)blockIdx.x;
-  const int c0 = share(chunks, block, gridDim.x), c1 = share(chunks, block + 1, gridDim.x);
-  if (c0 >= c1) return;
-  for (Walk w(t, c1 - 1); w.c >= c0; w.backward()) {
-    const void* g = t.g[w.k];
-    void* o = t.out[w.k];
+  for (int k0 = t.first[t.n] - 1 - (int)blockIdx.x; k0 >= 0; k0 -= gridDim.x) {
+    const int k = tensor_of(t, k0), dt = t.dtype[k];
+    const void* g = t.g[k];
+    void* o = t.out[k];
     if (c == 1.f && g == o) continue;  // in place and nothing to scale
-    const int dt = t.dtype[w.k];
-    if (dt == MOE_LORA_F32) chunk_scale<MOE_LORA_F32>(g, o, w.begin(), w.end(), c);
-    else if (dt == MOE_LORA_BF16) chunk_scale<MOE_LORA_BF16>(g, o, w.begin(), w.end(), c);
-    else chunk_scale<MOE_LORA_F16>(g, o, w.begin(), w.end(), c);
+    const int64_t i0 = (int64_t)(k0 - t.first[k]) * t.chunk, i1 = min(i0 + t.chunk, t.numel[k]);
+    if (dt == MOE_LORA_F32) chunk_scale<MOE_LORA_F32>(g, o, i0, i1, c);
+    else if (dt == MOE_LORA_BF16) chunk_scale<MOE_LORA_BF16>(g, o, i0, i1, c);
+    else chunk_scale<MOE_LORA_F16>(g, o, i0, i1, c);
   }
 }
 
 size_t dtype_size(int32_t d) { return d == MOE_LORA_F32 ? 4 : 2; }
 
-int64_t chunks_of(int64_t numel) { return (numel + kChunk - 1) / kChunk; }
+int64_t chunks_of(int64_t numel, int chunk) { return (numel + chunk - 1) / chunk; }
+
+int chunk_for(int64_t elements) {
+  int c = kChunkMin;
+  while (c < kChunkMax && elements > (int64_t)c * kMaxParts) c *= 2;
+  return c;
+}
 
 }  // namespace
 
@@ -252,16 +238,19 @@ int moe_lora_clip_grads(const moe_lora_grad* grads, int32_t n, float max_norm, f
   if (n < 0 || (n && !grads) || !norm || !(max_norm >= 0.f)) return MOE_LORA_EINVAL;
   if (!workspace || ws_bytes < moe_lora_clip_workspace_bytes(n)) return MOE_LORA_EWORKSPACE;
   if ((uintptr_t)workspace % 8 || (uintptr_t)norm % 4) return MOE_LORA_EALIGN;
-  int64_t total = 0;
+  int64_t elements = 0;
   for (int32_t i = 0; i < n; ++i) {
     const moe_lora_grad& t = grads[i];
     if (t.numel < 0 || (t.dtype != MOE_LORA_F32 && t.dtype != MOE_LORA_BF16 && t.dtype != MOE_LORA_F16))
       return MOE_LORA_EINVAL;
     if (t.numel && (!t.g || !t.out)) return MOE_LORA_EINVAL;
     if ((uintptr_t)t.g % dtype_size(t.dtype) || (uintptr_t)t.out % dtype_size(t.dtype)) return MOE_LORA_EALIGN;
-    if (t.numel > (1LL << 40)) return MOE_LORA_EUNSUPPORTED;
-    total += chunks_of(t.numel);
+    if (t.numel > (1LL << 40) || elements > (1LL << 50)) return MOE_LORA_EUNSUPPORTED;
+    elements += t.numel;
   }
+  const int chunk = chunk_for(elements);
+  int64_t total = 0;
+  for (int32_t i = 0; i < n; ++i) total += chunks_of(grads[i].numel, chunk);
   if (total > (1LL << 30)) return MOE_LORA_EUNSUPPORTED;
   // every byte written has one owner, and only a gradient's own output may
   // lie on it: the same tensor twice would be scaled twice
@@ -301,6 +290,7 @@ int moe_lora_clip_grads(const moe_lora_grad* grads, int32_t n, float max_norm, f
       // backwards in the second pass
       const int32_t i0 = (pass ? launches - 1 - l : l) * kTensors;
       Table t = {};
+      t.chunk = chunk;
       int64_t c = 0;
       while (t.n < kTensors && i0 + t.n < n) {
         const moe_lora_grad& e = grads[i0 + t.n];
@@ -309,7 +299,7 @@ int moe_lora_clip_grads(const moe_lora_grad* grads, int32_t n, float max_norm, f
         t.numel[t.n] = e.numel;
         t.dtype[t.n] = (uint8_t)e.dtype;
         t.first[t.n++] = (int)c;
-        c += chunks_of(e.numel);
+        c += chunks_of(e.numel, chunk);
       }
       t.first[t.n] = (int)c;
       if (pass == 0) {
