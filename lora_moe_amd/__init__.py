@@ -281,7 +281,9 @@ def check_operands(shape, workspace=None, **tensors) -> None:
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle without the Stream object around it (0.4 us against 2.7
+        # a call, a quarter of a small product's)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -517,9 +519,9 @@ def _check_tensors(specs) -> None:
     for name, t, shape, dtype in specs:
         if t is None:
             raise ValueError(f"{name} is required")
-        if str(t.dtype) != "torch." + dtype:
+        if t.dtype is not getattr(torch, dtype):
             raise ValueError(f"{name}: dtype {str(t.dtype)[6:]}, expected {dtype}")
-        if shape is not None and tuple(t.shape) != shape:
+        if shape is not None and t.shape != shape:
             raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
