@@ -30,22 +30,25 @@ struct FfnGemm {
   uint16_t* out2;    // DH: h
   float* gu;         // GATE_UP: kept pre-activations [M][2N] or NULL; DH: read
   int act;
+  float* slabs;      // scratch of ffn_gemm_slab_bytes
+  int splits;        // K splits, set by the launch
 };
 
-// Up to this many tokens a forward that keeps nothing streams the weights
-// (ffn_rows.hip); beyond it, its rows would be read more often than the
-// weights and the tiles take over.
+// Up to this many tokens a forward streams the weights (ffn_rows.hip); beyond
+// it the rows' side takes over and tiles are better.
 constexpr int kRowsMax = 64;
 // Up to this many, h goes from one product to the other as a bf16 pair hi +
 // lo, which costs nothing beside the weights.
 constexpr int kRowsPair = 16;
 
-// FFN_GATE_UP (g.gu unused) or FFN_DOWN of at most kRowsMax rows.  a_lo: the
-// remainder of A (at most kRowsPair rows), or NULL; out_lo: that of h, or
-// NULL; slabs: ffn_rows_slab_bytes of scratch.
-int launch_ffn_rows(const FfnGemm& g, FfnProduct product, const uint16_t* a_lo, uint16_t* out_lo, float* slabs,
-                    hipStream_t st);
+// FFN_GATE_UP or FFN_DOWN of at most kRowsMax rows.  a_lo: the remainder of A
+// (at most kRowsPair rows), or NULL; out_lo: that of h, or NULL; g.slabs:
+// ffn_rows_slab_bytes of scratch.
+int launch_ffn_rows(const FfnGemm& g, FfnProduct product, const uint16_t* a_lo, uint16_t* out_lo, hipStream_t st);
 size_t ffn_rows_slab_bytes(int T, int H, int I);
+
+// Bytes of scratch that a product of these sizes needs (0 where K is not split).
+size_t ffn_gemm_slab_bytes(int M, int N, int K, FfnProduct product);
 
 int launch_ffn_gemm(const FfnGemm& g, FfnProduct product, hipStream_t st);
 

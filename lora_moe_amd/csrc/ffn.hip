@@ -36,11 +36,21 @@ struct Sizes {  // bytes
   }
 };
 
+// forward: h (up to kRowsPair tokens its remainder too), slabs; backward: h,
+// dgu, slabs
+size_t forward_fixed(const moe_lora_ffn_shape& s) { return round256(Sizes(s).h) * (s.T <= kRowsPair ? 2 : 1); }
+size_t backward_fixed(const moe_lora_ffn_shape& s) { return round256(Sizes(s).h) + round256(Sizes(s).dgu); }
+
 size_t ws_bytes_of(const moe_lora_ffn_shape& s, bool backward) {
-  const Sizes z(s);
-  size_t forward = round256(z.h) * (s.T <= kRowsPair ? 2 : 1);
-  if (s.T <= kRowsMax) forward += round256(ffn_rows_slab_bytes(s.T, s.H, s.I));
-  return backward ? std::max(forward, round256(z.h) + round256(z.dgu)) : forward;
+  const int T = s.T, H = s.H, I = s.I;
+  const size_t slabs = T <= kRowsMax ? ffn_rows_slab_bytes(T, H, I)
+                                     : std::max(ffn_gemm_slab_bytes(T, I, H, FFN_GATE_UP),
+                                                ffn_gemm_slab_bytes(T, H, I, FFN_DOWN));
+  const size_t forward = forward_fixed(s) + round256(slabs);
+  if (!backward) return forward;
+  const size_t back = std::max({ffn_gemm_slab_bytes(T, I, H, FFN_DH), ffn_gemm_slab_bytes(T, H, 2 * I, FFN_DX),
+                                ffn_gemm_slab_bytes(2 * I, H, T, FFN_DW), ffn_gemm_slab_bytes(H, I, T, FFN_DW)});
+  return std::max(forward, backward_fixed(s) + round256(back));
 }
 
 }  // namespace
@@ -50,8 +60,8 @@ extern "C" {
 
 size_t moe_lora_ffn_workspace_bytes(const moe_lora_ffn_shape* shape, int backward) {
   if (check_shape(shape)) return 0;
-  const size_t n = ws_bytes_of(*shape, backward != 0);
-  return n ? n : 256;  // T = 0 too: 0 says the shape is invalid
+  // T = 0 too: 0 says the shape is invalid
+  return shape->T ? ws_bytes_of(*shape, backward != 0) : 256;
 }
 
 int moe_lora_ffn_forward(const moe_lora_ffn_shape* shape, const uint16_t* x, const uint16_t* W_gu,
@@ -76,13 +86,13 @@ int moe_lora_ffn_forward(const moe_lora_ffn_shape* shape, const uint16_t* x, con
   FfnGemm g = {};
   g.act = shape->act;
   g.A = x, g.lda = H, g.B = W_gu, g.ldb = H, g.M = T, g.N = I, g.K = H, g.out = h, g.gu = gu;
-  if (!gu && T <= kRowsMax) {
+  g.slabs = (float*)((char*)workspace + forward_fixed(*shape));
+  if (T <= kRowsMax) {
     uint16_t* h_lo = T <= kRowsPair ? (uint16_t*)((char*)workspace + round256(z.h)) : nullptr;
-    float* slabs = (float*)((char*)workspace + round256(z.h) * (h_lo ? 2 : 1));
-    const int r = launch_ffn_rows(g, FFN_GATE_UP, nullptr, h_lo, slabs, st);
+    const int r = launch_ffn_rows(g, FFN_GATE_UP, nullptr, h_lo, st);
     if (r) return r;
-    g.A = h, g.lda = I, g.B = W_down, g.ldb = I, g.N = H, g.K = I, g.out = y;
-    return launch_ffn_rows(g, FFN_DOWN, h_lo, nullptr, slabs, st);
+    g.A = h, g.lda = I, g.B = W_down, g.ldb = I, g.N = H, g.K = I, g.out = y, g.gu = nullptr;
+    return launch_ffn_rows(g, FFN_DOWN, h_lo, nullptr, st);
   }
   const int r1 = launch_ffn_gemm(g, FFN_GATE_UP, st);
   if (r1) return r1;
@@ -98,7 +108,7 @@ int moe_lora_ffn_backward(const moe_lora_ffn_shape* shape, const uint16_t* dy, c
   if (!dx && !dW_gu && !dW_down) return MOE_LORA_EINVAL;
   const int T = shape->T, H = shape->H, I = shape->I;
   const Sizes z(*shape);
-  const size_t need = ws_bytes_of(*shape, true);
+  const size_t need = T > 0 ? ws_bytes_of(*shape, true) : 0;
   if (T > 0) {
     if (!dy || !x || !gu || !W_gu || !W_down) return MOE_LORA_EINVAL;
     if (!workspace || ws_bytes < need) return MOE_LORA_EWORKSPACE;
@@ -110,13 +120,14 @@ int moe_lora_ffn_backward(const moe_lora_ffn_shape* shape, const uint16_t* dy, c
   const Range out[] = {{dx, dx ? z.x : 0},
                        {dW_gu, dW_gu ? z.w_gu : 0},
                        {dW_down, dW_down ? z.w_down : 0},
-                       {workspace, T > 0 ? need : 0}};
+                       {workspace, need}};
   if (any_overlap(in, 5, out, 4)) return MOE_LORA_EINVAL;
   hipStream_t st = (hipStream_t)stream;
   uint16_t* h = (uint16_t*)workspace;
   uint16_t* dgu = (uint16_t*)((char*)workspace + round256(z.h));
   FfnGemm g = {};
   g.act = shape->act;
+  g.slabs = (float*)((char*)workspace + backward_fixed(*shape));
   g.A = dy, g.lda = H, g.B = W_down, g.ldb = I, g.M = T, g.N = I, g.K = H;
   g.out = dgu, g.out2 = h, g.gu = const_cast<float*>(gu);
   int r = launch_ffn_gemm(g, FFN_DH, st);

@@ -6,6 +6,7 @@
 // dx, both sides of a weight gradient): the transposes that a backward pass
 // needs are never written out, they happen on the way from LDS to registers
 // (ds_read_b64_tr_b16).
+#include <algorithm>
 #include <type_traits>
 
 #include "device_util.h"
@@ -179,7 +180,54 @@ __device__ __forceinline__ void store8(uint16_t* p, const float* v) {
   *reinterpret_cast<u32x4_t*>(p) = o;
 }
 
-template <int PRODUCT, class C>
+// g and u of 8 neighbouring outputs, as the forward kept them
+__device__ __forceinline__ void load_kept(const FfnGemm& p, int m, int n, f32x4_t* g, f32x4_t* u) {
+  const f32x4_t* src = reinterpret_cast<const f32x4_t*>(p.gu + (int64_t)m * 2 * p.N + n);
+  g[0] = src[0];
+  g[1] = src[1];
+  u[0] = src[p.N / 4];
+  u[1] = src[p.N / 4 + 1];
+}
+
+// What becomes of 8 neighbouring sums a (gate_up: gate sums a and up sums u;
+// dh: kept g and u in kg and ku).
+template <int PRODUCT>
+__device__ __forceinline__ void finish(const FfnGemm& p, int m, int n, const f32x4_t* a, const f32x4_t* u,
+                                       const f32x4_t* kg, const f32x4_t* ku) {
+  float v[8], w[8], h[8];
+  if (PRODUCT == FFN_GATE_UP) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) h[q] = gate_act<false>(p.act, a[q >> 2][q & 3], nullptr) * u[q >> 2][q & 3];
+    store8(p.out + (int64_t)m * p.N + n, h);
+    if (p.gu) {
+      f32x4_t* dst = reinterpret_cast<f32x4_t*>(p.gu + (int64_t)m * 2 * p.N + n);
+      __builtin_nontemporal_store(a[0], dst);
+      __builtin_nontemporal_store(a[1], dst + 1);
+      __builtin_nontemporal_store(u[0], dst + p.N / 4);
+      __builtin_nontemporal_store(u[1], dst + p.N / 4 + 1);
+    }
+  } else if (PRODUCT == FFN_DH) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float g = kg[q >> 2][q & 3], k = ku[q >> 2][q & 3], dh = a[q >> 2][q & 3];
+      float da;
+      const float act = gate_act<true>(p.act, g, &da);
+      h[q] = act * k;
+      v[q] = dh * k * da;
+      w[q] = dh * act;
+    }
+    store8(p.out + (int64_t)m * 2 * p.N + n, v);
+    store8(p.out + (int64_t)m * 2 * p.N + p.N + n, w);
+    store8(p.out2 + (int64_t)m * p.N + n, h);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = a[q >> 2][q & 3];
+    store8(p.out + (int64_t)m * p.N + n, v);
+  }
+}
+
+// SPLIT: this split's sums go to the slabs.
+template <int PRODUCT, class C, bool SPLIT>
 __global__ __launch_bounds__(C::NT, 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
                                                                                             int nrow) {
   constexpr bool A_KC = PRODUCT != FFN_DW;
@@ -192,14 +240,17 @@ __global__ __launch_bounds__(C::NT, 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
   const int wm = wave / C::WN, wn = wave % C::WN;
 
   // Workgroup i runs on XCD i % 8: each XCD takes a contiguous eighth of the
-  // tiles, in panels of 4 row tiles, column by column, so that the 32 tiles
-  // that an XCD works on at a time share 4 row and 8 column panels in its L2.
+  // tiles (of each K split in turn), in panels of 4 row tiles, column by
+  // column, so that the 32 tiles that an XCD works on at a time share 4 row
+  // and 8 column panels in its L2.
   int t;
   {
-    const int total = ncol * nrow, x = blockIdx.x & 7, j = blockIdx.x >> 3;
+    const int total = ncol * nrow * (SPLIT ? p.splits : 1), x = blockIdx.x & 7, j = blockIdx.x >> 3;
     const int per = total >> 3, rest = total & 7;
     t = x * per + min(x, rest) + j;
   }
+  const int split = SPLIT ? t / (ncol * nrow) : 0;
+  t -= split * (ncol * nrow);
   constexpr int GM = 4;
   const int panel = t / (GM * ncol), in = t - panel * GM * ncol;
   const int gm = min(GM, nrow - panel * GM);
@@ -208,7 +259,10 @@ __global__ __launch_bounds__(C::NT, 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
 
   Operand<A_KC, C::BM, C::NCA, false> A;
   Operand<B_KC, C::BN, C::NCB, GATE> B;
-  const int nst = (p.K + BK - 1) / BK, kfirst = p.K - nst * BK;
+  const int all = (p.K + BK - 1) / BK, kfirst = p.K - all * BK;
+  // this split's stages
+  const int s0 = SPLIT ? (int)((int64_t)all * split / p.splits) : 0;
+  const int nst = SPLIT ? (int)((int64_t)all * (split + 1) / p.splits) : all;
   A.init(A_KC ? p.A + (int64_t)m0 * p.lda : p.A + m0, 0, p.lda, p.M - m0, kfirst, wave);
   B.init(B_KC ? p.B + (int64_t)n0 * p.ldb : p.B + n0, (int64_t)p.N * p.ldb, p.ldb, p.N - n0, kfirst, wave);
 
@@ -257,12 +311,17 @@ __global__ __launch_bounds__(C::NT, 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
   // Every stage runs the same code: the copies behind the last stage bring
   // zeros without touching memory, and the last reads take what is never
   // used (or, where the number of stages is odd, zeros).
-  A.at(0, nst > 0);
-  B.at(0, nst > 0);
-  for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, true>(smem_at, wave, kfirst); });
-  for_each<C::NCB>([&](auto i) { B.template copy<decltype(i)::value, true>(smem_at + C::ABYTES, wave, kfirst); });
-  A.at(1, nst > 1);
-  B.at(1, nst > 1);
+  A.at(s0, s0 < nst);
+  B.at(s0, s0 < nst);
+  if (s0 == 0) {
+    for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, true>(smem_at, wave, kfirst); });
+    for_each<C::NCB>([&](auto i) { B.template copy<decltype(i)::value, true>(smem_at + C::ABYTES, wave, kfirst); });
+  } else {
+    for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, false>(smem_at, wave, 0); });
+    for_each<C::NCB>([&](auto i) { B.template copy<decltype(i)::value, false>(smem_at + C::ABYTES, wave, 0); });
+  }
+  A.at(s0 + 1, s0 + 1 < nst);
+  B.at(s0 + 1, s0 + 1 < nst);
   for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, false>(smem_at + C::STAGE, wave, 0); });
   for_each<C::NCB>(
       [&](auto i) { B.template copy<decltype(i)::value, false>(smem_at + C::STAGE + C::ABYTES, wave, 0); });
@@ -270,7 +329,7 @@ __global__ __launch_bounds__(C::NT, 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
   bare_barrier();
 #pragma unroll
   for (int i = 0; i < NF; ++i) read(0, 0, 0, i);
-  for (int s = 0; s < nst; s += 2) {
+  for (int s = s0; s < nst; s += 2) {
     for_each<2>([&](auto h_c) __attribute__((always_inline)) {
       constexpr int slot = decltype(h_c)::value;
       slice(0, slot, 1, no());
@@ -307,16 +366,12 @@ __global__ __launch_bounds__(C::NT, 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
     constexpr int i = decltype(i_c)::value;
     const int mb = m0 + wm * (C::BM / C::WM) + i * 32 + lane / LPR;
     f32x4_t kg[32 / RPI][2], ku[32 / RPI][2];
-    if (PRODUCT == FFN_DH) {
+    if (PRODUCT == FFN_DH && !SPLIT) {
 #pragma unroll
       for (int r = 0; r < 32 / RPI; ++r) {
         const int m = mb + r * RPI;
         if (m < p.M && n < p.N) {
-          const f32x4_t* src = reinterpret_cast<const f32x4_t*>(p.gu + (int64_t)m * 2 * p.N + n);
-          kg[r][0] = src[0];
-          kg[r][1] = src[1];
-          ku[r][0] = src[p.N / 4];
-          ku[r][1] = src[p.N / 4 + 1];
+          load_kept(p, m, n, kg[r], ku[r]);
         }
       }
     }
@@ -328,69 +383,69 @@ __global__ __launch_bounds__(C::NT, 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
         *reinterpret_cast<f32x4_t*>(mine + l32 * ROWF + j * 32 + 8 * q + 4 * kh) =
             f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     asm volatile("" ::: "memory");  // a wavefront's LDS accesses run in order
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int r = 0; r < 32 / RPI; ++r) {
       const int m = mb + r * RPI;
       if (m >= p.M || n >= p.N) continue;
       const float* row = mine + (r * RPI + lane / LPR) * ROWF;
-      float v[8], w[8], h[8];
-      if (GATE) {
-        // 32-column blocks alternate: gate, up
-        const f32x4_t* src = reinterpret_cast<const f32x4_t*>(row + (oc >> 5) * 64 + (oc & 31));
-        const f32x4_t g0 = src[0], g1 = src[1], u0 = src[8], u1 = src[9];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          h[q] = gate_act<false>(p.act, g0[q], nullptr) * u0[q];
-          h[q + 4] = gate_act<false>(p.act, g1[q], nullptr) * u1[q];
-        }
-        store8(p.out + (int64_t)m * p.N + n, h);
-        if (p.gu) {
-          f32x4_t* dst = reinterpret_cast<f32x4_t*>(p.gu + (int64_t)m * 2 * p.N + n);
-          __builtin_nontemporal_store(g0, dst);
-          __builtin_nontemporal_store(g1, dst + 1);
-          __builtin_nontemporal_store(u0, dst + p.N / 4);
-          __builtin_nontemporal_store(u1, dst + p.N / 4 + 1);
+      // gate_up: 32-column blocks alternate, gate, up
+      const f32x4_t* src = reinterpret_cast<const f32x4_t*>(row + (GATE ? (oc >> 5) * 64 + (oc & 31) : oc));
+      const f32x4_t a[2] = {src[0], src[1]}, u[2] = {src[GATE ? 8 : 0], src[GATE ? 9 : 1]};
+      if constexpr (SPLIT) {
+        constexpr int W = GATE ? 2 : 1;
+        f32x4_t* dst = reinterpret_cast<f32x4_t*>(p.slabs + ((int64_t)split * p.M + m) * (W * p.N) + n);
+        dst[0] = a[0];
+        dst[1] = a[1];
+        if (GATE) {
+          dst[p.N / 4] = u[0];
+          dst[p.N / 4 + 1] = u[1];
         }
       } else {
-        const f32x4_t* src = reinterpret_cast<const f32x4_t*>(row + oc);
-        const f32x4_t a0 = src[0], a1 = src[1];
-        if (PRODUCT == FFN_DH) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float g = kg[r][q >> 2][q & 3], u = ku[r][q >> 2][q & 3], dh = q < 4 ? a0[q & 3] : a1[q & 3];
-            float da;
-            const float a = gate_act<true>(p.act, g, &da);
-            h[q] = a * u;
-            v[q] = dh * u * da;
-            w[q] = dh * a;
-          }
-          store8(p.out + (int64_t)m * 2 * p.N + n, v);
-          store8(p.out + (int64_t)m * 2 * p.N + p.N + n, w);
-          store8(p.out2 + (int64_t)m * p.N + n, h);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            v[q] = a0[q];
-            v[q + 4] = a1[q];
-          }
-          store8(p.out + (int64_t)m * p.N + n, v);
-        }
+        finish<PRODUCT>(p, m, n, a, u, kg[r], ku[r]);
       }
+      __builtin_amdgcn_sched_barrier(0);  // one row's registers at a time
     }
     asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
   });
 }
 
-template <int PRODUCT, class C>
+// Adds the slabs in their order and finishes 8 neighbouring outputs.
+template <int PRODUCT>
+__global__ __launch_bounds__(256) void ffn_join_kernel(FfnGemm p) {
+  constexpr int W = PRODUCT == FFN_GATE_UP ? 2 : 1;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = p.N / 8;
+  if (i >= per * p.M) return;
+  const int m = (int)(i / per), n = (int)(i % per) * 8;
+  f32x4_t kg[2], ku[2];
+  if (PRODUCT == FFN_DH) load_kept(p, m, n, kg, ku);
+  f32x4_t s[W][2];
+  for (int z = 0; z < p.splits; ++z)
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const f32x4_t* src =
+          reinterpret_cast<const f32x4_t*>(p.slabs + ((int64_t)z * p.M + m) * (W * p.N) + w * p.N + n);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) s[w][h] = z ? s[w][h] + src[h] : src[h];
+    }
+  finish<PRODUCT>(p, m, n, s[0], s[W - 1], kg, ku);
+}
+
+template <int PRODUCT, class C, bool SPLIT>
 int launch_cfg(const FfnGemm& g, hipStream_t st) {
   static std::atomic<uint64_t> attr_done;
   constexpr int bn = PRODUCT == FFN_GATE_UP ? C::BN / 2 : C::BN;
-  const int64_t ncol = (g.N + bn - 1) / bn, nrow = (g.M + C::BM - 1) / C::BM;
-  if (ncol * nrow > 0x7fffffff) return MOE_LORA_EUNSUPPORTED;
-  const void* fn = reinterpret_cast<const void*>(&ffn_gemm_kernel<PRODUCT, C>);
+  const int64_t ncol = (g.N + bn - 1) / bn, nrow = (g.M + C::BM - 1) / C::BM, grid = ncol * nrow * g.splits;
+  if (grid > 0x7fffffff) return MOE_LORA_EUNSUPPORTED;
+  const void* fn = reinterpret_cast<const void*>(&ffn_gemm_kernel<PRODUCT, C, SPLIT>);
   const int rc = ensure_dynamic_lds(fn, C::LDS, attr_done);
   if (rc) return rc;
-  ffn_gemm_kernel<PRODUCT, C><<<(unsigned)(ncol * nrow), C::NT, C::LDS, st>>>(g, (int)ncol, (int)nrow);
+  ffn_gemm_kernel<PRODUCT, C, SPLIT><<<(unsigned)grid, C::NT, C::LDS, st>>>(g, (int)ncol, (int)nrow);
+  if (SPLIT) {
+    const int64_t n = (int64_t)g.M * (g.N / 8);
+    ffn_join_kernel<PRODUCT><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g);
+  }
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
@@ -408,13 +463,55 @@ typedef FfnCfg<256, 256, 2, 4> Big;
 // few large ones to fill the chip.
 typedef FfnCfg<128, 128, 2, 2> Small;
 
+// us of a stage and of the rest of a workgroup (first copies, epilogue,
+// launch), fitted to a sweep of sizes
+constexpr double kBigStage = 1.1, kBigFixed = 8., kSmallStage = 0.9, kSmallFixed = 6., kJoinFixed = 5.;
+
+// Tile, and K splits of the small one, by the time that they would take: rounds
+// of workgroups (256 large ones or 512 small ones at a time) times a
+// workgroup's stages and its fixed part, and with splits the slabs' way to
+// memory and back and one more launch.
+struct FfnPlan {
+  bool big;
+  int splits;
+};
+
+FfnPlan plan(int M, int N, int K, FfnProduct product) {
+  const bool gate = product == FFN_GATE_UP;
+  const int64_t stages = std::max(1, (K + BK - 1) / BK), cols = (int64_t)N * (gate ? 2 : 1);
+  FfnPlan best{false, 1};
+  double least = 1e30;
+  for (int big = 0; big < 2; ++big) {
+    const int64_t b = big ? 256 : 128, tiles = ((M + b - 1) / b) * ((cols + b - 1) / b), slots = big ? 256 : 512;
+    const double stage_us = big ? kBigStage : kSmallStage, fixed_us = big ? kBigFixed : kSmallFixed;
+    for (int64_t s = 1; s <= (big ? 1 : 16) && s * 4 <= std::max<int64_t>(4, stages); ++s) {
+      if (s > 1 && tiles * s > 4 * slots) break;
+      const int64_t rounds = (tiles * s + slots - 1) / slots, each = (stages + s - 1) / s;
+      double us = rounds * (each * stage_us + fixed_us);
+      if (s > 1) us += kJoinFixed + s * (double)M * cols * 8 / 4e6;
+      if (us < least) {
+        least = us;
+        best = FfnPlan{big != 0, (int)s};
+      }
+    }
+  }
+  return best;
+}
+
 template <int PRODUCT>
-int launch(const FfnGemm& g, hipStream_t st) {
-  if ((int64_t)g.M * g.N >= 256LL * 256 * 128) return launch_cfg<PRODUCT, Big>(g, st);
-  return launch_cfg<PRODUCT, Small>(g, st);
+int launch(FfnGemm g, hipStream_t st) {
+  const FfnPlan f = plan(g.M, g.N, g.K, (FfnProduct)PRODUCT);
+  g.splits = f.splits;
+  if (f.big) return launch_cfg<PRODUCT, Big, false>(g, st);
+  return f.splits > 1 ? launch_cfg<PRODUCT, Small, true>(g, st) : launch_cfg<PRODUCT, Small, false>(g, st);
 }
 
 }  // namespace
+
+size_t ffn_gemm_slab_bytes(int M, int N, int K, FfnProduct product) {
+  const int s = plan(M, N, K, product).splits;
+  return s > 1 ? (size_t)s * M * N * (product == FFN_GATE_UP ? 2 : 1) * sizeof(float) : 0;
+}
 
 int launch_ffn_gemm(const FfnGemm& g, FfnProduct product, hipStream_t st) {
   if (g.M == 0 || g.N == 0) return MOE_LORA_OK;

@@ -60,9 +60,8 @@ struct Bf16Weights {
 
 }  // namespace
 
-int launch_ffn_rows(const FfnGemm& g, FfnProduct product, const uint16_t* a_lo, uint16_t* out_lo, float* slabs,
-                    hipStream_t st) {
-  const RowsArgs a{g.A, a_lo, g.out, out_lo, g.M, g.N, g.K, g.act, slabs, 1, 0};
+int launch_ffn_rows(const FfnGemm& g, FfnProduct product, const uint16_t* a_lo, uint16_t* out_lo, hipStream_t st) {
+  const RowsArgs a{g.A, a_lo, g.out, out_lo, g.gu, g.M, g.N, g.K, g.act, g.slabs, 1, 0};
   const Bf16Weights::Args wa{g.B};
   if (product == FFN_GATE_UP) launch_rows<Bf16Weights, true, false>(a, wa, st);
   else if (a_lo) launch_rows<Bf16Weights, false, true>(a, wa, st);

@@ -42,6 +42,7 @@ struct RowsArgs {
   const uint16_t* x_lo;  // PAIR: the rows' remainders, the product takes x + x_lo
   uint16_t* out;         // [M][N]
   uint16_t* out_lo;      // gated: the remainder of out's rounding, or NULL
+  float* gu;             // gated: [M][2N], both sums kept, or NULL
   int M, N, K;
   int act;
   float* slabs;          // K split over the grid: [split][M][N] (gated: [split][2][M][N]), or NULL
@@ -53,6 +54,10 @@ __device__ __forceinline__ void rows_store(const RowsArgs& p, bool gated, int m,
   const float r = gated ? gate_act<false>(p.act, a, nullptr) * u : a;
   const uint16_t hi = f32_to_bf16(r);
   p.out[(int64_t)m * p.N + n] = hi;
+  if (gated && p.gu) {
+    p.gu[(int64_t)m * 2 * p.N + n] = a;
+    p.gu[(int64_t)m * 2 * p.N + p.N + n] = u;
+  }
   if (gated && p.out_lo) p.out_lo[(int64_t)m * p.N + n] = f32_to_bf16(r - bf16_to_f32(hi));
 }
 

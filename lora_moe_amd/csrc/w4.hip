@@ -273,7 +273,7 @@ int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, void*
   const Range in[] = {{x, (size_t)M * L.K * 2}, {w->data, L.total}};
   const Range out[] = {{y, (size_t)M * L.N * 2}, {workspace, need}};
   if (any_overlap(in, 2, out, 2)) return MOE_LORA_EINVAL;
-  launch_product(RowsArgs{x, nullptr, y, nullptr, M, L.N, L.K, 0, (float*)workspace, 1, 0}, L, w->data, nullptr, (hipStream_t)stream);
+  launch_product(RowsArgs{x, nullptr, y, nullptr, nullptr, M, L.N, L.K, 0, (float*)workspace, 1, 0}, L, w->data, nullptr, (hipStream_t)stream);
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
@@ -312,8 +312,8 @@ int moe_lora_w4_ffn_forward(const moe_lora_w4* gate, const moe_lora_w4* up, cons
   uint16_t* h = (uint16_t*)workspace;
   uint16_t* h_lo = M <= kPairRows ? (uint16_t*)((char*)workspace + round256((size_t)M * Ld.K * 2)) : nullptr;
   float* slabs = (float*)((char*)workspace + ffn_h_bytes(M, Ld.K));
-  launch_product(RowsArgs{x, nullptr, h, h_lo, M, Lg.N, Lg.K, act, slabs, 1, 0}, Lg, gate->data, up->data, st);
-  launch_product(RowsArgs{h, h_lo, y, nullptr, M, Ld.N, Ld.K, 0, slabs, 1, 0}, Ld, down->data, nullptr, st);
+  launch_product(RowsArgs{x, nullptr, h, h_lo, nullptr, M, Lg.N, Lg.K, act, slabs, 1, 0}, Lg, gate->data, up->data, st);
+  launch_product(RowsArgs{h, h_lo, y, nullptr, nullptr, M, Ld.N, Ld.K, 0, slabs, 1, 0}, Ld, down->data, nullptr, st);
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
