@@ -30,6 +30,9 @@ struct FfnGemm {
   uint16_t* out2;    // DH: h
   float* gu;         // GATE_UP: kept pre-activations [M][2N] or NULL; DH: read
   int act;
+  int pair;          // DH: dgu and h get their remainders as rows M..2M-1; DX: A is such a pair (rows M..2M-1,
+                     // added to rows 0..M-1 of the product); DW: A or B is one (K = 2 tokens, see wrap)
+  int wrap_a, wrap_b;  // DW of a pair: k from here on meets the side's rows from 0 again (0: no pair); K <= 64
   float* slabs;      // scratch of ffn_gemm_slab_bytes
   int splits;        // K splits, set by the launch
 };
@@ -37,8 +40,11 @@ struct FfnGemm {
 // Up to this many tokens a forward streams the weights (ffn_rows.hip); beyond
 // it the rows' side takes over and tiles are better.
 constexpr int kRowsMax = 64;
-// Up to this many, h goes from one product to the other as a bf16 pair hi +
-// lo, which costs nothing beside the weights.
+// Up to this many, h, dg and du go from one product to the next as bf16 pairs
+// hi + lo, which costs nothing beside the weights.  With so few tokens a few
+// large values carry a result, so that one rounding more than its own can
+// show by more than its share (in 64-bit emulations of 1 to 3 tokens up to
+// 1.68 times a single rounding's error, from 17 on at most 1.48).
 constexpr int kRowsPair = 16;
 
 // FFN_GATE_UP or FFN_DOWN of at most kRowsMax rows.  a_lo: the remainder of A
@@ -47,8 +53,9 @@ constexpr int kRowsPair = 16;
 int launch_ffn_rows(const FfnGemm& g, FfnProduct product, const uint16_t* a_lo, uint16_t* out_lo, hipStream_t st);
 size_t ffn_rows_slab_bytes(int T, int H, int I);
 
-// Bytes of scratch that a product of these sizes needs (0 where K is not split).
-size_t ffn_gemm_slab_bytes(int M, int N, int K, FfnProduct product);
+// Bytes of scratch that a product of these sizes needs (0 where K is not split
+// and A is no pair).
+size_t ffn_gemm_slab_bytes(int M, int N, int K, FfnProduct product, bool pair = false);
 
 int launch_ffn_gemm(const FfnGemm& g, FfnProduct product, hipStream_t st);
 

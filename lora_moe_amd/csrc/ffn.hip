@@ -36,20 +36,24 @@ struct Sizes {  // bytes
   }
 };
 
-// forward: h (up to kRowsPair tokens its remainder too), slabs; backward: h,
-// dgu, slabs
-size_t forward_fixed(const moe_lora_ffn_shape& s) { return round256(Sizes(s).h) * (s.T <= kRowsPair ? 2 : 1); }
-size_t backward_fixed(const moe_lora_ffn_shape& s) { return round256(Sizes(s).h) + round256(Sizes(s).dgu); }
+// forward: h, slabs; backward: h, dgu, slabs; up to kRowsPair tokens h and
+// dgu with their remainders, of as many rows, right behind them
+size_t h_bytes(const moe_lora_ffn_shape& s) { return round256(Sizes(s).h * (s.T <= kRowsPair ? 2 : 1)); }
+size_t backward_fixed(const moe_lora_ffn_shape& s) {
+  return h_bytes(s) + round256(Sizes(s).dgu * (s.T <= kRowsPair ? 2 : 1));
+}
 
 size_t ws_bytes_of(const moe_lora_ffn_shape& s, bool backward) {
   const int T = s.T, H = s.H, I = s.I;
   const size_t slabs = T <= kRowsMax ? ffn_rows_slab_bytes(T, H, I)
                                      : std::max(ffn_gemm_slab_bytes(T, I, H, FFN_GATE_UP),
                                                 ffn_gemm_slab_bytes(T, H, I, FFN_DOWN));
-  const size_t forward = forward_fixed(s) + round256(slabs);
+  const size_t forward = h_bytes(s) + round256(slabs);
   if (!backward) return forward;
-  const size_t back = std::max({ffn_gemm_slab_bytes(T, I, H, FFN_DH), ffn_gemm_slab_bytes(T, H, 2 * I, FFN_DX),
-                                ffn_gemm_slab_bytes(2 * I, H, T, FFN_DW), ffn_gemm_slab_bytes(H, I, T, FFN_DW)});
+  const bool pair = T <= kRowsPair;
+  const int k = pair ? 2 * T : T;
+  const size_t back = std::max({ffn_gemm_slab_bytes(T, I, H, FFN_DH), ffn_gemm_slab_bytes(T, H, 2 * I, FFN_DX, pair),
+                                ffn_gemm_slab_bytes(2 * I, H, k, FFN_DW), ffn_gemm_slab_bytes(H, I, k, FFN_DW)});
   return std::max(forward, backward_fixed(s) + round256(back));
 }
 
@@ -86,9 +90,9 @@ int moe_lora_ffn_forward(const moe_lora_ffn_shape* shape, const uint16_t* x, con
   FfnGemm g = {};
   g.act = shape->act;
   g.A = x, g.lda = H, g.B = W_gu, g.ldb = H, g.M = T, g.N = I, g.K = H, g.out = h, g.gu = gu;
-  g.slabs = (float*)((char*)workspace + forward_fixed(*shape));
+  g.slabs = (float*)((char*)workspace + h_bytes(*shape));
   if (T <= kRowsMax) {
-    uint16_t* h_lo = T <= kRowsPair ? (uint16_t*)((char*)workspace + round256(z.h)) : nullptr;
+    uint16_t* h_lo = T <= kRowsPair ? h + (size_t)T * I : nullptr;
     const int r = launch_ffn_rows(g, FFN_GATE_UP, nullptr, h_lo, st);
     if (r) return r;
     g.A = h, g.lda = I, g.B = W_down, g.ldb = I, g.N = H, g.K = I, g.out = y, g.gu = nullptr;
@@ -124,12 +128,12 @@ int moe_lora_ffn_backward(const moe_lora_ffn_shape* shape, const uint16_t* dy, c
   if (any_overlap(in, 5, out, 4)) return MOE_LORA_EINVAL;
   hipStream_t st = (hipStream_t)stream;
   uint16_t* h = (uint16_t*)workspace;
-  uint16_t* dgu = (uint16_t*)((char*)workspace + round256(z.h));
+  uint16_t* dgu = (uint16_t*)((char*)workspace + h_bytes(*shape));
   FfnGemm g = {};
   g.act = shape->act;
   g.slabs = (float*)((char*)workspace + backward_fixed(*shape));
   g.A = dy, g.lda = H, g.B = W_down, g.ldb = I, g.M = T, g.N = I, g.K = H;
-  g.out = dgu, g.out2 = h, g.gu = const_cast<float*>(gu);
+  g.out = dgu, g.out2 = h, g.gu = const_cast<float*>(gu), g.pair = T <= kRowsPair;
   int r = launch_ffn_gemm(g, FFN_DH, st);
   if (r) return r;
   g.gu = nullptr, g.out2 = nullptr;
@@ -137,12 +141,16 @@ int moe_lora_ffn_backward(const moe_lora_ffn_shape* shape, const uint16_t* dy, c
     g.A = dgu, g.lda = 2 * (int64_t)I, g.B = W_gu, g.ldb = H, g.M = T, g.N = H, g.K = 2 * I, g.out = dx;
     if ((r = launch_ffn_gemm(g, FFN_DX, st))) return r;
   }
+  // the pair's remainders are further tokens of the sums, with the same x or dy
+  const int K = g.pair ? 2 * T : T;
   if (dW_gu) {
-    g.A = dgu, g.lda = 2 * (int64_t)I, g.B = x, g.ldb = H, g.M = 2 * I, g.N = H, g.K = T, g.out = dW_gu;
+    g.A = dgu, g.lda = 2 * (int64_t)I, g.B = x, g.ldb = H, g.M = 2 * I, g.N = H, g.K = K, g.out = dW_gu;
+    g.wrap_a = 0, g.wrap_b = g.pair ? T : 0;
     if ((r = launch_ffn_gemm(g, FFN_DW, st))) return r;
   }
   if (dW_down) {
-    g.A = dy, g.lda = H, g.B = h, g.ldb = I, g.M = H, g.N = I, g.K = T, g.out = dW_down;
+    g.A = dy, g.lda = H, g.B = h, g.ldb = I, g.M = H, g.N = I, g.K = K, g.out = dW_down;
+    g.wrap_a = g.pair ? T : 0, g.wrap_b = 0;
     if ((r = launch_ffn_gemm(g, FFN_DW, st))) return r;
   }
   return MOE_LORA_OK;

@@ -52,6 +52,7 @@ struct FfnCfg {
   static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;  // 32 x 32 blocks of a wavefront
   static constexpr int ABYTES = BM * BK * 2, BBYTES = BN * BK * 2, STAGE = ABYTES + BBYTES;
   static constexpr int LDS = 2 * STAGE;
+  static constexpr int LDS_ONE = std::max(STAGE, NW * 32 * (BN / WN + 4) * 4);  // one stage, or the epilogue's rows
   static constexpr int NCA = ABYTES / 1024 / NW, NCB = BBYTES / 1024 / NW;  // 1 KB copies per wavefront and stage
 };
 
@@ -90,9 +91,10 @@ struct Operand {
   uint32_t soff;
 
   // p: the tile's first output at k = 0; rows_left: outputs from there on;
-  // kfirst: stage 0's first k, in (-64, 0]
+  // kfirst: stage 0's first k, in (-64, 0]; wrap (else 0; one stage): k from
+  // there on are rows 0.. again
   __device__ __forceinline__ void init(const uint16_t* p, int64_t odd_, int64_t ld_, int rows_left, int kfirst,
-                                       int wave) {
+                                       int wave, int wrap) {
     base = p + kfirst * (KC ? (int64_t)1 : ld_);
     odd = odd_;
     ld = ld_;
@@ -110,7 +112,8 @@ struct Operand {
         constexpr int PER = 1024 / (ROWS * 2), LPR = ROWS / 8;  // k rows per copy, lanes per row
         const int k = c * PER + lane / LPR;
         const int ch = (lane % LPR) ^ (4 * (k & 3));
-        off[i] = ch * 8 < rows_left ? (uint32_t)(k * (int)ld + ch * 8) * 2u : kBufNone;
+        const int r = wrap && k + kfirst >= wrap ? k - wrap : k;
+        off[i] = ch * 8 < rows_left ? (uint32_t)(r * (int)ld + ch * 8) * 2u : kBufNone;
       }
     }
   }
@@ -180,6 +183,13 @@ __device__ __forceinline__ void store8(uint16_t* p, const float* v) {
   *reinterpret_cast<u32x4_t*>(p) = o;
 }
 
+// what rounding to bf16 takes off (in place)
+__device__ __forceinline__ const float* remainder8(float* v) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] -= bf16_to_f32(f32_to_bf16(v[i]));
+  return v;
+}
+
 // g and u of 8 neighbouring outputs, as the forward kept them
 __device__ __forceinline__ void load_kept(const FfnGemm& p, int m, int n, f32x4_t* g, f32x4_t* u) {
   const f32x4_t* src = reinterpret_cast<const f32x4_t*>(p.gu + (int64_t)m * 2 * p.N + n);
@@ -219,6 +229,12 @@ __device__ __forceinline__ void finish(const FfnGemm& p, int m, int n, const f32
     store8(p.out + (int64_t)m * 2 * p.N + n, v);
     store8(p.out + (int64_t)m * 2 * p.N + p.N + n, w);
     store8(p.out2 + (int64_t)m * p.N + n, h);
+    if (p.pair) {
+      const int64_t lo = m + p.M;
+      store8(p.out + lo * 2 * p.N + n, remainder8(v));
+      store8(p.out + lo * 2 * p.N + p.N + n, remainder8(w));
+      store8(p.out2 + lo * p.N + n, remainder8(h));
+    }
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] = a[q >> 2][q & 3];
@@ -226,9 +242,13 @@ __device__ __forceinline__ void finish(const FfnGemm& p, int m, int n, const f32
   }
 }
 
-// SPLIT: this split's sums go to the slabs.
-template <int PRODUCT, class C, bool SPLIT>
-__global__ __launch_bounds__(C::NT, 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
+// SPLIT: this split's sums go to the slabs.  ONE: K is one stage, and the ring
+// that single stage, so that twice as many workgroups share a CU: a weight
+// gradient of few tokens is bound by its own stores and by how many tiles'
+// first copies are in flight (22016 x 4096 of 64 tokens: XXX us so, 79
+// without).
+template <int PRODUCT, class C, bool SPLIT, bool ONE>
+__global__ __launch_bounds__(C::NT, ONE ? 4 : 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
                                                                                             int nrow) {
   constexpr bool A_KC = PRODUCT != FFN_DW;
   constexpr bool B_KC = PRODUCT == FFN_GATE_UP || PRODUCT == FFN_DOWN;
@@ -257,14 +277,16 @@ __global__ __launch_bounds__(C::NT, 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
   const int tn = in / gm, tm = panel * GM + in - tn * gm;
   const int m0 = tm * C::BM, n0 = tn * (GATE ? C::BN / 2 : C::BN);
 
+  const int rows = PRODUCT == FFN_DX && p.pair ? 2 * p.M : p.M;  // of A
   Operand<A_KC, C::BM, C::NCA, false> A;
   Operand<B_KC, C::BN, C::NCB, GATE> B;
   const int all = (p.K + BK - 1) / BK, kfirst = p.K - all * BK;
   // this split's stages
   const int s0 = SPLIT ? (int)((int64_t)all * split / p.splits) : 0;
   const int nst = SPLIT ? (int)((int64_t)all * (split + 1) / p.splits) : all;
-  A.init(A_KC ? p.A + (int64_t)m0 * p.lda : p.A + m0, 0, p.lda, p.M - m0, kfirst, wave);
-  B.init(B_KC ? p.B + (int64_t)n0 * p.ldb : p.B + n0, (int64_t)p.N * p.ldb, p.ldb, p.N - n0, kfirst, wave);
+  A.init(A_KC ? p.A + (int64_t)m0 * p.lda : p.A + m0, 0, p.lda, rows - m0, kfirst, wave, PRODUCT == FFN_DW ? p.wrap_a : 0);
+  B.init(B_KC ? p.B + (int64_t)n0 * p.ldb : p.B + n0, (int64_t)p.N * p.ldb, p.ldb, p.N - n0, kfirst, wave,
+         PRODUCT == FFN_DW ? p.wrap_b : 0);
 
   f32x16_t acc[MI][NI];
 #pragma unroll
@@ -320,28 +342,37 @@ __global__ __launch_bounds__(C::NT, 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
     for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, false>(smem_at, wave, 0); });
     for_each<C::NCB>([&](auto i) { B.template copy<decltype(i)::value, false>(smem_at + C::ABYTES, wave, 0); });
   }
-  A.at(s0 + 1, s0 + 1 < nst);
-  B.at(s0 + 1, s0 + 1 < nst);
-  for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, false>(smem_at + C::STAGE, wave, 0); });
-  for_each<C::NCB>(
-      [&](auto i) { B.template copy<decltype(i)::value, false>(smem_at + C::STAGE + C::ABYTES, wave, 0); });
+  if constexpr (!ONE) {
+    A.at(s0 + 1, s0 + 1 < nst);
+    B.at(s0 + 1, s0 + 1 < nst);
+    for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, false>(smem_at + C::STAGE, wave, 0); });
+    for_each<C::NCB>(
+        [&](auto i) { B.template copy<decltype(i)::value, false>(smem_at + C::STAGE + C::ABYTES, wave, 0); });
+  }
   __builtin_amdgcn_s_waitcnt(wait_vm0);
   bare_barrier();
 #pragma unroll
   for (int i = 0; i < NF; ++i) read(0, 0, 0, i);
-  for (int s = s0; s < nst; s += 2) {
-    for_each<2>([&](auto h_c) __attribute__((always_inline)) {
-      constexpr int slot = decltype(h_c)::value;
-      slice(0, slot, 1, no());
-      slice(1, slot, 2, no());
-      A.at(s + slot + 2, s + slot + 2 < nst);
-      B.at(s + slot + 2, s + slot + 2 < nst);
-      slice(0, slot, 3, no());
-      // own copies of the next stage have landed, own reads of this one are done
-      __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);
-      bare_barrier();
-      slice(1, slot ^ 1, 0, yes());
-    });
+  if constexpr (ONE) {
+    slice(0, 0, 1, no());
+    slice(1, 0, 2, no());
+    slice(0, 0, 3, no());
+    slice(1, 0, 0, no());
+  } else {
+    for (int s = s0; s < nst; s += 2) {
+      for_each<2>([&](auto h_c) __attribute__((always_inline)) {
+        constexpr int slot = decltype(h_c)::value;
+        slice(0, slot, 1, no());
+        slice(1, slot, 2, no());
+        A.at(s + slot + 2, s + slot + 2 < nst);
+        B.at(s + slot + 2, s + slot + 2 < nst);
+        slice(0, slot, 3, no());
+        // own copies of the next stage have landed, own reads of this one are done
+        __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);
+        bare_barrier();
+        slice(1, slot ^ 1, 0, yes());
+      });
+    }
   }
   __builtin_amdgcn_s_waitcnt(wait_vm0);  // no copy outlives the workgroup
 
@@ -357,7 +388,7 @@ __global__ __launch_bounds__(C::NT, 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
   constexpr int OUT = GATE ? WC / 2 : WC;    // its outputs per row
   constexpr int LPR = OUT / 8, RPI = 64 / LPR;  // lanes per row, rows per step
   float* mine = reinterpret_cast<float*>(smem) + wave * 32 * ROWF;
-  static_assert(C::NW * 32 * ROWF * 4 <= C::LDS, "staged rows must fit the ring");
+  static_assert(C::NW * 32 * ROWF * 4 <= (ONE ? C::LDS_ONE : C::LDS), "staged rows must fit the ring");
   bare_barrier();
   const int l32 = lane & 31, kh = lane >> 5;
   const int oc = (lane % LPR) * 8;           // first of this lane's outputs in the wavefront's columns
@@ -387,14 +418,14 @@ __global__ __launch_bounds__(C::NT, 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
 #pragma unroll
     for (int r = 0; r < 32 / RPI; ++r) {
       const int m = mb + r * RPI;
-      if (m >= p.M || n >= p.N) continue;
+      if (m >= (SPLIT ? rows : p.M) || n >= p.N) continue;
       const float* row = mine + (r * RPI + lane / LPR) * ROWF;
       // gate_up: 32-column blocks alternate, gate, up
       const f32x4_t* src = reinterpret_cast<const f32x4_t*>(row + (GATE ? (oc >> 5) * 64 + (oc & 31) : oc));
       const f32x4_t a[2] = {src[0], src[1]}, u[2] = {src[GATE ? 8 : 0], src[GATE ? 9 : 1]};
       if constexpr (SPLIT) {
         constexpr int W = GATE ? 2 : 1;
-        f32x4_t* dst = reinterpret_cast<f32x4_t*>(p.slabs + ((int64_t)split * p.M + m) * (W * p.N) + n);
+        f32x4_t* dst = reinterpret_cast<f32x4_t*>(p.slabs + ((int64_t)split * rows + m) * (W * p.N) + n);
         dst[0] = a[0];
         dst[1] = a[1];
         if (GATE) {
@@ -411,17 +442,19 @@ __global__ __launch_bounds__(C::NT, 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
   });
 }
 
-// Adds the slabs in their order and finishes 8 neighbouring outputs.
+// Adds the slabs in their order and finishes 8 neighbouring outputs.  DX of a
+// pair: a row's remainder is row M + m of the slabs.
 template <int PRODUCT>
 __global__ __launch_bounds__(256) void ffn_join_kernel(FfnGemm p) {
   constexpr int W = PRODUCT == FFN_GATE_UP ? 2 : 1;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = p.N / 8;
   if (i >= per * p.M) return;
   const int m = (int)(i / per), n = (int)(i % per) * 8;
+  const int halves = PRODUCT == FFN_DX && p.pair ? 2 : 1;
   f32x4_t kg[2], ku[2];
   if (PRODUCT == FFN_DH) load_kept(p, m, n, kg, ku);
   f32x4_t s[W][2];
-  for (int z = 0; z < p.splits; ++z)
+  for (int z = 0; z < p.splits * halves; ++z)
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       const f32x4_t* src =
@@ -432,16 +465,18 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(FfnGemm p) {
   finish<PRODUCT>(p, m, n, s[0], s[W - 1], kg, ku);
 }
 
-template <int PRODUCT, class C, bool SPLIT>
+template <int PRODUCT, class C, bool SPLIT, bool ONE = false>
 int launch_cfg(const FfnGemm& g, hipStream_t st) {
   static std::atomic<uint64_t> attr_done;
   constexpr int bn = PRODUCT == FFN_GATE_UP ? C::BN / 2 : C::BN;
-  const int64_t ncol = (g.N + bn - 1) / bn, nrow = (g.M + C::BM - 1) / C::BM, grid = ncol * nrow * g.splits;
+  constexpr int lds = ONE ? C::LDS_ONE : C::LDS;
+  const int rows = PRODUCT == FFN_DX && g.pair ? 2 * g.M : g.M;
+  const int64_t ncol = (g.N + bn - 1) / bn, nrow = (rows + C::BM - 1) / C::BM, grid = ncol * nrow * g.splits;
   if (grid > 0x7fffffff) return MOE_LORA_EUNSUPPORTED;
-  const void* fn = reinterpret_cast<const void*>(&ffn_gemm_kernel<PRODUCT, C, SPLIT>);
-  const int rc = ensure_dynamic_lds(fn, C::LDS, attr_done);
+  const void* fn = reinterpret_cast<const void*>(&ffn_gemm_kernel<PRODUCT, C, SPLIT, ONE>);
+  const int rc = ensure_dynamic_lds(fn, lds, attr_done);
   if (rc) return rc;
-  ffn_gemm_kernel<PRODUCT, C, SPLIT><<<(unsigned)grid, C::NT, C::LDS, st>>>(g, (int)ncol, (int)nrow);
+  ffn_gemm_kernel<PRODUCT, C, SPLIT, ONE><<<(unsigned)grid, C::NT, lds, st>>>(g, (int)ncol, (int)nrow);
   if (SPLIT) {
     const int64_t n = (int64_t)g.M * (g.N / 8);
     ffn_join_kernel<PRODUCT><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g);
@@ -463,36 +498,32 @@ typedef FfnCfg<256, 256, 2, 4> Big;
 // few large ones to fill the chip.
 typedef FfnCfg<128, 128, 2, 2> Small;
 
-// us of a stage and of the rest of a workgroup (first copies, epilogue,
-// launch), fitted to a sweep of sizes
-constexpr double kBigStage = 1.1, kBigFixed = 8., kSmallStage = 0.9, kSmallFixed = 6., kJoinFixed = 5.;
-
-// Tile, and K splits of the small one, by the time that they would take: rounds
-// of workgroups (256 large ones or 512 small ones at a time) times a
-// workgroup's stages and its fixed part, and with splits the slabs' way to
-// memory and back and one more launch.
+// Tile, and K splits of the small one, by the time that they would take: full
+// rounds of workgroups (256 large ones, or 512 small ones, two to a CU) and
+// their stages; a last round of small ones with a CU each is shorter; splits
+// cost a launch and the slabs' way to memory and back.  The constants (us)
+// are fitted to 1272 measured products of 65 to 2047 tokens, H 1024 to 5120,
+// I 2816 to 11008: the choice is 2 % above the best one on the mean.
 struct FfnPlan {
   bool big;
   int splits;
 };
 
 FfnPlan plan(int M, int N, int K, FfnProduct product) {
-  const bool gate = product == FFN_GATE_UP;
-  const int64_t stages = std::max(1, (K + BK - 1) / BK), cols = (int64_t)N * (gate ? 2 : 1);
-  FfnPlan best{false, 1};
-  double least = 1e30;
-  for (int big = 0; big < 2; ++big) {
-    const int64_t b = big ? 256 : 128, tiles = ((M + b - 1) / b) * ((cols + b - 1) / b), slots = big ? 256 : 512;
-    const double stage_us = big ? kBigStage : kSmallStage, fixed_us = big ? kBigFixed : kSmallFixed;
-    for (int64_t s = 1; s <= (big ? 1 : 16) && s * 4 <= std::max<int64_t>(4, stages); ++s) {
-      if (s > 1 && tiles * s > 4 * slots) break;
-      const int64_t rounds = (tiles * s + slots - 1) / slots, each = (stages + s - 1) / s;
-      double us = rounds * (each * stage_us + fixed_us);
-      if (s > 1) us += kJoinFixed + s * (double)M * cols * 8 / 4e6;
-      if (us < least) {
-        least = us;
-        best = FfnPlan{big != 0, (int)s};
-      }
+  const int64_t stages = std::max(1, (K + BK - 1) / BK), cols = (int64_t)N * (product == FFN_GATE_UP ? 2 : 1);
+  FfnPlan best{true, 1};
+  int64_t tiles = (int64_t)((M + 255) / 256) * ((cols + 255) / 256);
+  double least = (double)((tiles + 255) / 256) * (stages * 1.19 + 4.0);
+  tiles = (int64_t)((M + 127) / 128) * ((cols + 127) / 128);
+  for (int64_t s = 1; s <= 16 && s * 3 <= std::max<int64_t>(3, stages); ++s) {
+    if (s > 1 && tiles * s > 2048) break;
+    const int64_t each = (stages + s - 1) / s, full = tiles * s / 512, rest = tiles * s % 512;
+    const double round_us = each * 0.81 + 0.8;
+    double us = (full + (rest > 256)) * round_us + (rest > 0 && rest <= 256 ? each * 0.57 : 0.);
+    if (s > 1) us += 3.5 + s * (double)M * cols * 8 * 0.16e-6;
+    if (us < least) {
+      least = us;
+      best = FfnPlan{false, (int)s};
     }
   }
   return best;
@@ -500,17 +531,21 @@ FfnPlan plan(int M, int N, int K, FfnProduct product) {
 
 template <int PRODUCT>
 int launch(FfnGemm g, hipStream_t st) {
-  const FfnPlan f = plan(g.M, g.N, g.K, (FfnProduct)PRODUCT);
+  g.splits = 1;
+  if constexpr (PRODUCT == FFN_DW)
+    if (g.K <= BK) return launch_cfg<PRODUCT, Small, false, true>(g, st);
+  const bool pair = PRODUCT == FFN_DX && g.pair;
+  const FfnPlan f = plan(pair ? 2 * g.M : g.M, g.N, g.K, (FfnProduct)PRODUCT);
   g.splits = f.splits;
-  if (f.big) return launch_cfg<PRODUCT, Big, false>(g, st);
-  return f.splits > 1 ? launch_cfg<PRODUCT, Small, true>(g, st) : launch_cfg<PRODUCT, Small, false>(g, st);
+  if (pair || f.splits > 1) return launch_cfg<PRODUCT, Small, true>(g, st);
+  return f.big ? launch_cfg<PRODUCT, Big, false>(g, st) : launch_cfg<PRODUCT, Small, false>(g, st);
 }
 
 }  // namespace
 
-size_t ffn_gemm_slab_bytes(int M, int N, int K, FfnProduct product) {
-  const int s = plan(M, N, K, product).splits;
-  return s > 1 ? (size_t)s * M * N * (product == FFN_GATE_UP ? 2 : 1) * sizeof(float) : 0;
+size_t ffn_gemm_slab_bytes(int M, int N, int K, FfnProduct product, bool pair) {
+  const int s = plan(pair ? 2 * M : M, N, K, product).splits;
+  return s > 1 || pair ? (size_t)s * M * N * (product == FFN_GATE_UP || pair ? 2 : 1) * sizeof(float) : 0;
 }
 
 int launch_ffn_gemm(const FfnGemm& g, FfnProduct product, hipStream_t st) {

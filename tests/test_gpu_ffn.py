@@ -8,9 +8,9 @@ from dense_common import HALF_BF16, act64, ffn64, ffn_backward_bounds, ffn_bound
 pytestmark = pytest.mark.gpu
 
 
-def check_l2(l2, n, terms, what):
-    """The relative L2 error of a result with two independent roundings to
-    bf16 (of the summands and of the sum): each is at most 2^-8 / sqrt(3) of
+def check_l2(l2, n, terms, what, roundings=2):
+    """The relative L2 error of a result with one or two independent roundings
+    to bf16 (of the sum, and of the summands): each is at most 2^-8 / sqrt(3) of
     the value in the mean square (uniform within half a step), 1.3 for the
     spread.  It is a mean: over few elements or few summands a single result
     may err by its worst case, 2^-8 (1 + sum |terms| / |sum|), which passes
@@ -18,7 +18,7 @@ def check_l2(l2, n, terms, what):
     asked of 4096 elements of 64 terms on; the bound per element holds
     everywhere."""
     if n >= 4096 and terms >= 64:
-        assert l2 <= 1.3 * HALF_BF16 * (2 / 3) ** 0.5, (what, l2)
+        assert l2 <= 1.3 * HALF_BF16 * (roundings / 3) ** 0.5, (what, l2)
 
 
 def forward(lm, x, W_gu, W_down, act, keep=False, ws=None, stream=None):
@@ -66,7 +66,11 @@ def test_block(T, H, I, act):
     want = ffn_backward_bounds(dy.double(), x.double(), gu.double().cpu(), W_gu.double(), W_down.double(), act)
     for n, (v, e) in want.items():
         l2 = within(got[n], v, e, f"{what} {n}")
-        check_l2(l2, got[n].numel(), 2 * I if n == "dx" else T, f"{what} {n}")
+        # up to 16 tokens the summands carry their remainders, whatever their number
+        if T <= 16:
+            check_l2(l2, got[n].numel(), 64, f"{what} {n}", 1)
+        else:
+            check_l2(l2, got[n].numel(), 2 * I if n == "dx" else T, f"{what} {n}")
     again = gradients(lm, shape, ws, dyd, dx_, gu, dg_, dd_)
     for n in got:
         assert torch.equal(got[n], again[n]), n  # the same bits every time
