@@ -502,8 +502,8 @@ typedef FfnCfg<128, 128, 2, 2> Small;
 // rounds of workgroups (256 large ones, or 512 small ones, two to a CU) and
 // their stages; a last round of small ones with a CU each is shorter; splits
 // cost a launch and the slabs' way to memory and back.  The constants (us)
-// are fitted to 1272 measured products of 65 to 2047 tokens, H 1024 to 5120,
-// I 2816 to 11008: the choice is 2 % above the best one on the mean.
+// are fitted to 2200 measured products of 65 to 8192 tokens, H 1024 to 5120,
+// I 2816 to 25600: the choice is 1.6 % above the best one on the mean.
 struct FfnPlan {
   bool big;
   int splits;
@@ -516,7 +516,7 @@ FfnPlan plan(int M, int N, int K, FfnProduct product) {
   double least = (double)((tiles + 255) / 256) * (stages * 1.19 + 4.0);
   tiles = (int64_t)((M + 127) / 128) * ((cols + 127) / 128);
   for (int64_t s = 1; s <= 16 && s * 3 <= std::max<int64_t>(3, stages); ++s) {
-    if (s > 1 && tiles * s > 2048) break;
+    if (s > 1 && (tiles > 512 || tiles * s > 2048)) break;  // less than a round to begin with
     const int64_t each = (stages + s - 1) / s, full = tiles * s / 512, rest = tiles * s % 512;
     const double round_us = each * 0.81 + 0.8;
     double us = (full + (rest > 256)) * round_us + (rest > 0 && rest <= 256 ? each * 0.57 : 0.);
