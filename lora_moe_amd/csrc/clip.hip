@@ -95,7 +95,7 @@ struct Piece {
         q[i] = __float_as_uint(v[i] * c);
       } else {
         const float a = v[2 * i % N] * c, b = v[(2 * i + 1) % N] * c;
-        q[i] = DT == MOE_LORA_BF16 ? f32_to_bf16(a) | (uint32_t)f32_to_bf16(b) << 16
+        q[i] = DT == MOE_LORA_BF16 ? f32x2_to_bf16(a, b)
                                    : f32_to_f16(a) | (uint32_t)f32_to_f16(b) << 16;
       }
     }

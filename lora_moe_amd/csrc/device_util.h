@@ -23,6 +23,14 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) {
   return (uint16_t)(u >> 16);
 }
 
+// Two fp32 -> bf16 bits at once, a in the low half, round to nearest even (one
+// instruction of gfx950's).
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t f32x2_to_bf16(float a, float b) {
+  const bf16x2_t v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
 // D(16x16, fp32) += A(16x32, bf16) * B(32x16, bf16) on one wavefront.
 // Lane l supplies A[m = l%16][k = 8*(l/16) .. +8] and B[k = 8*(l/16) .. +8][n = l%16];
 // it receives D[m = 4*(l/16) + i][n = l%16], i = 0..3.  Only the pairing of

@@ -179,14 +179,18 @@ __device__ __forceinline__ void bare_barrier() {
 __device__ __forceinline__ void store8(uint16_t* p, const float* v) {
   u32x4_t o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = f32_to_bf16(v[2 * i]) | ((uint32_t)f32_to_bf16(v[2 * i + 1]) << 16);
+  for (int i = 0; i < 4; ++i) o[i] = f32x2_to_bf16(v[2 * i], v[2 * i + 1]);
   *reinterpret_cast<u32x4_t*>(p) = o;
 }
 
 // what rounding to bf16 takes off (in place)
 __device__ __forceinline__ const float* remainder8(float* v) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] -= bf16_to_f32(f32_to_bf16(v[i]));
+  for (int i = 0; i < 8; i += 2) {
+    const uint32_t r = f32x2_to_bf16(v[i], v[i + 1]);
+    v[i] -= bf16_lo(r);
+    v[i + 1] -= bf16_hi(r);
+  }
   return v;
 }
 
@@ -393,32 +397,28 @@ __global__ __launch_bounds__(C::NT, ONE ? 4 : 2) void ffn_gemm_kernel(FfnGemm p,
   const int l32 = lane & 31, kh = lane >> 5;
   const int oc = (lane % LPR) * 8;           // first of this lane's outputs in the wavefront's columns
   const int n = n0 + wn * OUT + oc;
-  for_each<MI>([&](auto i_c) __attribute__((always_inline)) {
-    constexpr int i = decltype(i_c)::value;
-    const int mb = m0 + wm * (C::BM / C::WM) + i * 32 + lane / LPR;
-    f32x4_t kg[32 / RPI][2], ku[32 / RPI][2];
-    if (PRODUCT == FFN_DH && !SPLIT) {
+  // A runtime loop over the row blocks: all unrolled, the gate's code came to
+  // 70 KB, more than the instruction cache.  What dh reads of the forward is a
+  // step ahead (dh at T = 8192, H = 4096, I = 11008: 873 us with a block's loads
+  // at its start, 805 so).
+  constexpr int STEPS = 32 / RPI;
+  const int mb = m0 + wm * (C::BM / C::WM) + lane / LPR, rows_here = SPLIT ? rows : p.M;
+  constexpr bool KEPT = PRODUCT == FFN_DH && !SPLIT;
+  f32x4_t kg[2], ku[2], ng[2], nu[2];
+  if (KEPT && mb < p.M && n < p.N) load_kept(p, mb, n, ng, nu);
+  auto one = [&](int i, int r) __attribute__((always_inline)) {
+    const int step = i * STEPS + r;
+    const int m = mb + i * 32 + r * RPI;
+    if (KEPT) {
 #pragma unroll
-      for (int r = 0; r < 32 / RPI; ++r) {
-        const int m = mb + r * RPI;
-        if (m < p.M && n < p.N) {
-          load_kept(p, m, n, kg[r], ku[r]);
-        }
+      for (int h = 0; h < 2; ++h) {
+        kg[h] = ng[h];
+        ku[h] = nu[h];
       }
+      const int next = mb + (step + 1) / STEPS * 32 + (step + 1) % STEPS * RPI;
+      if (step + 1 < MI * STEPS && next < p.M && n < p.N) load_kept(p, next, n, ng, nu);
     }
-    // element v of a 32 x 32 block: row l % 32, column 8 (v / 4) + 4 (l / 32) + v % 4
-#pragma unroll
-    for (int j = 0; j < NI; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<f32x4_t*>(mine + l32 * ROWF + j * 32 + 8 * q + 4 * kh) =
-            f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-    asm volatile("" ::: "memory");  // a wavefront's LDS accesses run in order
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int r = 0; r < 32 / RPI; ++r) {
-      const int m = mb + r * RPI;
-      if (m >= (SPLIT ? rows : p.M) || n >= p.N) continue;
+    if (m < rows_here && n < p.N) {
       const float* row = mine + (r * RPI + lane / LPR) * ROWF;
       // gate_up: 32-column blocks alternate, gate, up
       const f32x4_t* src = reinterpret_cast<const f32x4_t*>(row + (GATE ? (oc >> 5) * 64 + (oc & 31) : oc));
@@ -433,13 +433,28 @@ __global__ __launch_bounds__(C::NT, ONE ? 4 : 2) void ffn_gemm_kernel(FfnGemm p,
           dst[p.N / 4 + 1] = u[1];
         }
       } else {
-        finish<PRODUCT>(p, m, n, a, u, kg[r], ku[r]);
+        finish<PRODUCT>(p, m, n, a, u, kg, ku);
       }
-      __builtin_amdgcn_sched_barrier(0);  // one row's registers at a time
     }
+  };
+#pragma unroll 1
+  for (int i = 0; i < MI; ++i) {
+    // element v of a 32 x 32 block: row l % 32, column 8 (v / 4) + 4 (l / 32) + v % 4
+    for_each<MI>([&](auto b_c) __attribute__((always_inline)) {
+      constexpr int b = decltype(b_c)::value;
+      if (i != b) return;
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<f32x4_t*>(mine + l32 * ROWF + j * 32 + 8 * q + 4 * kh) =
+              f32x4_t{acc[b][j][4 * q], acc[b][j][4 * q + 1], acc[b][j][4 * q + 2], acc[b][j][4 * q + 3]};
+    });
+    asm volatile("" ::: "memory");  // a wavefront's LDS accesses run in order
+#pragma unroll
+    for (int r = 0; r < STEPS; ++r) one(i, r);
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-  });
+  }
 }
 
 // Adds the slabs in their order and finishes 8 neighbouring outputs.  DX of a
