@@ -52,6 +52,7 @@ struct Bf16Weights {
         for (int t = 0; t < CT; ++t) a[f][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
     __device__ __forceinline__ void begin(const Bf16Weights&, const Buf*, int) {}
+    __device__ __forceinline__ void rows(int, u32x4_t) {}
     __device__ __forceinline__ void mul(int f, int t, u32x4_t x, u32x4_t w) { a[f][t] = mfma_16x16x32(x, w, a[f][t]); }
     __device__ __forceinline__ void end(const Bf16Weights&, const Buf*, int) {}
     __device__ __forceinline__ f32x4_t sum(int f, int t) const { return a[f][t]; }

@@ -158,6 +158,7 @@ __global__ __launch_bounds__(512, 2) void rows_direct_kernel(RowsArgs p, typenam
       const u32x4_t a =
           *reinterpret_cast<const u32x4_t*>(xl + (l16 & (R * NX - 1)) * XROW + j * 64 + kq * 16);
       acc.begin(w, q[u], j);
+      acc.rows(0, a);
 #pragma unroll
       for (int t = 0; t < CT; ++t) acc.mul(0, t, a, w.operand(q[u][t], j));
       acc.end(w, q[u], j);
@@ -250,7 +251,9 @@ __global__ __launch_bounds__(512, 2) void rows_shared_kernel(RowsArgs p, typenam
     for (int i = 0; i < XPT; ++i) {
       const int r = (tid >> 4) + i * 32;
       if (PIECES >= 512 || r < NX * 16 * RF)
-        xl[b][((r >> 4) * 4 + (piece >> 2)) * 64 + (piece & 3) * 16 + (r & 15)] = xr[u][i];
+        // rows swizzled by the piece, so that a wavefront's write (4 rows, 16
+        // pieces) meets all banks alike
+        xl[b][((r >> 4) * 4 + (piece >> 2)) * 64 + (piece & 3) * 16 + ((r & 15) ^ ((piece & 3) << 2))] = xr[u][i];
     }
   };
   typename W::Buf q[D][CT];
@@ -274,8 +277,12 @@ __global__ __launch_bounds__(512, 2) void rows_shared_kernel(RowsArgs p, typenam
 #pragma unroll
       for (int v = 0; v < NX; ++v)
 #pragma unroll
-        for (int f = 0; f < RF; ++f) a[v][f] = xl[u & 1][((v * RF + f) * 4 + j) * 64 + lane];
+        for (int f = 0; f < RF; ++f) a[v][f] = xl[u & 1][((v * RF + f) * 4 + j) * 64 + (lane ^ (kq << 2))];
       acc.begin(w, q[u], j);
+#pragma unroll
+      for (int v = 0; v < NX; ++v)
+#pragma unroll
+        for (int f = 0; f < RF; ++f) acc.rows(f, a[v][f]);
 #pragma unroll
       for (int t = 0; t < CT; ++t) {
         const u32x4_t bw = w.operand(q[u][t], j);

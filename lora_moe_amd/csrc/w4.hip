@@ -153,10 +153,12 @@ struct PackedWeights {
         z[t] = u32x4_t{v, v, v, v};
       }
     }
-    __device__ __forceinline__ void mul(int f, int t, u32x4_t x, u32x4_t w) {
-      a[f][t] = mfma_16x16x32(x, z[t], a[f][t]);
-      a[f][t] = mfma_16x16x32(x, w, a[f][t]);
+    // the zero points' share of a step
+    __device__ __forceinline__ void rows(int f, u32x4_t x) {
+#pragma unroll
+      for (int t = 0; t < CT; ++t) a[f][t] = mfma_16x16x32(x, z[t], a[f][t]);
     }
+    __device__ __forceinline__ void mul(int f, int t, u32x4_t x, u32x4_t w) { a[f][t] = mfma_16x16x32(x, w, a[f][t]); }
     // after step j: a group's sum is scaled where it ends
     __device__ __forceinline__ void end(const PackedWeights& w, const Buf* b, int j) {
       if ((j + 1) % SPG) return;
