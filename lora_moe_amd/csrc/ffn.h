@@ -38,8 +38,11 @@ struct FfnGemm {
 };
 
 // Up to this many tokens a forward streams the weights (ffn_rows.hip); beyond
-// it the rows' side takes over and tiles are better.
-constexpr int kRowsMax = 64;
+// it the rows' side takes over and tiles are better.  Measured, us, streamed
+// and tiled: H 1024, I 2816, 24 tokens 20 and 22, 64 tokens 23 and 25; 2880,
+// 2880, 24 tokens 28 and 28, 64 tokens 36 and 32; 4096, 11008, 24 tokens 70
+// and 70, 33 tokens 75 and 73, 64 tokens 83 and 81.
+constexpr int kRowsMax = 32;
 // Up to this many, h, dg and du go from one product to the next as bf16 pairs
 // hi + lo, which costs nothing beside the weights.  With so few tokens a few
 // large values carry a result, so that one rounding more than its own can

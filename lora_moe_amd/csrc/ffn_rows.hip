@@ -14,6 +14,7 @@ struct Bf16Weights {
   };
   static constexpr int DEPTH = 2;
   static constexpr int LINES = 32;  // of 128 bytes, per chunk of a tile
+  static constexpr int MAX_FRAGMENTS = kRowsMax / 16;
   struct Tile {
     const uint16_t* base;
     uint32_t bytes;

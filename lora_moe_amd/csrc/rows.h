@@ -23,7 +23,8 @@
 //
 // The weights' format is a policy W (ffn_rows.hip, w4.hip): Tile, where a
 // tile lies; Buf, a chunk of it in registers; load(); operand(), the 32-deep
-// step j of a chunk as bf16; Acc, the sums.  W::DEPTH chunks are in flight.
+// step j of a chunk as bf16; Acc, the sums.  W::DEPTH chunks are in flight;
+// a workgroup has up to W::MAX_FRAGMENTS fragments of 16 rows.
 #pragma once
 
 #include <algorithm>
@@ -418,7 +419,8 @@ void launch_rows(RowsArgs a, const typename W::Args& wa, hipStream_t st) {
   if (rf == 1) rows_shared_kernel<W, 1, GATE, PAIR><<<grid, 512, 0, st>>>(a, wa);
   if constexpr (!PAIR) {
     if (rf == 2) rows_shared_kernel<W, 2, GATE, false><<<grid, 512, 0, st>>>(a, wa);
-    if (rf == 4) rows_shared_kernel<W, 4, GATE, false><<<grid, 512, 0, st>>>(a, wa);
+    if constexpr (W::MAX_FRAGMENTS >= 4)
+      if (rf == 4) rows_shared_kernel<W, 4, GATE, false><<<grid, 512, 0, st>>>(a, wa);
   }
   if (a.splits > 1) {
     const int64_t n = (int64_t)a.M * a.N;

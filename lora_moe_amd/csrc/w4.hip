@@ -73,6 +73,7 @@ struct PackedWeights {
   };
   static constexpr int GPC = 4 / SPG;  // groups of a chunk
   static constexpr int LINES = 8;
+  static constexpr int MAX_FRAGMENTS = 4;
   static constexpr int DEPTH = SPG == 1 ? 2 : 4;
   struct Tile {  // chunk 0 of the tile's weights, scales and zero points
     const char* q;
