@@ -354,7 +354,8 @@ size_t moe_lora_ffn_workspace_bytes(const moe_lora_ffn_shape* shape, int backwar
  *           backward; NULL where none follows
  *   y       device [T][H] bf16, overwritten
  * Sums and the gate are fp32; h is rounded to bf16 once, between the two
- * products, and y once.  The same inputs give the same bits. */
+ * products (up to 16 tokens it goes on as a sum of two bf16, 16 bits), and y
+ * once.  The same inputs give the same bits. */
 int moe_lora_ffn_forward(const moe_lora_ffn_shape* shape, const uint16_t* x, const uint16_t* W_gu,
                          const uint16_t* W_down, float* gu, void* workspace, size_t ws_bytes, uint16_t* y,
                          void* stream);
@@ -366,9 +367,10 @@ int moe_lora_ffn_forward(const moe_lora_ffn_shape* shape, const uint16_t* x, con
  *   gu               device [T][2I] fp32, as the forward wrote it
  *   dx               device [T][H] bf16 or NULL (not wanted)
  *   dW_gu, dW_down   device, shaped as the weights, bf16 or NULL; at least
- *                    one of the three is wanted
+ *                    one of the three is wanted (where T > 0)
  * Gradients are overwritten (with zeros for T = 0), not added to.  dg, du and
- * h are rounded to bf16 once, before the products that take them.  The same
+ * h are rounded to bf16 once, before the products that take them (up to 16
+ * tokens they are sums of two bf16).  The same
  * inputs give the same bits. */
 int moe_lora_ffn_backward(const moe_lora_ffn_shape* shape, const uint16_t* dy, const uint16_t* x, const float* gu,
                           const uint16_t* W_gu, const uint16_t* W_down, void* workspace, size_t ws_bytes,
@@ -403,8 +405,8 @@ int moe_lora_w4_pack(const moe_lora_w4* w, const uint8_t* q, const uint16_t* sca
  *   y          device [M][N] bf16, overwritten
  *   workspace  device, 16-byte aligned, ws_bytes >= moe_lora_w4_workspace_bytes(w, M)
  * The weights enter as integers and the scales in fp32, so y differs from
- * the exact product by its own rounding and that of fp32 sums.  A row of x
- * with an infinity or NaN gives a row of y that is not finite.  The same
+ * the exact product by its own rounding and that of fp32 sums.  x up to 1e34
+ * in size; a row of x with an infinity or NaN gives a row of y that is not finite.  The same
  * inputs give the same bits. */
 int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, void* workspace, size_t ws_bytes,
                        uint16_t* y, void* stream);
@@ -414,7 +416,7 @@ int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, void*
 size_t moe_lora_w4_workspace_bytes(const moe_lora_w4* w, int32_t M);
 
 /* The gated block on 4-bit weights: h = act(x gate^T) * (x up^T), y = h
- * down^T, h rounded to bf16.  gate and up are [I][H] alike in group and zero
+ * down^T, h rounded to bf16 (up to 16 rows: a sum of two).  gate and up are [I][H] alike in group and zero
  * points, down is [H][I]; I is a multiple of 8 as well.
  *   x, y  device [M][H] bf16   workspace  device, 16-byte aligned */
 size_t moe_lora_w4_ffn_workspace_bytes(int32_t M, int32_t I);
@@ -447,8 +449,9 @@ size_t moe_lora_clip_workspace_bytes(int32_t n);
  *             only the norm is computed)
  *   norm      device [1] fp32, written
  * Sums are fp64 in a fixed order: the same gradients give the same bits.  A
- * gradient that is not finite shows in norm and, by the formula, in out: an
- * infinite norm makes finite gradients 0, NaN makes all of them NaN. */
+ * gradient that is not finite shows in norm and, under a finite max_norm and
+ * by the formula, in out: an infinite norm makes finite gradients 0, NaN makes
+ * all of them NaN. */
 int moe_lora_clip_grads(const moe_lora_grad* grads, int32_t n, float max_norm, float* norm, void* workspace,
                         size_t ws_bytes, void* stream);
 

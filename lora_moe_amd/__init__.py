@@ -546,6 +546,8 @@ def _used_on(stream, *tensors) -> None:
 
 
 def _check_workspace(workspace, need: int, what: str):
+    if workspace is None:
+        raise ValueError(f"workspace is required ({what})")
     if str(workspace.dtype) != "torch.uint8" or workspace.dim() != 1:
         raise ValueError(f"workspace must be a 1-D uint8 tensor ({what})")
     if workspace.numel() < need:
@@ -721,8 +723,10 @@ def moe_lora_w4_ffn_forward(x, gate: W4Weight, up: W4Weight, down: W4Weight, wor
 
 class GradSet:
     """The gradients of one training program for moe_lora_clip_grads: checked
-    and listed once, kept as long as the program uses these tensors.  out:
-    where the clipped gradients go (like ``grads``); None: in place."""
+    and listed once, kept as long as the program uses these tensors (a tensor
+    that is given other memory, by ``.data = ``, needs a new set).  out: where
+    the clipped gradients go (like ``grads``); None: in place.  A set has one
+    workspace: its calls follow one another."""
 
     def __init__(self, grads, out=None):
         import torch
@@ -741,6 +745,8 @@ class GradSet:
             specs += [(f"grads[{i}]", g, shape, dtype), (f"out[{i}]", o, shape, dtype)]
             self._arr[i] = moe_lora_grad(g.data_ptr(), o.data_ptr(), g.numel(), _GRAD_TYPES[str(g.dtype)])
         _check_tensors(specs)
+        # the listed memory stays allocated, whatever the tensors become
+        self._held = [t.detach() for t in self.grads + self.out]
         need = moe_lora_clip_workspace_bytes(n)
         device = self.grads[0].device if n else "cuda"
         self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
@@ -756,10 +762,10 @@ def moe_lora_clip_workspace_bytes(n: int) -> int:
 def moe_lora_clip_grads(grads, max_norm: float, norm, stream=None) -> None:
     """Scales the gradients (a GradSet, or a list of tensors, in place) by
     min(1, max_norm / (norm + 1e-6)) and writes their global norm to ``norm``
-    ([1] fp32, device).  max_norm = inf: the norm only."""
+    ([1] fp32, device).  max_norm = inf: the norm only (with out: a copy)."""
     if not isinstance(grads, GradSet):
         grads = GradSet(grads)
-        _used_on(stream, grads.workspace)
+    _used_on(stream, grads.workspace)
     _check_tensors([("norm", norm, (1,), "float32"), ("workspace", grads.workspace, None, "uint8")])
     _check("moe_lora_clip_grads", load_library().moe_lora_clip_grads(
         grads._arr, len(grads), float(max_norm), norm.data_ptr(), grads.workspace.data_ptr(),

@@ -197,7 +197,8 @@ __global__ __launch_bounds__(256) void scale_kernel(Table t, const double* __res
   s = sqrt(block_sum(s, lds));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)s;
   const double cd = (double)max_norm / (s + (double)kEps);
-  const float c = cd > 1. ? 1.f : (float)cd;  // NaN stays NaN
+  // NaN stays NaN; without a bound (infinity) the norm does not matter
+  const float c = cd > 1. || max_norm == INFINITY ? 1.f : (float)cd;
   for (int k0 = t.first[t.n] - 1 - (int)blockIdx.x; k0 >= 0; k0 -= gridDim.x) {
     const int k = tensor_of(t, k0), dt = t.dtype[k];
     const void* g = t.g[k];

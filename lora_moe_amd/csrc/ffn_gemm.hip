@@ -184,12 +184,16 @@ __device__ __forceinline__ void store8(uint16_t* p, const float* v) {
 }
 
 // what rounding to bf16 takes off (in place)
+__device__ __forceinline__ float remainder1(float v, float hi) {
+  const float r = v - hi;
+  return r == r ? r : 0.f;  // infinities have none
+}
 __device__ __forceinline__ const float* remainder8(float* v) {
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
     const uint32_t r = f32x2_to_bf16(v[i], v[i + 1]);
-    v[i] -= bf16_lo(r);
-    v[i + 1] -= bf16_hi(r);
+    v[i] = remainder1(v[i], bf16_lo(r));
+    v[i + 1] = remainder1(v[i + 1], bf16_hi(r));
   }
   return v;
 }
@@ -487,7 +491,7 @@ int launch_cfg(const FfnGemm& g, hipStream_t st) {
   constexpr int lds = ONE ? C::LDS_ONE : C::LDS;
   const int rows = PRODUCT == FFN_DX && g.pair ? 2 * g.M : g.M;
   const int64_t ncol = (g.N + bn - 1) / bn, nrow = (rows + C::BM - 1) / C::BM, grid = ncol * nrow * g.splits;
-  if (grid > 0x7fffffff) return MOE_LORA_EUNSUPPORTED;
+  if (grid * C::NT > 0xffffffff) return MOE_LORA_EUNSUPPORTED;
   const void* fn = reinterpret_cast<const void*>(&ffn_gemm_kernel<PRODUCT, C, SPLIT, ONE>);
   const int rc = ensure_dynamic_lds(fn, lds, attr_done);
   if (rc) return rc;

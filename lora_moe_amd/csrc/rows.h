@@ -59,7 +59,10 @@ __device__ __forceinline__ void rows_store(const RowsArgs& p, bool gated, int m,
     p.gu[(int64_t)m * 2 * p.N + n] = a;
     p.gu[(int64_t)m * 2 * p.N + p.N + n] = u;
   }
-  if (gated && p.out_lo) p.out_lo[(int64_t)m * p.N + n] = f32_to_bf16(r - bf16_to_f32(hi));
+  if (gated && p.out_lo) {
+    const float lo = r - bf16_to_f32(hi);
+    p.out_lo[(int64_t)m * p.N + n] = lo == lo ? f32_to_bf16(lo) : (uint16_t)0;  // infinities have none
+  }
 }
 
 __device__ __forceinline__ u32x4_t rows_load(const void* base, uint32_t bytes, uint32_t voff, uint32_t soff) {

@@ -69,6 +69,17 @@ def test_ffn_arguments(lib):
         assert ffn_backward(lib, s, **{n: at(9, 4)}) == EALIGN, n
 
 
+def test_ffn_no_tokens_backward(lib):
+    s = lm.make_ffn_shape(0, 64, 128)
+    assert ffn_backward(lib, s, dx=None, dW_gu=None, dW_down=None) == 0
+
+
+def test_workspace_is_required():
+    x = torch.zeros((2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="workspace is required"):
+        lm.moe_lora_ffn_forward(lm.make_ffn_shape(2, 64, 64), x, x, x, None, x)
+
+
 def test_ffn_overlaps(lib):
     """An output or the workspace on an input or on another output, by its
     first or last 16 bytes."""

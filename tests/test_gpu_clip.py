@@ -86,6 +86,33 @@ def test_norm_only():
         assert torch.equal(a, b)
 
 
+def test_no_bound_leaves_gradients_that_are_not_finite():
+    """max_norm = inf: every value goes on as it is, whatever the norm is."""
+    import lora_moe_amd as lm
+    for v in (float("inf"), float("nan")):
+        grads = make([(1000,), (33, 77)], DTYPES, 1)
+        grads[1][3, 5] = v
+        outs = [torch.zeros_like(t) for t in grads]
+        norm = clip(lm, grads, float("inf"), outs)
+        assert not math.isfinite(float(norm))
+        for a, b in zip(grads, outs):
+            assert torch.equal(torch.nan_to_num(a, 7.0), torch.nan_to_num(b, 7.0))
+
+
+def test_tensors_given_other_memory():
+    """A set keeps the memory that it listed, and clips that."""
+    import lora_moe_amd as lm
+    g = torch.full((5000,), 2.0, device="cuda")
+    old = g.detach()
+    gs = lm.GradSet([g])
+    g.data = torch.full((5000,), 3.0, device="cuda")
+    norm = torch.empty(1, device="cuda")
+    lm.moe_lora_clip_grads(gs, 1.0, norm)
+    want = 2.0 * math.sqrt(5000)
+    assert abs(float(norm) - want) <= 1e-6 * want
+    assert torch.allclose(old, torch.full_like(old, 2.0 / want), rtol=1e-5) and (g == 3.0).all()
+
+
 def test_no_tensors():
     import lora_moe_amd as lm
     assert float(clip(lm, [], 1.0)) == 0.0

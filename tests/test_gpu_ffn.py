@@ -130,6 +130,36 @@ def test_no_tokens():
     assert not got["dW_gu"].any() and not got["dW_down"].any()
 
 
+def test_no_tokens_dx_only():
+    """T = 0 with an empty dx as the only gradient is nothing to do."""
+    import lora_moe_amd as lm
+    H, I = 72, 40
+    e = torch.empty((0, H), dtype=torch.bfloat16, device="cuda")
+    _, W_gu, W_down, _ = (t.cuda() for t in ffn_inputs(1, H, I, 1))
+    shape = lm.make_ffn_shape(0, H, I)
+    ws = lm.alloc_ffn_workspace(shape)
+    gu = torch.empty((0, 2 * I), device="cuda")
+    lm.moe_lora_ffn_backward(shape, e, e, gu, W_gu, W_down, ws, dx=torch.empty_like(e))
+
+
+@pytest.mark.parametrize("T", [1, 6, 16, 20])
+def test_infinities_stay_infinite(T):
+    """Where h or a gradient leaves bf16's range the outputs are the formula's
+    infinities, also where values go on as pairs (up to 16 tokens)."""
+    import lora_moe_amd as lm
+    H, I = 64, 64
+    x = torch.full((T, H), 2.0 ** 62, dtype=torch.bfloat16, device="cuda")
+    W_gu = torch.full((2 * I, H), 0.25, dtype=torch.bfloat16, device="cuda")
+    W_down = torch.full((H, I), 0.5, dtype=torch.bfloat16, device="cuda")
+    # g = u = 2^66: h = 2^132 is past every range
+    shape, ws, y, gu = forward(lm, x, W_gu, W_down, "silu", keep=True)
+    assert (gu == 2.0 ** 66).all() and (y == float("inf")).all()
+    dy = torch.full((T, H), 2.0 ** 62, dtype=torch.bfloat16, device="cuda")
+    got = gradients(lm, shape, ws, dy, x, gu, W_gu, W_down)
+    for n, t in got.items():  # dh = 2^67, dg = dh u and du = dh g likewise
+        assert (t == float("inf")).all(), n
+
+
 def test_extreme_gates():
     """Pre-activations far out on both sides: the gate saturates, nothing
     overflows on the way (gelu's cube, exp)."""
