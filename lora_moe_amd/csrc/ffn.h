@@ -62,4 +62,9 @@ size_t ffn_gemm_slab_bytes(int M, int N, int K, FfnProduct product, bool pair = 
 
 int launch_ffn_gemm(const FfnGemm& g, FfnProduct product, hipStream_t st);
 
+// The FFN_DX and the two FFN_DW of a backward that wants all three; dx.slabs:
+// the larger of ffn_grads_slab_bytes and the products' own.
+size_t ffn_grads_slab_bytes(int T, int H, int I);
+int launch_ffn_grads(const FfnGemm& dx, const FfnGemm& dw_gu, const FfnGemm& dw_down, hipStream_t st);
+
 }  // namespace moelora

@@ -52,7 +52,7 @@ size_t ws_bytes_of(const moe_lora_ffn_shape& s, bool backward) {
   if (!backward) return forward;
   const bool pair = T <= kRowsPair;
   const int k = pair ? 2 * T : T;
-  const size_t back = std::max({ffn_gemm_slab_bytes(T, I, H, FFN_DH), ffn_gemm_slab_bytes(T, H, 2 * I, FFN_DX, pair),
+  const size_t back = std::max({ffn_grads_slab_bytes(T, H, I), ffn_gemm_slab_bytes(T, I, H, FFN_DH), ffn_gemm_slab_bytes(T, H, 2 * I, FFN_DX, pair),
                                 ffn_gemm_slab_bytes(2 * I, H, k, FFN_DW), ffn_gemm_slab_bytes(H, I, k, FFN_DW)});
   return std::max(forward, backward_fixed(s) + round256(back));
 }
@@ -138,22 +138,18 @@ int moe_lora_ffn_backward(const moe_lora_ffn_shape* shape, const uint16_t* dy, c
   int r = launch_ffn_gemm(g, FFN_DH, st);
   if (r) return r;
   g.gu = nullptr, g.out2 = nullptr;
-  if (dx) {
-    g.A = dgu, g.lda = 2 * (int64_t)I, g.B = W_gu, g.ldb = H, g.M = T, g.N = H, g.K = 2 * I, g.out = dx;
-    if ((r = launch_ffn_gemm(g, FFN_DX, st))) return r;
-  }
+  FfnGemm gx = g, gw = g, gd = g;
+  gx.A = dgu, gx.lda = 2 * (int64_t)I, gx.B = W_gu, gx.ldb = H, gx.M = T, gx.N = H, gx.K = 2 * I, gx.out = dx;
   // the pair's remainders are further tokens of the sums, with the same x or dy
   const int K = g.pair ? 2 * T : T;
-  if (dW_gu) {
-    g.A = dgu, g.lda = 2 * (int64_t)I, g.B = x, g.ldb = H, g.M = 2 * I, g.N = H, g.K = K, g.out = dW_gu;
-    g.wrap_a = 0, g.wrap_b = g.pair ? T : 0;
-    if ((r = launch_ffn_gemm(g, FFN_DW, st))) return r;
-  }
-  if (dW_down) {
-    g.A = dy, g.lda = H, g.B = h, g.ldb = I, g.M = H, g.N = I, g.K = K, g.out = dW_down;
-    g.wrap_a = g.pair ? T : 0, g.wrap_b = 0;
-    if ((r = launch_ffn_gemm(g, FFN_DW, st))) return r;
-  }
+  gw.A = dgu, gw.lda = 2 * (int64_t)I, gw.B = x, gw.ldb = H, gw.M = 2 * I, gw.N = H, gw.K = K, gw.out = dW_gu;
+  gw.wrap_a = 0, gw.wrap_b = g.pair ? T : 0;
+  gd.A = dy, gd.lda = H, gd.B = h, gd.ldb = I, gd.M = H, gd.N = I, gd.K = K, gd.out = dW_down;
+  gd.wrap_a = g.pair ? T : 0, gd.wrap_b = 0;
+  if (dx && dW_gu && dW_down) return launch_ffn_grads(gx, gw, gd, st);
+  if (dx && (r = launch_ffn_gemm(gx, FFN_DX, st))) return r;
+  if (dW_gu && (r = launch_ffn_gemm(gw, FFN_DW, st))) return r;
+  if (dW_down && (r = launch_ffn_gemm(gd, FFN_DW, st))) return r;
   return MOE_LORA_OK;
 }
 

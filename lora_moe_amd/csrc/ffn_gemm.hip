@@ -255,9 +255,10 @@ __device__ __forceinline__ void finish(const FfnGemm& p, int m, int n, const f32
 // gradient of few tokens is bound by its own stores and by how many tiles'
 // first copies are in flight (22016 x 4096 of 64 tokens: 48 us so, 79
 // without).
+//
+// Workgroup `block` of the product's ncol x nrow tiles (times its splits).
 template <int PRODUCT, class C, bool SPLIT, bool ONE>
-__global__ __launch_bounds__(C::NT, ONE ? 4 : 2) void ffn_gemm_kernel(FfnGemm p, int ncol,
-                                                                                            int nrow) {
+__device__ __forceinline__ void ffn_tile(const FfnGemm& p, int ncol, int nrow, int block) {
   constexpr bool A_KC = PRODUCT != FFN_DW;
   constexpr bool B_KC = PRODUCT == FFN_GATE_UP || PRODUCT == FFN_DOWN;
   constexpr bool GATE = PRODUCT == FFN_GATE_UP;
@@ -273,7 +274,7 @@ __global__ __launch_bounds__(C::NT, ONE ? 4 : 2) void ffn_gemm_kernel(FfnGemm p,
   // and 8 column panels in its L2.
   int t;
   {
-    const int total = ncol * nrow * (SPLIT ? p.splits : 1), x = blockIdx.x & 7, j = blockIdx.x >> 3;
+    const int total = ncol * nrow * (SPLIT ? p.splits : 1), x = block & 7, j = block >> 3;
     const int per = total >> 3, rest = total & 7;
     t = x * per + min(x, rest) + j;
   }
@@ -461,6 +462,33 @@ __global__ __launch_bounds__(C::NT, ONE ? 4 : 2) void ffn_gemm_kernel(FfnGemm p,
   }
 }
 
+template <int PRODUCT, class C, bool SPLIT, bool ONE>
+__global__ __launch_bounds__(C::NT, ONE ? 4 : 2) void ffn_gemm_kernel(FfnGemm p, int ncol, int nrow) {
+  ffn_tile<PRODUCT, C, SPLIT, ONE>(p, ncol, nrow, blockIdx.x);
+}
+
+// The three products of a backward that follow dh, none of which needs
+// another, as one grid: dx, whose tiles take longest, then the weight
+// gradients, so that no product ends in a round of its own (backward of 1001
+// tokens, H = I = 2880: 130 us so, 174 as three grids; 4096 x 11008: 150 tokens
+// 225 and 238, 2048 tokens 999 and 1140, 8192 tokens 3723 and 3759).
+struct FfnGrads {
+  FfnGemm g[3];  // dx, dW_gu, dW_down
+  int ncol[3], nrow[3];
+  int first[3];  // workgroup
+};
+
+template <class C, bool SPLIT>
+__global__ __launch_bounds__(C::NT, 2) void ffn_grads_kernel(FfnGrads p) {
+  const int block = blockIdx.x;
+  if (block < p.first[1]) {
+    ffn_tile<FFN_DX, C, SPLIT, false>(p.g[0], p.ncol[0], p.nrow[0], block);
+  } else {
+    const int i = block < p.first[2] ? 1 : 2;
+    ffn_tile<FFN_DW, C, false, false>(p.g[i], p.ncol[i], p.nrow[i], block - p.first[i]);
+  }
+}
+
 // Adds the slabs in their order and finishes 8 neighbouring outputs.  DX of a
 // pair: a row's remainder is row M + m of the slabs.
 template <int PRODUCT>
@@ -484,6 +512,12 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(FfnGemm p) {
   finish<PRODUCT>(p, m, n, s[0], s[W - 1], kg, ku);
 }
 
+template <int PRODUCT>
+void launch_join(const FfnGemm& g, hipStream_t st) {
+  const int64_t n = (int64_t)g.M * (g.N / 8);
+  ffn_join_kernel<PRODUCT><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g);
+}
+
 template <int PRODUCT, class C, bool SPLIT, bool ONE = false>
 int launch_cfg(const FfnGemm& g, hipStream_t st) {
   static std::atomic<uint64_t> attr_done;
@@ -496,10 +530,7 @@ int launch_cfg(const FfnGemm& g, hipStream_t st) {
   const int rc = ensure_dynamic_lds(fn, lds, attr_done);
   if (rc) return rc;
   ffn_gemm_kernel<PRODUCT, C, SPLIT, ONE><<<(unsigned)grid, C::NT, lds, st>>>(g, (int)ncol, (int)nrow);
-  if (SPLIT) {
-    const int64_t n = (int64_t)g.M * (g.N / 8);
-    ffn_join_kernel<PRODUCT><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g);
-  }
+  if (SPLIT) launch_join<PRODUCT>(g, st);
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
@@ -526,11 +557,12 @@ typedef FfnCfg<128, 128, 2, 2> Small;
 struct FfnPlan {
   bool big;
   int splits;
+  double us;
 };
 
 FfnPlan plan(int M, int N, int K, FfnProduct product) {
   const int64_t stages = std::max(1, (K + BK - 1) / BK), cols = (int64_t)N * (product == FFN_GATE_UP ? 2 : 1);
-  FfnPlan best{true, 1};
+  FfnPlan best{true, 1, 0.};
   int64_t tiles = (int64_t)((M + 255) / 256) * ((cols + 255) / 256);
   double least = (double)((tiles + 255) / 256) * (stages * 1.19 + 4.0);
   tiles = (int64_t)((M + 127) / 128) * ((cols + 127) / 128);
@@ -545,7 +577,54 @@ FfnPlan plan(int M, int N, int K, FfnProduct product) {
       best = FfnPlan{false, (int)s};
     }
   }
+  best.us = least;
   return best;
+}
+
+int64_t tiles_of(int M, int N, int tile) { return (int64_t)((M + tile - 1) / tile) * ((N + tile - 1) / tile); }
+
+// The same for the three products as one grid: all stages share the chip, and
+// on the mean half a weight gradient's tile is what the last workgroups wait
+// for.  us = 0: three grids (few tokens, and what the constants say).
+FfnPlan grads_plan(int T, int H, int I) {
+  FfnPlan best{false, 1, 0.};
+  if (T <= BK) return best;
+  double least = plan(T, H, 2 * I, FFN_DX).us + plan(2 * I, H, T, FFN_DW).us + plan(H, I, T, FFN_DW).us;
+  const int sx = (2 * I + BK - 1) / BK, sw = (T + BK - 1) / BK;
+  auto take = [&](bool big, int s, double us) {
+    if (us < least) best = FfnPlan{big, s, us}, least = us;
+  };
+  {
+    const int64_t x = tiles_of(T, H, 256), w = tiles_of(2 * I, H, 256) + tiles_of(H, I, 256);
+    const double all = (x * (sx * 1.19 + 4.) + w * (sw * 1.19 + 4.)) / 256, last = sw * 1.19 + 4.;
+    take(true, 1, std::max(all + last / 2, sx * 1.19 + 4.));
+  }
+  const int64_t x = tiles_of(T, H, 128), w = tiles_of(2 * I, H, 128) + tiles_of(H, I, 128);
+  for (int s = 1; s <= 16 && s * 3 <= std::max(3, sx); ++s) {
+    if (s > 1 && x * s > 2048) break;
+    const int each = (sx + s - 1) / s;
+    const double all = (x * s * (each * 0.81 + 0.8) + w * (sw * 0.81 + 0.8)) / 512, last = sw * 0.81 + 0.8;
+    take(false, s, std::max(all + last / 2, each * 0.81 + 0.8) + (s > 1 ? 3.5 + s * (double)T * H * 8 * 0.16e-6 : 0.));
+  }
+  return best;
+}
+
+template <class C, bool SPLIT>
+int launch_grads_cfg(FfnGrads g, hipStream_t st) {
+  static std::atomic<uint64_t> attr_done;
+  int64_t n = 0;
+  for (int i = 0; i < 3; ++i) {
+    g.ncol[i] = (g.g[i].N + C::BN - 1) / C::BN;
+    g.nrow[i] = (g.g[i].M + C::BM - 1) / C::BM;
+    g.first[i] = (int)n;
+    n += (int64_t)g.ncol[i] * g.nrow[i] * g.g[i].splits;
+    if (n * C::NT > 0xffffffff) return MOE_LORA_EUNSUPPORTED;
+  }
+  const int rc = ensure_dynamic_lds(reinterpret_cast<const void*>(&ffn_grads_kernel<C, SPLIT>), C::LDS, attr_done);
+  if (rc) return rc;
+  ffn_grads_kernel<C, SPLIT><<<(unsigned)n, C::NT, C::LDS, st>>>(g);
+  if (SPLIT) launch_join<FFN_DX>(g.g[0], st);
+  return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
 template <int PRODUCT>
@@ -565,6 +644,25 @@ int launch(FfnGemm g, hipStream_t st) {
 size_t ffn_gemm_slab_bytes(int M, int N, int K, FfnProduct product, bool pair) {
   const int s = plan(pair ? 2 * M : M, N, K, product).splits;
   return s > 1 || pair ? (size_t)s * M * N * (product == FFN_GATE_UP || pair ? 2 : 1) * sizeof(float) : 0;
+}
+
+size_t ffn_grads_slab_bytes(int T, int H, int I) {
+  const FfnPlan f = grads_plan(T, H, I);
+  return f.us > 0. && f.splits > 1 ? (size_t)f.splits * T * H * sizeof(float) : 0;
+}
+
+int launch_ffn_grads(const FfnGemm& dx, const FfnGemm& dw_gu, const FfnGemm& dw_down, hipStream_t st) {
+  const FfnPlan f = grads_plan(dx.M, dx.N, dx.K / 2);
+  if (f.us > 0.) {
+    FfnGrads g = {{dx, dw_gu, dw_down}, {}, {}, {}};
+    g.g[0].splits = f.splits;
+    g.g[1].splits = g.g[2].splits = 1;
+    if (f.splits > 1) return launch_grads_cfg<Small, true>(g, st);
+    return f.big ? launch_grads_cfg<Big, false>(g, st) : launch_grads_cfg<Small, false>(g, st);
+  }
+  int r = launch_ffn_gemm(dx, FFN_DX, st);
+  if (!r) r = launch_ffn_gemm(dw_gu, FFN_DW, st);
+  return r ? r : launch_ffn_gemm(dw_down, FFN_DW, st);
 }
 
 int launch_ffn_gemm(const FfnGemm& g, FfnProduct product, hipStream_t st) {
