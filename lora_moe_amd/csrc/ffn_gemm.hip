@@ -583,12 +583,24 @@ FfnPlan plan(int M, int N, int K, FfnProduct product) {
 
 int64_t tiles_of(int M, int N, int tile) { return (int64_t)((M + tile - 1) / tile) * ((N + tile - 1) / tile); }
 
+// Up to BK tokens: one grid up to this many tiles of the weight gradients,
+// beyond it their one-stage form in grids of their own gains more than the
+// launches cost.  33 tokens, one grid and three, us: 256 x 512 (24 tiles) 18
+// and 25, 1024 x 2816 (528) 30 and 35, 2880 x 2880 (1564) 46 and 49, 2880 x
+// 5760 (3105) 65 and 63, 4096 x 11008 (8256) 174 and 153.
+constexpr int64_t kGradsFew = 2048;
+
 // The same for the three products as one grid: all stages share the chip, and
 // on the mean half a weight gradient's tile is what the last workgroups wait
-// for.  us = 0: three grids (few tokens, and what the constants say).
+// for.  us = 0: three grids.
 FfnPlan grads_plan(int T, int H, int I) {
   FfnPlan best{false, 1, 0.};
-  if (T <= BK) return best;
+  if (T <= BK) {
+    const bool pair = T <= kRowsPair;
+    const int64_t s = plan(pair ? 2 * T : T, H, 2 * I, FFN_DX).splits;
+    if (tiles_of(2 * I, H, 128) + tiles_of(H, I, 128) <= kGradsFew) best = FfnPlan{false, (int)s, 1.};
+    return best;
+  }
   double least = plan(T, H, 2 * I, FFN_DX).us + plan(2 * I, H, T, FFN_DW).us + plan(H, I, T, FFN_DW).us;
   const int sx = (2 * I + BK - 1) / BK, sw = (T + BK - 1) / BK;
   auto take = [&](bool big, int s, double us) {
@@ -615,7 +627,7 @@ int launch_grads_cfg(FfnGrads g, hipStream_t st) {
   int64_t n = 0;
   for (int i = 0; i < 3; ++i) {
     g.ncol[i] = (g.g[i].N + C::BN - 1) / C::BN;
-    g.nrow[i] = (g.g[i].M + C::BM - 1) / C::BM;
+    g.nrow[i] = ((i == 0 && g.g[0].pair ? 2 : 1) * g.g[i].M + C::BM - 1) / C::BM;
     g.first[i] = (int)n;
     n += (int64_t)g.ncol[i] * g.nrow[i] * g.g[i].splits;
     if (n * C::NT > 0xffffffff) return MOE_LORA_EUNSUPPORTED;
@@ -648,7 +660,8 @@ size_t ffn_gemm_slab_bytes(int M, int N, int K, FfnProduct product, bool pair) {
 
 size_t ffn_grads_slab_bytes(int T, int H, int I) {
   const FfnPlan f = grads_plan(T, H, I);
-  return f.us > 0. && f.splits > 1 ? (size_t)f.splits * T * H * sizeof(float) : 0;
+  const bool pair = T <= kRowsPair;
+  return f.us > 0. && (f.splits > 1 || pair) ? (size_t)f.splits * (pair ? 2 : 1) * T * H * sizeof(float) : 0;
 }
 
 int launch_ffn_grads(const FfnGemm& dx, const FfnGemm& dw_gu, const FfnGemm& dw_down, hipStream_t st) {
@@ -657,7 +670,7 @@ int launch_ffn_grads(const FfnGemm& dx, const FfnGemm& dw_gu, const FfnGemm& dw_
     FfnGrads g = {{dx, dw_gu, dw_down}, {}, {}, {}};
     g.g[0].splits = f.splits;
     g.g[1].splits = g.g[2].splits = 1;
-    if (f.splits > 1) return launch_grads_cfg<Small, true>(g, st);
+    if (f.splits > 1 || dx.pair) return launch_grads_cfg<Small, true>(g, st);
     return f.big ? launch_grads_cfg<Big, false>(g, st) : launch_grads_cfg<Small, false>(g, st);
   }
   int r = launch_ffn_gemm(dx, FFN_DX, st);
