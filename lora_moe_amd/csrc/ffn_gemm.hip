@@ -535,14 +535,14 @@ int launch_cfg(const FfnGemm& g, hipStream_t st) {
 }
 
 // 256 x 256 tiles on 8 wavefronts of 128 x 64, one workgroup per CU (128 KB
-// of LDS).  T = 8192, H = 4096, I = 11008 (0.74 TFLOP, dx and the gate_up
-// pair 1.48), us: down 576, dx 1119, dW_down about 590, gate_up with its kept
-// gu 1200, dh with its gate 900, i.e. 1.25 to 1.32 PFLOP/s where the epilogue
-// is only a store.  What bounds them is power: at 71 % of the MFMA slots the
-// clock is 1.85 GHz of 2.4, and a copy of the loop that waits less reached
-// 87 % at 1.59 GHz and the same time within 4 %.  Four wavefronts of 128 x
-// 128 read less LDS but stall the only wavefront of a SIMD while it issues
-// its copies (dx 1250 us against 1177, alternating runs).
+// of LDS).  T = 8192, H = 4096, I = 11008 (0.74 TFLOP, the gate_up pair 1.48,
+// the gradients that follow dh 3.69), us: down 586, gate_up with its kept gu
+// 1445, dh with its gate 843, the gradients 2951, i.e. 1.25 PFLOP/s where the
+// epilogue is only a store.  What bounds them is power: at 75 % of the MFMA
+// slots the clock is 1.5 to 1.85 GHz of 2.4, and a copy of the loop that waits
+// less reached 87 % at 1.59 GHz and the same time within 4 %.  Four wavefronts
+// of 128 x 128 read less LDS but stall the only wavefront of a SIMD while it
+// issues its copies (dx 1250 us against 1177, alternating runs).
 typedef FfnCfg<256, 256, 2, 4> Big;
 // 128 x 128 tiles on 4 wavefronts, two workgroups per CU, where there are too
 // few large ones to fill the chip.

@@ -17,6 +17,10 @@
 //     through LDS.  Where that leaves too few workgroups K is split over
 //     the grid into fp32 slabs, which rows_join_kernel adds up.
 //
+// Measured, bf16: one row, 4096 x 11008 (gate and up 180 MB, down 90): 35 and
+// 20 us, 5.1 and 4.6 TB/s; 32 rows, 5120 x 25600 (524 and 262 MB): 118 and 59
+// us, 4.4 TB/s; a large copy moves 4.9.
+//
 // Loads are buffer loads, so that rows, k and chunks past the end are zeros
 // without traffic or branches: the loops are straight-line code in which each
 // wait names the loads it needs.
@@ -393,7 +397,9 @@ inline size_t rows_slab_bound(int M) {
 }
 
 // Wavefronts that split K in the direct form: about 2048 of them over the
-// chip, at least two chunks each.
+// chip, at least two chunks each.  (4 bits, us, at most 1536, 3072 and 6144:
+// one row, 5120 x 25600 21.4, 20.6, 20.6; 25600 x 5120 17.3, 16.4, 16.9; five
+// rows, 11008 x 4096 10.7, 9.8, 12.6.)
 inline int rows_ksplit(int64_t workgroups, int K) {
   int ks = 8;
   while (ks > 1 && (workgroups * ks > 3072 || K / 128 < 2 * ks)) ks >>= 1;
