@@ -13,7 +13,7 @@
 // vanish, and the order of addition does not show in fp32.
 //
 // Measured: 541 M bf16 gradients (1.08 GB) 181 us for the norm, 6.0 TB/s, and
-// 420 for the second pass, 5.1 TB/s (1.08 GB read, as much written); 112
+// 420 for the second pass, 5.1 TB/s (1.08 GB read, as much written); 224
 // tensors of 52 MB in all 13 and 20 us, half of it the launch, the table's
 // search and the partial sums.
 //
