@@ -377,9 +377,12 @@ inline RowsPlan rows_plan(int M, int N, int K, int lines_per_chunk) {
   r.direct = M <= 8 && (2 * M <= lines_per_chunk / 2 || tiles * chunks * 2 * M * 128 < 5 * 7000000LL);
   if (r.direct) return r;
   // at most one workgroup per CU (256) where K is split, since a second round
-  // of a few would take as long as the first; 4 chunks each at least
+  // of a few would take as long as the first; 6 chunks each, where there are
+  // fewer the slabs cost more than they spare (us with 4, 6 and 8: 16 rows
+  // through the bf16 block, 2880 x 2880 27.1, 23.4, 26.1; 32 rows, 4 bits,
+  // 4096 x 4096 12.2, 11.5, 10.5; 64 rows, 1024 x 2048 9.3, 9.8, 10.9)
   const int64_t rt = 16 * rows_fragments(M), row_tiles = (M + rt - 1) / rt, least = (tiles + 7) / 8;
-  const int64_t s = std::min<int64_t>(256 / (least * row_tiles), (chunks + 3) / 4);
+  const int64_t s = std::min<int64_t>(256 / (least * row_tiles), (chunks + 5) / 6);
   r.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, kRowsJoinMax));
   r.groups = (int)std::max<int64_t>(least, std::min<int64_t>(tiles, 256 / (r.splits * row_tiles)));
   return r;
