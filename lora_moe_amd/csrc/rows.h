@@ -400,12 +400,12 @@ inline size_t rows_slab_bound(int M) {
 }
 
 // Wavefronts that split K in the direct form: about 2048 of them over the
-// chip, at least two chunks each.  (4 bits, us, at most 1536, 3072 and 6144:
+// chip, at least two chunks each.  (4 bits, us, at most about 1500, 3000 and 6000:
 // one row, 5120 x 25600 21.4, 20.6, 20.6; 25600 x 5120 17.3, 16.4, 16.9; five
 // rows, 11008 x 4096 10.7, 9.8, 12.6.)
 inline int rows_ksplit(int64_t workgroups, int K) {
   int ks = 8;
-  while (ks > 1 && (workgroups * ks > 3072 || K / 128 < 2 * ks)) ks >>= 1;
+  while (ks > 1 && (workgroups * ks > 3000 || K / 128 < 2 * ks)) ks >>= 1;
   return ks;
 }
 
