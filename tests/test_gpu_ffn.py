@@ -302,8 +302,10 @@ def test_one_call_form():
     assert torch.equal(lm.gated_ffn(x, W_gu, W_down, act="gelu"), forward(lm, x, W_gu, W_down, "gelu")[2])
 
 
-# sizes at which each product takes the large tiles, ending inside them
-@pytest.mark.parametrize("T,H,I,act", [(2050, 2072, 4104, "silu"), (4200, 2056, 2008, "gelu")])
+# sizes at which each product takes the large tiles, ending inside them, and
+# few tokens with more weight-gradient tiles than one grid takes
+@pytest.mark.parametrize("T,H,I,act", [(2050, 2072, 4104, "silu"), (4200, 2056, 2008, "gelu"),
+                                       (13, 2056, 5512, "silu"), (40, 2056, 5512, "gelu")])
 def test_large_block(T, H, I, act):
     """The same bounds with the 64-bit products formed on the GPU."""
     import lora_moe_amd as lm
