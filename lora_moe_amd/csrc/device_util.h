@@ -31,6 +31,17 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+// v as the sum of two bf16, 16 bits of it: hi is v rounded, but never to an
+// infinity that v is not (between the largest bf16 and 2^128 the remainder
+// takes the rest).  An infinity or NaN goes to hi alone.
+__device__ __forceinline__ void f32_to_bf16_pair(float v, uint16_t* hi, uint16_t* lo) {
+  const bool finite = (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u;
+  uint16_t h = __builtin_bit_cast(uint16_t, (__bf16)v);
+  if (finite && (h & 0x7fffu) == 0x7f80u) h -= 1;  // the largest bf16
+  *hi = h;
+  *lo = finite ? __builtin_bit_cast(uint16_t, (__bf16)(v - bf16_to_f32(h))) : (uint16_t)0;
+}
+
 // D(16x16, fp32) += A(16x32, bf16) * B(32x16, bf16) on one wavefront.
 // Lane l supplies A[m = l%16][k = 8*(l/16) .. +8] and B[k = 8*(l/16) .. +8][n = l%16];
 // it receives D[m = 4*(l/16) + i][n = l%16], i = 0..3.  Only the pairing of

@@ -183,19 +183,19 @@ __device__ __forceinline__ void store8(uint16_t* p, const float* v) {
   *reinterpret_cast<u32x4_t*>(p) = o;
 }
 
-// what rounding to bf16 takes off (in place)
-__device__ __forceinline__ float remainder1(float v, float hi) {
-  const float r = v - hi;
-  return r == r ? r : 0.f;  // infinities have none
-}
-__device__ __forceinline__ const float* remainder8(float* v) {
+// 8 values as sums of two bf16
+__device__ __forceinline__ void store8_pair(uint16_t* hi, uint16_t* lo, const float* v) {
+  u32x4_t a, b;
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const uint32_t r = f32x2_to_bf16(v[i], v[i + 1]);
-    v[i] = remainder1(v[i], bf16_lo(r));
-    v[i + 1] = remainder1(v[i + 1], bf16_hi(r));
+  for (int i = 0; i < 4; ++i) {
+    uint16_t h[2], l[2];
+    f32_to_bf16_pair(v[2 * i], h, l);
+    f32_to_bf16_pair(v[2 * i + 1], h + 1, l + 1);
+    a[i] = h[0] | (uint32_t)h[1] << 16;
+    b[i] = l[0] | (uint32_t)l[1] << 16;
   }
-  return v;
+  *reinterpret_cast<u32x4_t*>(hi) = a;
+  *reinterpret_cast<u32x4_t*>(lo) = b;
 }
 
 // g and u of 8 neighbouring outputs, as the forward kept them
@@ -234,14 +234,17 @@ __device__ __forceinline__ void finish(const FfnGemm& p, int m, int n, const f32
       v[q] = dh * k * da;
       w[q] = dh * act;
     }
-    store8(p.out + (int64_t)m * 2 * p.N + n, v);
-    store8(p.out + (int64_t)m * 2 * p.N + p.N + n, w);
-    store8(p.out2 + (int64_t)m * p.N + n, h);
+    uint16_t* dg = p.out + (int64_t)m * 2 * p.N + n;
+    uint16_t* ho = p.out2 + (int64_t)m * p.N + n;
     if (p.pair) {
-      const int64_t lo = m + p.M;
-      store8(p.out + lo * 2 * p.N + n, remainder8(v));
-      store8(p.out + lo * 2 * p.N + p.N + n, remainder8(w));
-      store8(p.out2 + lo * p.N + n, remainder8(h));
+      const int64_t lo = (int64_t)p.M * p.N;
+      store8_pair(dg, dg + 2 * lo, v);
+      store8_pair(dg + p.N, dg + 2 * lo + p.N, w);
+      store8_pair(ho, ho + lo, h);
+    } else {
+      store8(dg, v);
+      store8(dg + p.N, w);
+      store8(ho, h);
     }
   } else {
 #pragma unroll

@@ -57,16 +57,13 @@ struct RowsArgs {
 
 __device__ __forceinline__ void rows_store(const RowsArgs& p, bool gated, int m, int n, float a, float u) {
   const float r = gated ? gate_act<false>(p.act, a, nullptr) * u : a;
-  const uint16_t hi = f32_to_bf16(r);
-  p.out[(int64_t)m * p.N + n] = hi;
+  const int64_t at = (int64_t)m * p.N + n;
   if (gated && p.gu) {
     p.gu[(int64_t)m * 2 * p.N + n] = a;
     p.gu[(int64_t)m * 2 * p.N + p.N + n] = u;
   }
-  if (gated && p.out_lo) {
-    const float lo = r - bf16_to_f32(hi);
-    p.out_lo[(int64_t)m * p.N + n] = lo == lo ? f32_to_bf16(lo) : (uint16_t)0;  // infinities have none
-  }
+  if (gated && p.out_lo) f32_to_bf16_pair(r, p.out + at, p.out_lo + at);
+  else p.out[at] = f32_to_bf16(r);
 }
 
 __device__ __forceinline__ u32x4_t rows_load(const void* base, uint32_t bytes, uint32_t voff, uint32_t soff) {

@@ -1,0 +1,45 @@
+"""Calls of the dense operators at the edges of what their contracts allow."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T", [1, 8, 9, 16])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_pairs_between_the_ranges(T, sign):
+    """h, dg or du within fp32's range and past bf16's (2^128 - 2^116): as a
+    sum of two bf16 each is finite, and so is what takes half of it, 2^127 -
+    2^115, which rounds to 2^127."""
+    import lora_moe_amd as lm
+    H, I = 64, 64
+    z = lambda *d: torch.zeros(d, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    x, W_gu, W_down = z(T, H), z(2 * I, H), z(H, I)
+    x[:, 0], x[:, 1] = 2.0 ** 62, 2.0 ** 52
+    W_gu[5, 0] = 4  # g = 2^64
+    W_gu[I + 5, 0], W_gu[I + 5, 1] = 4 * sign, -sign  # u = 2^64 - 2^52
+    W_down[:, 5] = 0.5
+    shape = lm.make_ffn_shape(T, H, I)
+    ws = lm.alloc_ffn_workspace(shape)
+    y, gu = z(T, H), torch.empty((T, 2 * I), device="cuda")
+    for kept in (gu, None):
+        lm.moe_lora_ffn_forward(shape, x, W_gu, W_down, ws, y, gu=kept)
+        assert (y == sign * 2.0 ** 127).all(), y
+    assert (gu[:, 5] == 2.0 ** 64).all() and (gu[:, I + 5] == sign * (2.0 ** 64 - 2.0 ** 52)).all()
+    # dh = 2^64: dg = du = h in size; a token each (or token 0's alone) in the weights' gradients
+    dy, dx, dW_gu, dW_down = z(T, H), z(T, H), z(2 * I, H), z(H, I)
+    dy[0, 3] = 2.0 ** 65
+    x = z(T, H)
+    x[0, 7] = 0.5
+    gu = torch.zeros((T, 2 * I), device="cuda")
+    gu[:, 5], gu[:, I + 5] = 2.0 ** 64 - 2.0 ** 52, sign * (2.0 ** 64 - 2.0 ** 52)
+    W_gu = z(2 * I, H)
+    W_gu[5, 11] = W_gu[I + 5, 12] = 0.5
+    lm.moe_lora_ffn_backward(shape, dy, x, gu, W_gu, W_down, ws, dx=dx, dW_gu=dW_gu)
+    assert dx[0, 11] == sign * 2.0 ** 127 and dx[0, 12] == 2.0 ** 127, dx[0, 11:13]
+    assert dW_gu[5, 7] == sign * 2.0 ** 127 and dW_gu[I + 5, 7] == 2.0 ** 127
+    # h = g u = 2^128 - 2^116 beside a dy of one half
+    gu[:, 5] = 2.0 ** 64
+    dy[0, 3] = 0.5
+    lm.moe_lora_ffn_backward(shape, dy, x, gu, W_gu, W_down, ws, dW_down=dW_down)
+    assert dW_down[3, 5] == sign * 2.0 ** 127, dW_down[3, 5]
