@@ -109,8 +109,10 @@ int moe_lora_ffn_backward(const moe_lora_ffn_shape* shape, const uint16_t* dy, c
                           uint16_t* dx, uint16_t* dW_gu, uint16_t* dW_down, void* stream) {
   const int rc = check_shape(shape);
   if (rc) return rc;
-  // (without tokens dx is empty and may be NULL)
-  if (shape->T > 0 && !dx && !dW_gu && !dW_down) return MOE_LORA_EINVAL;
+  // without tokens dx is empty, whatever its address, and only the weights'
+  // gradients are left to write
+  if (shape->T == 0) dx = nullptr;
+  else if (!dx && !dW_gu && !dW_down) return MOE_LORA_EINVAL;
   const int T = shape->T, H = shape->H, I = shape->I;
   const Sizes z(*shape);
   const size_t need = T > 0 ? ws_bytes_of(*shape, true) : 0;

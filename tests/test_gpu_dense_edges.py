@@ -1,4 +1,6 @@
 """Calls of the dense operators at the edges of what their contracts allow."""
+import ctypes
+
 import pytest
 import torch
 
@@ -43,3 +45,23 @@ def test_pairs_between_the_ranges(T, sign):
     dy[0, 3] = 0.5
     lm.moe_lora_ffn_backward(shape, dy, x, gu, W_gu, W_down, ws, dW_down=dW_down)
     assert dW_down[3, 5] == sign * 2.0 ** 127, dW_down[3, 5]
+
+
+@pytest.mark.parametrize("H,I", [(72, 40), (2056, 5512)])
+def test_no_tokens_with_an_address_for_dx(H, I):
+    """T = 0 from C with all three gradients: the weights' are zeros, dx is
+    empty and what lies at its address stays."""
+    import lora_moe_amd as lm
+    lib = lm.load_library()
+    W_gu, W_down = (torch.full(s, 2.0, dtype=torch.bfloat16, device="cuda") for s in ((2 * I, H), (H, I)))
+    dW_gu, dW_down = torch.full_like(W_gu, 3.0), torch.full_like(W_down, 3.0)
+    there = torch.full((256,), 7.0, dtype=torch.bfloat16, device="cuda")
+    shape = lm.make_ffn_shape(0, H, I)
+    stream = torch.cuda.current_stream().cuda_stream
+    for dx in (there.data_ptr(), None):
+        rc = lib.moe_lora_ffn_backward(ctypes.byref(shape), None, None, None, W_gu.data_ptr(), W_down.data_ptr(),
+                                       None, 0, dx, dW_gu.data_ptr(), dW_down.data_ptr(), stream)
+        assert rc == lm.MOE_LORA_OK
+        assert not dW_gu.any() and not dW_down.any() and (there == 7).all()
+        dW_gu.fill_(3.0)
+        dW_down.fill_(3.0)
