@@ -411,8 +411,9 @@ int moe_lora_w4_pack(const moe_lora_w4* w, const uint8_t* q, const uint16_t* sca
 int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, void* workspace, size_t ws_bytes,
                        uint16_t* y, void* stream);
 
-/* Bytes of workspace that moe_lora_w4_matmul needs for M rows (0 when w or M
- * is invalid).  Host only, pure. */
+/* Bytes of workspace that moe_lora_w4_matmul needs for M rows: 0 when w or M
+ * is invalid, 256 exactly when the call uses none (workspace may then be
+ * NULL), else at least 512.  Host only, pure. */
 size_t moe_lora_w4_workspace_bytes(const moe_lora_w4* w, int32_t M);
 
 /* The gated block on 4-bit weights: h = act(x gate^T) * (x up^T), y = h

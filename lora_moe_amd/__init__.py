@@ -688,7 +688,7 @@ def moe_lora_w4_matmul(x, w: W4Weight, y, workspace=None, stream=None) -> None:
     if workspace is not None:
         specs.append(_check_workspace(workspace, need, "moe_lora_w4_workspace_bytes"))
     _check_tensors(specs)
-    if workspace is None and need > 256:  # 256: nothing is written
+    if workspace is None and need > 256:  # 256: none is used
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
         _used_on(stream, workspace)
     _check("moe_lora_w4_matmul", load_library().moe_lora_w4_matmul(

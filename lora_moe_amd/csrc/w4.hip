@@ -266,8 +266,9 @@ int moe_lora_w4_pack(const moe_lora_w4* w, const uint8_t* q, const uint16_t* sca
 size_t moe_lora_w4_workspace_bytes(const moe_lora_w4* w, int32_t M) {
   W4Layout L;
   if (check_matrix(w, &L) || M < 0 || M > kMaxRows) return 0;
-  const size_t n = M ? round256(slab_bytes(L, M)) : 0;
-  return n ? n : 256;
+  // 256 says that nothing is needed, so slabs of a few bytes count as more
+  const size_t n = M ? slab_bytes(L, M) : 0;
+  return n ? std::max<size_t>(round256(n), 512) : 256;
 }
 
 int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, void* workspace, size_t ws_bytes,

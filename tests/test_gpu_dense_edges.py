@@ -4,6 +4,8 @@ import ctypes
 import pytest
 import torch
 
+from dense_common import w4_bounds, w4_inputs, w4_values, within
+
 pytestmark = pytest.mark.gpu
 
 
@@ -65,3 +67,18 @@ def test_no_tokens_with_an_address_for_dx(H, I):
         assert not dW_gu.any() and not dW_down.any() and (there == 7).all()
         dW_gu.fill_(3.0)
         dW_down.fill_(3.0)
+
+
+@pytest.mark.parametrize("N,M,K", [(1, 9, 1024), (2, 9, 2048), (3, 10, 896), (1, 32, 1024), (2, 16, 1024),
+                                   (5, 32, 1024)])
+def test_few_outputs_without_a_workspace(N, M, K):
+    """K split over the grid with slabs of a few bytes: the binding finds
+    their memory."""
+    import lora_moe_amd as lm
+    parts = w4_inputs(N, K, 128, False, N + K)
+    w = lm.moe_lora_w4_pack(parts[0].cuda(), parts[1].cuda(), group=128)
+    x = torch.randn((M, K), generator=torch.Generator().manual_seed(M)).bfloat16()
+    y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lm.moe_lora_w4_matmul(x.cuda(), w, y)
+    want, _, bound = w4_bounds(x.double(), *w4_values(*parts, 128))
+    within(y, want, bound, f"M={M} N={N} K={K}")
