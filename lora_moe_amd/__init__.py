@@ -534,6 +534,24 @@ def _check_tensors(specs) -> None:
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
+def _allocated_on(stream, make, returned=False):
+    """What make() allocates, as memory of ``stream``: the allocator hands a
+    block of one stream to the next user in that stream's order alone, so
+    memory that work on ``stream`` writes has to come from its own pool, both
+    when it is taken (earlier users may still run) and when it is let go.
+    returned: the caller uses it on the current stream afterwards."""
+    import torch
+    if stream is None or _stream(stream) == _stream(None):
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream))
+    with torch.cuda.stream(stream):
+        t = make()
+    if returned:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _used_on(stream, *tensors) -> None:
     """Tensors allocated here for the current stream and used on ``stream``:
     their memory is not handed out again before that stream has passed them."""
@@ -618,11 +636,9 @@ def gated_ffn(x, W_gu, W_down, act="silu", workspace=None, y=None, stream=None):
             raise ValueError(f"{name}: {t.dim()} dimensions, expected 2")
     shape = make_ffn_shape(x.shape[0], x.shape[1], W_gu.shape[0] // 2, act)
     if workspace is None:
-        workspace = alloc_ffn_workspace(shape, False, x.device)
-        _used_on(stream, workspace)
+        workspace = _allocated_on(stream, lambda: alloc_ffn_workspace(shape, False, x.device))
     if y is None:
-        y = torch.empty_like(x)
-        _used_on(stream, y)
+        y = _allocated_on(stream, lambda: torch.empty_like(x), returned=True)
     moe_lora_ffn_forward(shape, x, W_gu, W_down, workspace, y, stream=stream)
     return y
 
@@ -665,8 +681,8 @@ def moe_lora_w4_pack(q, scales, zeros=None, group=128, stream=None) -> W4Weight:
     if zeros is not None:
         specs.append(("zeros", zeros, (N, G), "uint8"))
     _check_tensors(specs)
-    w.packed = torch.empty(n, dtype=torch.uint8, device=q.device)
-    _used_on(stream, w.packed)
+    w.packed = _allocated_on(stream, lambda: torch.empty(n, dtype=torch.uint8, device=q.device),
+                             returned=True)
     w.desc.data = w.packed.data_ptr()
     _check("moe_lora_w4_pack", load_library().moe_lora_w4_pack(
         ctypes.byref(w.desc), q.data_ptr(), scales.data_ptr(),
@@ -689,8 +705,8 @@ def moe_lora_w4_matmul(x, w: W4Weight, y, workspace=None, stream=None) -> None:
         specs.append(_check_workspace(workspace, need, "moe_lora_w4_workspace_bytes"))
     _check_tensors(specs)
     if workspace is None and need > 256:  # 256: none is used
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        _used_on(stream, workspace)
+        workspace = _allocated_on(
+            stream, lambda: torch.empty(need, dtype=torch.uint8, device=x.device))
     _check("moe_lora_w4_matmul", load_library().moe_lora_w4_matmul(
         ctypes.byref(w.desc), M, x.data_ptr(), None if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.numel(), y.data_ptr(), _stream(stream)))

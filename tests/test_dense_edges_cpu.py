@@ -3,6 +3,7 @@ without a GPU."""
 import ctypes
 
 import pytest
+import torch
 
 import lora_moe_amd as lm
 
@@ -22,3 +23,86 @@ def test_slabs_of_a_few_bytes_are_asked_for(N, M, K):
                                                 None)
     assert call(None, 0) == lm.MOE_LORA_EWORKSPACE and call(BASE + 3 * STEP, 0) == lm.MOE_LORA_EWORKSPACE
     assert need >= 512
+
+
+class FakeStream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+class FakeTensor:
+    """Memory of the stream that was current when it was allocated."""
+    dtype, device, is_cuda = torch.uint8, torch.device("cuda", 0), True
+
+    def __init__(self, shape, pool):
+        self.shape, self.pool, self.used_on = tuple(shape), pool, set()
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return int(torch.Size(self.shape).numel())
+
+    def data_ptr(self):
+        return id(self)
+
+    def detach(self):
+        return self
+
+    def record_stream(self, stream):
+        self.used_on.add(stream.cuda_stream)
+
+
+class Streams:
+    """Stands in for the GPU's streams and allocator; made: what the code
+    under test allocated; calls: the stream of each library call."""
+
+    def __init__(self, monkeypatch):
+        self.now, self.made, self.calls = 3, [], []
+        outer = self
+
+        class Scope:
+            def __init__(self, stream):
+                self.stream = stream
+
+            def __enter__(self):
+                self.before, outer.now = outer.now, self.stream.cuda_stream
+
+            def __exit__(self, *exc):
+                outer.now = self.before
+
+        class Library:
+            def __getattr__(self, name):
+                if name.endswith("_bytes"):
+                    return lambda *a: 4096
+                return lambda *a: outer.calls.append(a[-1]) or 0
+
+        def empty(shape, *more, **kw):
+            t = FakeTensor((shape,) if isinstance(shape, int) else shape, outer.now)
+            outer.made.append(t)
+            return t
+
+        monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", FakeStream)
+        monkeypatch.setattr(torch.cuda, "stream", Scope)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: FakeStream(outer.now))
+        monkeypatch.setattr(torch, "empty", empty)
+        monkeypatch.setattr(torch, "empty_like", lambda t: empty(t.shape))
+        monkeypatch.setattr(lm, "load_library", lambda *a: Library())
+        monkeypatch.setattr(lm, "_check_tensors", lambda specs: None)
+        monkeypatch.setattr(lm, "_stream", lambda s: outer.now if s is None else getattr(s, "cuda_stream", s))
+
+
+@pytest.mark.parametrize("stream", [FakeStream(7), 7, FakeStream(3), 3, None])
+def test_buffers_are_memory_of_the_stream_that_writes_them(monkeypatch, stream):
+    s = Streams(monkeypatch)
+    want = 3 if stream is None else getattr(stream, "cuda_stream", stream)
+    t = lambda *shape: FakeTensor(shape, 3)  # noqa: E731
+    w = lm.moe_lora_w4_pack(t(64, 32), t(64, 1), group=64, stream=stream)
+    y = lm.gated_ffn(t(4, 64), t(64, 64), t(64, 32), stream=stream)
+    lm.moe_lora_w4_matmul(t(4, 64), w, t(4, 64), stream=stream)
+    assert s.calls == [want] * 3 and len(s.made) == 4
+    assert [m.pool for m in s.made] == [want] * 4
+    if want != 3:  # what the caller gets is also used on the stream that is current there
+        assert w.packed.used_on == {3} and y.used_on == {3}
+    assert s.now == 3

@@ -4,7 +4,7 @@ import ctypes
 import pytest
 import torch
 
-from dense_common import w4_bounds, w4_inputs, w4_values, within
+from dense_common import ffn_inputs, w4_bounds, w4_inputs, w4_values, within
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +82,36 @@ def test_few_outputs_without_a_workspace(N, M, K):
     lm.moe_lora_w4_matmul(x.cuda(), w, y)
     want, _, bound = w4_bounds(x.double(), *w4_values(*parts, 128))
     within(y, want, bound, f"M={M} N={N} K={K}")
+
+
+def pool_of(t):
+    """The stream whose memory the allocator gave to t."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+@pytest.mark.parametrize("by_handle", [False, True])
+def test_buffers_are_memory_of_the_stream_that_writes_them(by_handle):
+    """On another stream, given as an object or by its handle, results are
+    that stream's memory, and right; on the current one they are its own."""
+    import lora_moe_amd as lm
+    x, W_gu, W_down, _ = (t.cuda() for t in ffn_inputs(40, 136, 200, 3))
+    parts = [t.cuda() for t in w4_inputs(300, 2048, 64, True, 4)]
+    rows = torch.randn((20, 2048), generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    want = []
+    for s in (None, torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        st = s.cuda_stream if s and by_handle else s
+        y, w = lm.gated_ffn(x, W_gu, W_down, stream=st), lm.moe_lora_w4_pack(*parts, group=64, stream=st)
+        here = torch.cuda.current_stream().cuda_stream
+        for t in (y, w.packed):
+            assert pool_of(t) == (s.cuda_stream if s else here)
+        out = torch.zeros((20, 300), dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        lm.moe_lora_w4_matmul(rows, w, out, stream=st)
+        torch.cuda.synchronize()
+        want.append((y, w.packed, out))
+        assert torch.cuda.current_stream().cuda_stream == here
+    for a, b in zip(*want):
+        assert torch.equal(a, b)
