@@ -552,17 +552,6 @@ def _allocated_on(stream, make, returned=False):
     return t
 
 
-def _used_on(stream, *tensors) -> None:
-    """Tensors allocated here for the current stream and used on ``stream``:
-    their memory is not handed out again before that stream has passed them."""
-    if stream is not None:
-        import torch
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(_stream(stream))
-        for t in tensors:
-            t.record_stream(stream)
-
-
 def _check_workspace(workspace, need: int, what: str):
     if workspace is None:
         raise ValueError(f"workspace is required ({what})")
@@ -742,7 +731,9 @@ class GradSet:
     and listed once, kept as long as the program uses these tensors (a tensor
     that is given other memory, by ``.data = ``, needs a new set).  out: where
     the clipped gradients go (like ``grads``); None: in place.  A set has one
-    workspace: its calls follow one another."""
+    workspace for each stream that it is used on, kept as long as the set: its
+    calls on one stream follow one another, as do the replays of the graphs
+    that it was captured into on one stream."""
 
     def __init__(self, grads, out=None):
         import torch
@@ -763,12 +754,20 @@ class GradSet:
         _check_tensors(specs)
         # the listed memory stays allocated, whatever the tensors become
         self._held = [t.detach() for t in self.grads + self.out]
-        need = moe_lora_clip_workspace_bytes(n)
-        device = self.grads[0].device if n else "cuda"
-        self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        self._workspaces = {}  # by the stream's handle
 
     def __len__(self):
         return len(self.grads)
+
+    def _workspace(self, stream):
+        handle = _stream(stream)
+        if handle not in self._workspaces:
+            import torch
+            need = moe_lora_clip_workspace_bytes(len(self.grads))
+            device = self.grads[0].device if self.grads else "cuda"
+            self._workspaces[handle] = _allocated_on(
+                stream, lambda: torch.empty(need, dtype=torch.uint8, device=device))
+        return self._workspaces[handle]
 
 
 def moe_lora_clip_workspace_bytes(n: int) -> int:
@@ -781,11 +780,11 @@ def moe_lora_clip_grads(grads, max_norm: float, norm, stream=None) -> None:
     ([1] fp32, device).  max_norm = inf: the norm only (with out: a copy)."""
     if not isinstance(grads, GradSet):
         grads = GradSet(grads)
-    _used_on(stream, grads.workspace)
-    _check_tensors([("norm", norm, (1,), "float32"), ("workspace", grads.workspace, None, "uint8")])
+    workspace = grads._workspace(stream)
+    _check_tensors([("norm", norm, (1,), "float32"), ("workspace", workspace, None, "uint8")])
     _check("moe_lora_clip_grads", load_library().moe_lora_clip_grads(
-        grads._arr, len(grads), float(max_norm), norm.data_ptr(), grads.workspace.data_ptr(),
-        grads.workspace.numel(), _stream(stream)))
+        grads._arr, len(grads), float(max_norm), norm.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _stream(stream)))
 
 
 __all__ = [n for n in dir() if n.startswith("moe_lora") or n in (

@@ -106,3 +106,25 @@ def test_buffers_are_memory_of_the_stream_that_writes_them(monkeypatch, stream):
     if want != 3:  # what the caller gets is also used on the stream that is current there
         assert w.packed.used_on == {3} and y.used_on == {3}
     assert s.now == 3
+
+
+def test_a_set_of_gradients_has_a_workspace_for_each_stream(monkeypatch):
+    """Listed on one stream and clipped on others, given or current: each
+    call writes memory of its own stream, and the same one every time."""
+    s = Streams(monkeypatch)
+    g = FakeTensor((8,), 3)
+    g.dtype = torch.float32
+    norm, seen = FakeTensor((1,), 3), []
+    library = lm.load_library()
+    monkeypatch.setattr(type(library), "moe_lora_clip_grads", lambda self, *a: seen.append((a[4], a[6])) or 0,
+                        raising=False)
+    gs = lm.GradSet([g])
+    for now, given in ((3, None), (3, 7), (9, None), (3, None), (9, 7), (3, 9)):
+        s.now = now
+        lm.moe_lora_clip_grads(gs, 1.0, norm, stream=given)
+    pools = {m.data_ptr(): m.pool for m in s.made}
+    assert [pools[ws] for ws, _ in seen] == [stream for _, stream in seen] == [3, 7, 9, 3, 7, 9]
+    assert len(s.made) == 3
+    s.now = 3
+    lm.moe_lora_clip_grads([g], 1.0, norm, stream=11)
+    assert s.made[-1].pool == 11 and seen[-1] == (s.made[-1].data_ptr(), 11)

@@ -115,3 +115,38 @@ def test_buffers_are_memory_of_the_stream_that_writes_them(by_handle):
         assert torch.cuda.current_stream().cuda_stream == here
     for a, b in zip(*want):
         assert torch.equal(a, b)
+
+
+def test_a_set_of_gradients_on_several_streams():
+    """One set, clipped on the current stream, under others and captured:
+    the same norm everywhere, and each stream's partial sums in memory of its
+    own, which replays use after the eager calls' has changed."""
+    import lora_moe_amd as lm
+    gen = torch.Generator().manual_seed(6)
+    grads = [torch.randn(n, generator=gen).cuda() for n in (5000, 33, 70000)]
+    outs = [torch.empty_like(t) for t in grads]
+    gs = lm.GradSet(grads, outs)
+    norms = torch.zeros((4, 1), device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    lm.moe_lora_clip_grads(gs, 2.0, norms[0])
+    want = [t.clone() for t in outs]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(streams[0]):
+        lm.moe_lora_clip_grads(gs, 2.0, norms[1])
+    torch.cuda.synchronize()
+    lm.moe_lora_clip_grads(gs, 2.0, norms[2], stream=streams[1].cuda_stream)
+    torch.cuda.synchronize()
+    handles = [torch.cuda.current_stream().cuda_stream] + [s.cuda_stream for s in streams]
+    assert [pool_of(gs._workspace(h)) for h in handles] == handles
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lm.moe_lora_clip_grads(gs, 2.0, norms[3])
+    for rep in range(3):
+        lm.moe_lora_clip_grads([grads[1].clone()], 2.0, torch.empty(1, device="cuda"))
+        norms[3].zero_()
+        for t in outs:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(n, norms[0]) for n in norms), (rep, norms)
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
