@@ -489,9 +489,10 @@ def fused_moe_lora(x, topk_ids, topk_weights, lora_ids, W_gu, W_down, A_gu, B_gu
     check_operands(shape, x=x, topk_ids=topk_ids, topk_weights=topk_weights, lora_ids=lora_ids,
                    W_gu=W_gu, W_down=W_down, A_gu=A_gu, B_gu=B_gu, A_down=A_down, B_down=B_down)
     if workspace is None:
-        workspace = alloc_workspace(shape, x.device)
+        workspace = _allocated_on(stream, lambda: alloc_workspace(shape, x.device))
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        y = _allocated_on(stream, lambda: torch.empty((T, H), dtype=torch.bfloat16, device=x.device),
+                          returned=True)
     moe_lora_align(shape, topk_ids, lora_ids, workspace, stream)
     moe_lora_forward(shape, x, topk_ids, topk_weights, lora_ids, W_gu, W_down, A_gu, B_gu, A_down,
                      B_down, workspace, y, stream)

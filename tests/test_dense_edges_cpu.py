@@ -128,3 +128,17 @@ def test_a_set_of_gradients_has_a_workspace_for_each_stream(monkeypatch):
     s.now = 3
     lm.moe_lora_clip_grads([g], 1.0, norm, stream=11)
     assert s.made[-1].pool == 11 and seen[-1] == (s.made[-1].data_ptr(), 11)
+
+
+@pytest.mark.parametrize("stream", [FakeStream(7), 7, None])
+def test_the_layer_in_one_call_allocates_on_its_stream(monkeypatch, stream):
+    s = Streams(monkeypatch)
+    monkeypatch.setattr(lm, "check_operands", lambda *a, **kw: None)
+    t = lambda *shape: FakeTensor(shape, 3)  # noqa: E731
+    streams = []
+    monkeypatch.setattr(lm, "moe_lora_align", lambda *a: streams.append(a[-1]))
+    monkeypatch.setattr(lm, "moe_lora_forward", lambda *a: streams.append(a[-1]))
+    y = lm.fused_moe_lora(t(4, 64), t(4, 2), t(4, 2), t(4), t(8, 64, 64), t(8, 64, 32), t(2, 8, 16, 64),
+                          t(2, 8, 64, 16), t(2, 8, 16, 32), t(2, 8, 64, 16), stream=stream)
+    want = 3 if stream is None else 7
+    assert streams == [stream] * 2 and [m.pool for m in s.made] == [want] * 2 and y is s.made[1]
