@@ -30,14 +30,19 @@ constexpr int BK = 64;  // K depth of a stage
 // the compiler takes every later LDS read for a read of this copy's target
 // and waits for the copy first.  Callers wait themselves.  Resource, offset
 // and m0 come from scalar arithmetic, which needs no wait states before a
-// vector memory operation, and one between m0 and a copy into LDS.
+// vector memory operation, and one between m0 and a copy into LDS.  m0 is
+// named as overwritten; that the compiler never keeps values of its own in it
+// (a "reserved" register, says its warning) is what lets the block set it.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <int IMM>
 __device__ __forceinline__ void copy16(u32x4_t rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
   asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff), "n"(IMM)
-               : "memory", "scc");
+               : "memory", "scc", "m0");
 }
+#pragma clang diagnostic pop
 
 __device__ __forceinline__ u32x4_t rsrc_of(const void* base, uint32_t bytes) {
   const uint64_t b = (uint64_t)base;

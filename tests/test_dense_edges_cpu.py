@@ -1,6 +1,9 @@
 """The dense operators' host side at the edges of what their contracts allow,
 without a GPU."""
 import ctypes
+import os
+import re
+import subprocess
 
 import pytest
 import torch
@@ -142,3 +145,50 @@ def test_the_layer_in_one_call_allocates_on_its_stream(monkeypatch, stream):
                           t(2, 8, 64, 16), t(2, 8, 16, 32), t(2, 8, 64, 16), stream=stream)
     want = 3 if stream is None else 7
     assert streams == [stream] * 2 and [m.pool for m in s.made] == [want] * 2 and y is s.made[1]
+
+
+CSRC = os.path.join(lm.PKG, "csrc")
+
+
+def test_assembly_names_the_registers_it_sets():
+    """A block of assembly that sets m0 says so to the compiler."""
+    found = 0
+    for name in sorted(os.listdir(CSRC)):
+        with open(os.path.join(CSRC, name)) as f:
+            text = f.read()
+        for block in re.findall(r"\basm\s*(?:volatile)?\s*\((.*?)\);", text, re.S):
+            if re.search(r"\bs_\w+ m0\b", block):
+                found += 1
+                assert '"m0"' in block.rsplit(":", 1)[1], (name, block)
+    assert found
+
+
+def test_copies_keep_their_distance_from_vector_writes(tmp_path):
+    """A vector instruction that writes a scalar register needs five wait
+    states before a memory instruction that reads it; the compiler does not
+    see into the copies' assembly, so what it puts before them is checked."""
+    from lora_moe_amd import build
+    out = str(tmp_path / "ffn_gemm.s")
+    subprocess.run([build.HIPCC, *build.FLAGS, "-w", "-S", "--cuda-device-only",
+                    os.path.join(CSRC, "ffn_gemm.hip"), "-o", out], check=True, capture_output=True)
+
+    def scalars(text):
+        regs = {int(n) for n in re.findall(r"\bs(\d+)\b", text)}
+        for a, b in re.findall(r"\bs\[(\d+):(\d+)\]", text):
+            regs |= set(range(int(a), int(b) + 1))
+        return regs
+
+    before, copies = [], 0
+    with open(out) as f:
+        for line in f:
+            ins = line.split(";")[0].strip()
+            if not ins or ins.startswith(".") or ins.endswith(":"):
+                continue
+            if ins.startswith("buffer_load") and ins.endswith(" lds"):
+                copies += 1
+                for w in before:
+                    if w.startswith("v_") and not w.startswith("v_mfma"):
+                        written = ",".join(w.split(",")[:2 if "_co_" in w else 1])
+                        assert not scalars(written) & scalars(ins), (w, ins)
+            before = before[-4:] + [ins]
+    assert copies > 500
