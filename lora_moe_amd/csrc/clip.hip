@@ -8,9 +8,8 @@
 // every workgroup (in the same order, so c is the same everywhere and from
 // run to run) and scales.  Both are bound by memory; the second goes through
 // the chunks backwards, so that what the first read last is still in the 256
-// MB cache beside the HBM.  Sums are fp64 of fp32 sums of one 16-byte piece,
-// redone in fp64 where that leaves fp32's range: squares cannot overflow or
-// vanish, and the order of addition does not show in fp32.
+// MB cache beside the HBM.  Squares and sums are fp64: squares cannot overflow
+// or vanish, and the order of addition does not show in fp32.
 //
 // Measured: 541 M bf16 gradients (1.08 GB) 181 us for the norm, 6.0 TB/s, and
 // 420 for the second pass, 5.1 TB/s (1.08 GB read, as much written); 224
@@ -82,14 +81,9 @@ struct Piece {
     }
   }
   __device__ __forceinline__ double squares() const {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) s += v[i] * v[i];
-    // in fp32's range, no square that matters beside the others was lost
-    if (s > 1e-30f && s < 1e38f) return (double)s;
     double d = 0.;
 #pragma unroll
-    for (int i = 0; i < N; ++i) d += (double)v[i] * (double)v[i];
+    for (int i = 0; i < N; ++i) d = fma((double)v[i], (double)v[i], d);
     return d;
   }
   __device__ __forceinline__ u32x4_t scaled(float c) const {

@@ -1,5 +1,6 @@
 """Calls of the dense operators at the edges of what their contracts allow."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -150,3 +151,21 @@ def test_a_set_of_gradients_on_several_streams():
         torch.cuda.synchronize()
         assert all(torch.equal(n, norms[0]) for n in norms), (rep, norms)
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_norm_of_a_few_elements(dtype):
+    """Sums of squares are fp64: the norm of the 1 to 9 elements around one
+    16-byte piece is off by its own rounding to fp32 alone, draw for draw."""
+    import lora_moe_amd as lm
+    gen = torch.Generator().manual_seed(11)
+    n = 4 if dtype is torch.float32 else 8
+    for size in (1, n - 1, n, n + 1):
+        host = torch.randn((250, size), generator=gen).to(dtype)
+        norms = torch.empty((250, 1), device="cuda")
+        for t, norm in zip(host.cuda(), norms):
+            lm.moe_lora_clip_grads([t.clone()], math.inf, norm)
+        want = host.double().square().sum(1).sqrt()
+        worst = float(((norms[:, 0].double().cpu() - want).abs() / want).max())
+        print(f"{dtype} {size}: worst {worst * 2 ** 24:.3f} half steps", flush=True)
+        assert worst <= 2.0 ** -24 + 2.0 ** -40
