@@ -370,8 +370,7 @@ int moe_lora_ffn_forward(const moe_lora_ffn_shape* shape, const uint16_t* x, con
  *                    one of the three is wanted (where T > 0)
  * Gradients are overwritten (with zeros for T = 0), not added to.  dg, du and
  * h are rounded to bf16 once, before the products that take them (up to 16
- * tokens they are sums of two bf16).  The same
- * inputs give the same bits. */
+ * tokens they are sums of two bf16).  The same inputs give the same bits. */
 int moe_lora_ffn_backward(const moe_lora_ffn_shape* shape, const uint16_t* dy, const uint16_t* x, const float* gu,
                           const uint16_t* W_gu, const uint16_t* W_down, void* workspace, size_t ws_bytes,
                           uint16_t* dx, uint16_t* dW_gu, uint16_t* dW_down, void* stream);
@@ -404,10 +403,11 @@ int moe_lora_w4_pack(const moe_lora_w4* w, const uint8_t* q, const uint16_t* sca
  *   x          device [M][K] bf16, 16-byte aligned
  *   y          device [M][N] bf16, overwritten
  *   workspace  device, 16-byte aligned, ws_bytes >= moe_lora_w4_workspace_bytes(w, M)
- * The weights enter as integers and the scales in fp32, so y differs from
- * the exact product by its own rounding and that of fp32 sums.  x up to 1e34
- * in size; a row of x with an infinity or NaN gives a row of y that is not finite.  The same
- * inputs give the same bits. */
+ * The weights enter as integers 128 + q beside 128 + z and the scales in
+ * fp32, so y differs from the exact product by its own rounding and that of
+ * fp32 sums, at most (K + 8) 2^-24 sum |x| s (256 + q + z).  x up to 1e34 in
+ * size; a row of x with an infinity or NaN gives a row of y that is not
+ * finite.  The same inputs give the same bits. */
 int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, void* workspace, size_t ws_bytes,
                        uint16_t* y, void* stream);
 
@@ -417,8 +417,9 @@ int moe_lora_w4_matmul(const moe_lora_w4* w, int32_t M, const uint16_t* x, void*
 size_t moe_lora_w4_workspace_bytes(const moe_lora_w4* w, int32_t M);
 
 /* The gated block on 4-bit weights: h = act(x gate^T) * (x up^T), y = h
- * down^T, h rounded to bf16 (up to 16 rows: a sum of two).  gate and up are [I][H] alike in group and zero
- * points, down is [H][I]; I is a multiple of 8 as well.
+ * down^T, h rounded to bf16 (up to 16 rows: a sum of two).  gate and up are
+ * [I][H] alike in group and zero points, down is [H][I]; I is a multiple of 8
+ * as well.  x and h up to 1e34 in size.
  *   x, y  device [M][H] bf16   workspace  device, 16-byte aligned */
 size_t moe_lora_w4_ffn_workspace_bytes(int32_t M, int32_t I);
 int moe_lora_w4_ffn_forward(const moe_lora_w4* gate, const moe_lora_w4* up, const moe_lora_w4* down, int32_t M,

@@ -618,8 +618,11 @@ def moe_lora_ffn_backward(shape, dy, x, gu, W_gu, W_down, workspace, dx=None, dW
 
 
 def gated_ffn(x, W_gu, W_down, act="silu", workspace=None, y=None, stream=None):
-    """The block's forward on the current stream; returns y [T, H] (bf16).
-    x [T,H], W_gu [2I,H], W_down [H,I], all bf16."""
+    """The block's forward on the current stream (or ``stream``); returns y
+    [T, H] (bf16).  x [T,H], W_gu [2I,H], W_down [H,I], all bf16.  Like every
+    call here it records nothing for autograd, whatever its operands require:
+    a training program calls moe_lora_ffn_forward with gu and
+    moe_lora_ffn_backward itself."""
     import torch
     for name, t in (("x", x), ("W_gu", W_gu)):
         if t.dim() != 2:

@@ -37,17 +37,24 @@ struct FfnGemm {
   int splits;        // K splits, set by the launch
 };
 
-// Up to this many tokens a forward streams the weights (ffn_rows.hip); beyond
-// it the rows' side takes over and tiles are better.  Measured, us, streamed
-// and tiled: H 1024, I 2816, 24 tokens 20 and 22, 64 tokens 23 and 25; 2880,
-// 2880, 24 tokens 28 and 28, 64 tokens 36 and 32; 4096, 11008, 24 tokens 70
-// and 70, 33 tokens 75 and 73, 64 tokens 83 and 81.
+// Up to this many tokens a forward streams the weights (ffn_rows.hip), beyond
+// it takes tiles.  One limit for all sizes, between what small and what wide
+// blocks would rather have.  Measured, us, streamed and tiled, at 24, 33 and 64
+// tokens: H 1024, I 2816, 18 and 23, 21 and 23, 23 and 25; 2880, 2880, 26 and
+// 32, 28 and 33, 32 and 35; 4096, 11008, 70 and 78, 75 and 79, 83 and 86; 5120,
+// 25600, 179 and 157, 187 and 162, 197 and 177 (there tiles are better from 17
+// tokens on, 174 and 167).
 constexpr int kRowsMax = 32;
 // Up to this many, h, dg and du go from one product to the next as bf16 pairs
-// hi + lo, which costs nothing beside the weights.  With so few tokens a few
-// large values carry a result, so that one rounding more than its own can
-// show by more than its share (in 64-bit emulations of 1 to 3 tokens up to
-// 1.68 times a single rounding's error, from 17 on at most 1.48).
+// hi + lo: with so few tokens a few large values carry a result, so that one
+// rounding more than its own can show by more than its share (in 64-bit
+// emulations of 1 to 3 tokens up to 1.68 times a single rounding's error).  It
+// costs nothing beside the weights: the remainders lie in the same fragment of
+// 16 rows, or in a second one.  From 17 tokens on they are rounded once, as by
+// a layer that writes bf16 between its products: y and the gradients are then
+// off by 1.41 times their own rounding (relative L2 2.35e-3 against 1.66e-3),
+// at most 1.48 in the emulations, while pairs would double the operations of
+// the down, dx and weight-gradient products, which these bound in training.
 constexpr int kRowsPair = 16;
 
 // FFN_GATE_UP or FFN_DOWN of at most kRowsMax rows.  a_lo: the remainder of A

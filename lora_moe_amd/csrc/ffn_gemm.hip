@@ -560,8 +560,9 @@ typedef FfnCfg<128, 128, 2, 2> Small;
 // rounds of workgroups (256 large ones, or 512 small ones, two to a CU) and
 // their stages; a last round of small ones with a CU each is shorter; splits
 // cost a launch and the slabs' way to memory and back.  The constants (us)
-// are fitted to 2200 measured products of 65 to 8192 tokens, H 1024 to 5120,
-// I 2816 to 25600: the choice is 1.6 % above the best one on the mean.
+// are fitted to 2189 times of 386 products of 65 to 8192 tokens, H 1024 to
+// 5120, I 2816 to 25600: the choice is 1.6 % above the best one on the mean, and
+// furthest off, by 47 %, for dh of 256 tokens at H 1024, I 2816.
 struct FfnPlan {
   bool big;
   int splits;

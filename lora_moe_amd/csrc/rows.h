@@ -374,10 +374,12 @@ inline RowsPlan rows_plan(int M, int N, int K, int lines_per_chunk) {
   r.direct = M <= 8 && (2 * M <= lines_per_chunk / 2 || tiles * chunks * 2 * M * 128 < 5 * 7000000LL);
   if (r.direct) return r;
   // at most one workgroup per CU (256) where K is split, since a second round
-  // of a few would take as long as the first; 6 chunks each, where there are
-  // fewer the slabs cost more than they spare (us with 4, 6 and 8: 16 rows
-  // through the bf16 block, 2880 x 2880 27.1, 23.4, 26.1; 32 rows, 4 bits,
-  // 4096 x 4096 12.2, 11.5, 10.5; 64 rows, 1024 x 2048 9.3, 9.8, 10.9)
+  // of a few would take as long as the first; 6 chunks each, the best on the
+  // mean: with fewer the slabs cost more than they spare, with more too few
+  // workgroups are left in small matrices (us with 4, 6 and 8: 16 rows through
+  // the bf16 block, 2880 x 2880 27.4, 24.4, 26.9; 32 rows, 29.4, 26.5, 27.8; 4
+  // bits, 32 rows, 2880 x 2880 10.2, 9.7, 10.5, 4096 x 4096 12.3, 11.5, 10.8; 64
+  // rows, 1024 x 2048 9.5, 9.9, 11.0; 4096 x 11008 24.4, 24.4, 24.2)
   const int64_t rt = 16 * rows_fragments(M), row_tiles = (M + rt - 1) / rt, least = (tiles + 7) / 8;
   const int64_t s = std::min<int64_t>(256 / (least * row_tiles), (chunks + 5) / 6);
   r.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, kRowsJoinMax));
@@ -396,10 +398,10 @@ inline size_t rows_slab_bound(int M) {
   return (size_t)256 * 128 * 16 * rows_fragments(M) * 2 * sizeof(float);
 }
 
-// Wavefronts that split K in the direct form: about 2048 of them over the
-// chip, at least two chunks each.  (4 bits, us, at most about 1500, 3000 and 6000:
-// one row, 5120 x 25600 21.4, 20.6, 20.6; 25600 x 5120 17.3, 16.4, 16.9; five
-// rows, 11008 x 4096 10.7, 9.8, 12.6.)
+// Wavefronts that split K in the direct form: at most 3000 of them over the
+// chip, at least two chunks each.  (4 bits, us with 1500, 3000 and 6000 at most,
+// N x K, one row: 4096 x 11008 10.3, 8.0, 8.0; 5120 x 25600 20.5, 18.6, 18.4;
+// 25600 x 5120 18.0, 18.2, 17.0; five rows: 11008 x 4096 9.1, 9.4, 12.6.)
 inline int rows_ksplit(int64_t workgroups, int K) {
   int ks = 8;
   while (ks > 1 && (workgroups * ks > 3000 || K / 128 < 2 * ks)) ks >>= 1;

@@ -8,8 +8,11 @@
 // 128 + q (one AND-OR for two weights), 128 + z is exact in bf16 as well, and
 // the MFMAs sum x (128 + q) and -x (128 + z) into the same fp32 accumulator,
 // once per 32-deep step each.  A group's sum, sum x (q - z), is then scaled
-// and added to the row's.  What cancels is at most ~30 times the result's
-// size (136 against a spread of 4.6), so fp32 keeps 18 bits and more of it.
+// and added to the row's.  The two sums cancel: each has terms of up to 143
+// |x| where the result's have 4.6 on the mean.  For x of mixed signs that is 30
+// times the result's size and fp32 keeps 19 bits of it; x of one sign makes it
+// about 170 times over a step, and 16 bits.  In all the result is off by at
+// most (K + 8) 2^-24 sum |x| s (256 + q + z).
 //
 // Measured: one row, 5120 x 25600 and back (gate and up 135 MB, down 68): 25
 // and 20 us, 5.2 TB/s where tiles are many (1600 pairs), 3.4 where 320 tiles
@@ -81,9 +84,14 @@ struct PackedWeights {
   static constexpr int GPC = 4 / SPG;  // groups of a chunk
   static constexpr int LINES = 8;
   static constexpr int MAX_FRAGMENTS = 4;
-  // 4 took longer to start than it gained (one row, 4096 x 11008: 7.5 us with
-  // 2, 8.4 with 4, 8.7 with 1; 25600 x 5120: 18.9, 16.8, 15.2; 32 rows: 16.7,
-  // 18.1, 16.7 and 29.7, 32.3, 29.3)
+  // 4 starts later and gains nothing; 1 is up to 9 % faster in some products
+  // and 9 to 15 % slower in others.  us with 1, 2 and 4,
+  // N x K, one row: 11008 x 4096 7.5, 8.2, 9.0; 4096 x 11008 8.7, 8.0, 9.0;
+  // 25600 x 5120 21, 18, 18; 5120 x 25600 17.7, 18.6, 20.3; 32 rows: 4096 x
+  // 11008 16.6, 17.0, 18.1; 25600 x 5120 30, 30, 31.  The block, 2 and 4: one
+  // row, H 5120, I 25600 47.5 and 51; 32 rows, 4096, 11008 43 and 45.  (The
+  // shared form takes turns in two buffers of rows, so that a gated product
+  // needs 2.)
   static constexpr int DEPTH = 2;
   struct Tile {  // chunk 0 of the tile's weights, scales and zero points
     const char* q;
