@@ -541,11 +541,13 @@ def _allocated_on(stream, make, returned=False):
     memory that work on ``stream`` writes has to come from its own pool, both
     when it is taken (earlier users may still run) and when it is let go.
     returned: the caller uses it on the current stream afterwards."""
-    import torch
     if stream is None or _stream(stream) == _stream(None):
         return make()
+    import torch
+    handle = _stream(stream)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream))
+        # (an ExternalStream of address 0 is not the default stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
         t = make()
     if returned:

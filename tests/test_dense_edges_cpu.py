@@ -86,7 +86,8 @@ class Streams:
             return t
 
         monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
-        monkeypatch.setattr(torch.cuda, "ExternalStream", FakeStream)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: FakeStream(handle or 99))
+        monkeypatch.setattr(torch.cuda, "default_stream", lambda *a: FakeStream(0))
         monkeypatch.setattr(torch.cuda, "stream", Scope)
         monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: FakeStream(outer.now))
         monkeypatch.setattr(torch, "empty", empty)
@@ -96,7 +97,7 @@ class Streams:
         monkeypatch.setattr(lm, "_stream", lambda s: outer.now if s is None else getattr(s, "cuda_stream", s))
 
 
-@pytest.mark.parametrize("stream", [FakeStream(7), 7, FakeStream(3), 3, None])
+@pytest.mark.parametrize("stream", [FakeStream(7), 7, FakeStream(3), 3, None, 0])
 def test_buffers_are_memory_of_the_stream_that_writes_them(monkeypatch, stream):
     s = Streams(monkeypatch)
     want = 3 if stream is None else getattr(stream, "cuda_stream", stream)

@@ -169,3 +169,19 @@ def test_norm_of_a_few_elements(dtype):
         worst = float(((norms[:, 0].double().cpu() - want).abs() / want).max())
         print(f"{dtype} {size}: worst {worst * 2 ** 24:.3f} half steps", flush=True)
         assert worst <= 2.0 ** -24 + 2.0 ** -40
+
+
+def test_the_default_stream_by_its_handle_under_another():
+    """stream=0 while another stream is current: the default stream's memory."""
+    import lora_moe_amd as lm
+    x, W_gu, W_down, _ = (t.cuda() for t in ffn_inputs(40, 136, 200, 3))
+    want = lm.gated_ffn(x, W_gu, W_down)
+    grads = lm.GradSet([torch.ones(100, device="cuda")])
+    norm = torch.zeros(1, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        y = lm.gated_ffn(x, W_gu, W_down, stream=0)
+        lm.moe_lora_clip_grads(grads, math.inf, norm, stream=0)
+    torch.cuda.synchronize()
+    assert pool_of(y) == 0 and pool_of(grads._workspace(0)) == 0
+    assert torch.equal(y, want) and float(norm) == 10.0
