@@ -457,6 +457,127 @@ size_t moe_lora_clip_workspace_bytes(int32_t n);
 int moe_lora_clip_grads(const moe_lora_grad* grads, int32_t n, float max_norm, float* norm, void* workspace,
                         size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Tokens to their experts and back, for programs that run the experts
+ * themselves (training above all: a run's rows are what moe_lora_ffn_forward
+ * and _backward take), with the gradients down to the router's logits.
+ * ------------------------------------------------------------------------ */
+
+typedef struct moe_lora_sort_shape {
+  int32_t T;     /* tokens (up to 2^25, T*topk below 2^31 - 256)               */
+  int32_t H;     /* elements of a row, a multiple of 8 (up to 2^20)            */
+  int32_t E;     /* experts (up to 4096)                                       */
+  int32_t topk;  /* experts per token, 1 <= topk <= E, at most 64              */
+  int32_t dtype; /* MOE_LORA_F32, MOE_LORA_BF16 or MOE_LORA_F16: of the rows   */
+} moe_lora_sort_shape;
+
+/* Bytes of workspace of moe_lora_sort, 0 when the shape is invalid.  Host
+ * only, pure. */
+size_t moe_lora_sort_workspace_bytes(const moe_lora_sort_shape* shape);
+
+/* Sorts the pairs p = t*topk + j by expert, pairs of one expert in ascending
+ * p, without padding, and brings each pair its token's row:
+ *     row(p) = expert_off[e_p] + #{p' < p with e_p' = e_p},  rows[row(p)] = x[t]
+ *   topk_ids     device [T][topk] int32; an id outside [0,E) drops the pair.  A
+ *                token may name an expert twice: it then has two rows there
+ *   x            device [T][H], rows device [T*topk][H] of the shape's type;
+ *                both NULL: the order alone
+ *   expert_off   device [E+1] int32, written (zeros for T = 0): expert e has
+ *                rows expert_off[e] .. expert_off[e+1]-1
+ *   row_of_pair  device [T][topk] int32, written; -1 for a dropped pair
+ *   pair_of_row  device [T*topk] int32, written, or NULL
+ * With dropped pairs the rows (and pair_of_row) from expert_off[E] on are left
+ * as they were.  Bit-exact, deterministic.  Every pointer 16-byte aligned. */
+int moe_lora_sort(const moe_lora_sort_shape* shape, const int32_t* topk_ids, const void* x, void* workspace,
+                  size_t ws_bytes, void* rows, int32_t* expert_off, int32_t* row_of_pair, int32_t* pair_of_row,
+                  void* stream);
+
+/* The sort's gradient: dx[t] = sum_j drows[row(t,j)], summed in fp32 in the
+ * order of j, rounded once; dropped pairs add nothing. */
+int moe_lora_sort_backward(const moe_lora_sort_shape* shape, const void* drows, const int32_t* row_of_pair, void* dx,
+                           void* stream);
+
+/* Back to the tokens: y[t] = sum_j weights[t][j] rows[row(t,j)], in fp32 in
+ * the order of j, rounded once.
+ *   rows         device [T*topk][H], what the experts made of the sorted rows
+ *   row_of_pair  as moe_lora_sort wrote it (an index outside [0, T*topk): the
+ *                pair is dropped)
+ *   weights      device [T][topk] fp32, or NULL: ones
+ *   y            device [T][H], overwritten */
+int moe_lora_unsort(const moe_lora_sort_shape* shape, const void* rows, const int32_t* row_of_pair,
+                    const float* weights, void* y, void* stream);
+
+/* Its gradients: drows[row(t,j)] = weights[t][j] dy[t], dweights[t][j] =
+ * <dy[t], rows[row(t,j)]> (fp32 sums; 0 for a dropped pair).
+ *   drows     device [T*topk][H] or NULL; rows without a pair are left as they
+ *             were
+ *   dweights  device [T][topk] fp32 or NULL (rows may then be NULL); one of
+ *             the two is wanted */
+int moe_lora_unsort_backward(const moe_lora_sort_shape* shape, const void* dy, const void* rows,
+                             const int32_t* row_of_pair, const float* weights, void* drows, float* dweights,
+                             void* stream);
+
+/* The gradient of moe_lora_route's weights: with w the softmax over the chosen
+ * logits,
+ *     dlogits[t][e_j] = w_j (dw_j - sum_i w_i dw_i),  0 for every other expert
+ *   topk_ids, topk_weights  as moe_lora_route wrote them (slots without an
+ *                           expert take no part; a repeated id gets the sum)
+ *   dweights                device [T][topk] fp32
+ *   dlogits                 device [T][E] fp32, overwritten, 16-byte aligned
+ * Of the shape T, E and topk (at most 64) are read. */
+int moe_lora_route_backward(const moe_lora_shape* shape, const int32_t* topk_ids, const float* topk_weights,
+                            const float* dweights, float* dlogits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A projection that all requests share (attention's, or a dense layer's)
+ * beside which each request has a low-rank adapter of its own.
+ * ------------------------------------------------------------------------ */
+
+typedef struct moe_lora_proj_shape {
+  int32_t T;        /* tokens                                                  */
+  int32_t K, N;     /* inputs and outputs, multiples of 8 (up to 2^20)         */
+  int32_t L;        /* adapters resident in the A/B stacks (1..4095)           */
+  int32_t r;        /* adapter rank, a multiple of 8 up to 128                 */
+  float lora_scale; /* see s_l below                                           */
+} moe_lora_proj_shape;
+/* MOE_LORA_EUNSUPPORTED beyond these, and where x, dy (y) or one of the A and
+ * B stacks has 2 GiB or more. */
+
+/* Bytes of workspace for the forward (backward = 0), or for either call
+ * (backward != 0); 0 when the shape is invalid.  Host only, pure. */
+size_t moe_lora_proj_workspace_bytes(const moe_lora_proj_shape* shape, int backward);
+
+/* The forward, for every token t with adapter l = lora_ids[t]:
+ *     z[t] = A_l x[t],  y[t] = W x[t] + s_l B_l z[t],  s_l = lora_scale * scales[l]
+ * A token whose id is -1 (or outside [-1,L)) has no adapter: y[t] = W x[t].
+ *   x         device [T][K] bf16        lora_ids  device [T] int32
+ *   W         device [N][K] bf16        A  device [L][r][K] bf16
+ *   B         device [L][N][r] bf16     scales  device [L] fp32, or NULL: ones
+ *   z         device [T][r] fp32, written for the backward (zeros for tokens
+ *             without an adapter); NULL where none follows
+ *   y         device [T][N] bf16, overwritten
+ * Sums are fp32; s_l z goes into the second product as a sum of two bf16 (16
+ * bits) or in fp32; y is rounded once.  The same inputs give the same bits. */
+int moe_lora_proj_forward(const moe_lora_proj_shape* shape, const uint16_t* x, const int32_t* lora_ids,
+                          const uint16_t* W, const uint16_t* A, const uint16_t* B, const float* scales, float* z,
+                          void* workspace, size_t ws_bytes, uint16_t* y, void* stream);
+
+/* The backward, from dy and the kept z (W is frozen and gets no gradient):
+ *     u[t] = s_l B_l^T dy[t],  dx[t] = W^T dy[t] + A_l^T u[t]
+ *     dA_l = sum of u[t] x[t]^T,  dB_l = s_l * sum of dy[t] z[t]^T, over the tokens of adapter l
+ *   dy       device [T][N] bf16
+ *   dx       device [T][K] bf16 or NULL
+ *   dA, dB   device, shaped as A and B, bf16 or NULL; at least one of the
+ *            three is wanted (where T > 0)
+ * Gradients are overwritten (zeros for an adapter without tokens, and for T =
+ * 0), not added to.  Sums are fp32, u and s_l z enter the products as sums of
+ * two bf16, each gradient is rounded once.  The same inputs give the same
+ * bits. */
+int moe_lora_proj_backward(const moe_lora_proj_shape* shape, const uint16_t* dy, const uint16_t* x,
+                           const int32_t* lora_ids, const float* z, const uint16_t* W, const uint16_t* A,
+                           const uint16_t* B, const float* scales, void* workspace, size_t ws_bytes, uint16_t* dx,
+                           uint16_t* dA, uint16_t* dB, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

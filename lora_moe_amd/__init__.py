@@ -85,6 +85,10 @@ class moe_lora_grad(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+class moe_lora_sort_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "E", "topk", "dtype")]
+
+
 # An entry's tuned configuration applies to shapes within this distance of
 # its key (sum over rows per expert (x4), H, I, E, r, L of |log2 ratio|):
 # e.g. a shape with half or twice the entry's rows per expert and the same
@@ -193,6 +197,7 @@ def load_library(path: str = LIB_PATH):
     lib.moe_lora_profiler_destroy.argtypes = [vp]
     lib.moe_lora_profiler_destroy.restype = None
     fp, wp = ctypes.POINTER(moe_lora_ffn_shape), ctypes.POINTER(moe_lora_w4)
+    op = ctypes.POINTER(moe_lora_sort_shape)
     sz, c32 = ctypes.c_size_t, ctypes.c_int32
     for name, restype, argtypes in (
             ("moe_lora_ffn_workspace_bytes", sz, [fp, i32]),
@@ -206,7 +211,13 @@ def load_library(path: str = LIB_PATH):
             ("moe_lora_w4_ffn_forward", i32, [wp, wp, wp, c32, c32, vp, vp, sz, vp, vp]),
             ("moe_lora_clip_workspace_bytes", sz, [c32]),
             ("moe_lora_clip_grads", i32,
-             [ctypes.POINTER(moe_lora_grad), c32, ctypes.c_float, vp, vp, sz, vp])):
+             [ctypes.POINTER(moe_lora_grad), c32, ctypes.c_float, vp, vp, sz, vp]),
+            ("moe_lora_sort_workspace_bytes", sz, [op]),
+            ("moe_lora_sort", i32, [op] + [vp] * 3 + [sz] + [vp] * 5),
+            ("moe_lora_sort_backward", i32, [op] + [vp] * 4),
+            ("moe_lora_unsort", i32, [op] + [vp] * 5),
+            ("moe_lora_unsort_backward", i32, [op] + [vp] * 7),
+            ("moe_lora_route_backward", i32, [sp] + [vp] * 5)):
         f = getattr(lib, name)
         f.restype, f.argtypes = restype, argtypes
     _lib = lib
@@ -793,7 +804,113 @@ def moe_lora_clip_grads(grads, max_norm: float, norm, stream=None) -> None:
         workspace.numel(), _stream(stream)))
 
 
+# ------------------------------------------------------------------ tokens to their experts and back
+
+_ROW_TYPES = {MOE_LORA_F32: "float32", MOE_LORA_BF16: "bfloat16", MOE_LORA_F16: "float16"}
+
+
+def make_sort_shape(T, H, E, topk, dtype="bfloat16") -> moe_lora_sort_shape:
+    """Sizes of a sort by expert; dtype: of the rows, bfloat16, float16 or
+    float32 (a torch dtype or its name)."""
+    name = str(dtype).replace("torch.", "")
+    code = {n: c for c, n in _ROW_TYPES.items()}.get(name)
+    if code is None:
+        raise ValueError(f"dtype: {name}, expected one of {sorted(_ROW_TYPES.values())}")
+    return moe_lora_sort_shape(int(T), int(H), int(E), int(topk), code)
+
+
+def moe_lora_sort_workspace_bytes(shape: moe_lora_sort_shape) -> int:
+    return int(load_library().moe_lora_sort_workspace_bytes(ctypes.byref(shape)))
+
+
+def alloc_sort_workspace(shape: moe_lora_sort_shape, device="cuda"):
+    """Workspace of moe_lora_sort."""
+    import torch
+    n = moe_lora_sort_workspace_bytes(shape)
+    if n == 0:
+        raise MoeLoraError("moe_lora_sort_workspace_bytes", MOE_LORA_EINVAL)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _row_type(shape) -> str:
+    if shape.dtype not in _ROW_TYPES:
+        raise ValueError(f"shape: dtype {shape.dtype}, expected one of {sorted(_ROW_TYPES)}")
+    return _ROW_TYPES[shape.dtype]
+
+
+def moe_lora_sort(shape, topk_ids, x, workspace, rows, expert_off, row_of_pair, pair_of_row=None,
+                  stream=None) -> None:
+    """Sorts the (token, slot) pairs of topk_ids [T, k] by expert and copies
+    each pair's token row: rows [T k, H] from x [T, H] (both None: the order
+    alone).  expert_off [E+1], row_of_pair [T, k] and pair_of_row [T k] are
+    int32 and written."""
+    T, k, dtype = shape.T, shape.topk, _row_type(shape)
+    specs = [("topk_ids", topk_ids, (T, k), "int32"),
+             _check_workspace(workspace, moe_lora_sort_workspace_bytes(shape), "alloc_sort_workspace"),
+             ("expert_off", expert_off, (shape.E + 1,), "int32"), ("row_of_pair", row_of_pair, (T, k), "int32")]
+    if x is not None or rows is not None:
+        specs += [("x", x, (T, shape.H), dtype), ("rows", rows, (T * k, shape.H), dtype)]
+    if pair_of_row is not None:
+        specs.append(("pair_of_row", pair_of_row, (T * k,), "int32"))
+    _check_tensors(specs)
+    _check("moe_lora_sort", load_library().moe_lora_sort(
+        ctypes.byref(shape), topk_ids.data_ptr(), None if x is None else x.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), None if rows is None else rows.data_ptr(), expert_off.data_ptr(), row_of_pair.data_ptr(),
+        None if pair_of_row is None else pair_of_row.data_ptr(), _stream(stream)))
+
+
+def moe_lora_sort_backward(shape, drows, row_of_pair, dx, stream=None) -> None:
+    """dx [T, H]: each token's sum of its pairs' rows of drows [T k, H]."""
+    T, k, dtype = shape.T, shape.topk, _row_type(shape)
+    _check_tensors([("drows", drows, (T * k, shape.H), dtype), ("row_of_pair", row_of_pair, (T, k), "int32"),
+                    ("dx", dx, (T, shape.H), dtype)])
+    _check("moe_lora_sort_backward", load_library().moe_lora_sort_backward(
+        ctypes.byref(shape), drows.data_ptr(), row_of_pair.data_ptr(), dx.data_ptr(), _stream(stream)))
+
+
+def moe_lora_unsort(shape, rows, row_of_pair, y, weights=None, stream=None) -> None:
+    """y [T, H]: each token's sum of its pairs' rows [T k, H], times weights
+    [T, k] (fp32; None: ones)."""
+    T, k, dtype = shape.T, shape.topk, _row_type(shape)
+    specs = [("rows", rows, (T * k, shape.H), dtype), ("row_of_pair", row_of_pair, (T, k), "int32"),
+             ("y", y, (T, shape.H), dtype)]
+    if weights is not None:
+        specs.append(("weights", weights, (T, k), "float32"))
+    _check_tensors(specs)
+    _check("moe_lora_unsort", load_library().moe_lora_unsort(
+        ctypes.byref(shape), rows.data_ptr(), row_of_pair.data_ptr(),
+        None if weights is None else weights.data_ptr(), y.data_ptr(), _stream(stream)))
+
+
+def moe_lora_unsort_backward(shape, dy, rows, row_of_pair, drows=None, weights=None, dweights=None,
+                             stream=None) -> None:
+    """Gradients of moe_lora_unsort from dy [T, H] into those of drows [T k,
+    H] and dweights [T, k] (fp32) that are given; rows (as given to the
+    forward) are needed for dweights alone."""
+    T, k, dtype = shape.T, shape.topk, _row_type(shape)
+    specs = [("dy", dy, (T, shape.H), dtype), ("row_of_pair", row_of_pair, (T, k), "int32")]
+    opt = (("rows", rows, (T * k, shape.H), dtype), ("weights", weights, (T, k), "float32"),
+           ("drows", drows, (T * k, shape.H), dtype), ("dweights", dweights, (T, k), "float32"))
+    specs += [s for s in opt if s[1] is not None]
+    _check_tensors(specs)
+    p = [None if s[1] is None else s[1].data_ptr() for s in opt]
+    _check("moe_lora_unsort_backward", load_library().moe_lora_unsort_backward(
+        ctypes.byref(shape), dy.data_ptr(), p[0], row_of_pair.data_ptr(), p[1], p[2], p[3], _stream(stream)))
+
+
+def moe_lora_route_backward(shape, topk_ids, topk_weights, dweights, dlogits, stream=None) -> None:
+    """The gradient of moe_lora_route's weights: dlogits [T, E] from dweights
+    [T, k] (both fp32) and what the router wrote."""
+    T, k = shape.T, shape.topk
+    _check_tensors([("topk_ids", topk_ids, (T, k), "int32"), ("topk_weights", topk_weights, (T, k), "float32"),
+                    ("dweights", dweights, (T, k), "float32"), ("dlogits", dlogits, (T, shape.E), "float32")])
+    _check("moe_lora_route_backward", load_library().moe_lora_route_backward(
+        ctypes.byref(shape), topk_ids.data_ptr(), topk_weights.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(),
+        _stream(stream)))
+
+
 __all__ = [n for n in dir() if n.startswith("moe_lora") or n in (
     "make_shape", "alloc_workspace", "workspace_tensors", "fused_moe_lora", "load_library",
     "make_ffn_shape", "alloc_ffn_workspace", "gated_ffn",
-    "W4Weight", "alloc_w4_ffn_workspace", "GradSet", "MoeLoraError", "Profiler", "check_operands", "layer_operand_specs")]
+    "W4Weight", "alloc_w4_ffn_workspace", "GradSet", "make_sort_shape", "alloc_sort_workspace",
+    "MoeLoraError", "Profiler", "check_operands", "layer_operand_specs")]
