@@ -534,14 +534,14 @@ int moe_lora_route_backward(const moe_lora_shape* shape, const int32_t* topk_ids
  * ------------------------------------------------------------------------ */
 
 typedef struct moe_lora_proj_shape {
-  int32_t T;        /* tokens                                                  */
+  int32_t T;        /* tokens (up to 2^17)                                     */
   int32_t K, N;     /* inputs and outputs, multiples of 8 (up to 2^20)         */
-  int32_t L;        /* adapters resident in the A/B stacks (1..4095)           */
+  int32_t L;        /* adapters resident in the A/B stacks (1..2047)           */
   int32_t r;        /* adapter rank, a multiple of 8 up to 128                 */
   float lora_scale; /* see s_l below                                           */
 } moe_lora_proj_shape;
-/* MOE_LORA_EUNSUPPORTED beyond these, and where x, dy (y) or one of the A and
- * B stacks has 2 GiB or more. */
+/* MOE_LORA_EUNSUPPORTED beyond these, and where x, y or one of the A and B
+ * stacks has more than 2^31 - 256 bytes. */
 
 /* Bytes of workspace for the forward (backward = 0), or for either call
  * (backward != 0); 0 when the shape is invalid.  Host only, pure. */

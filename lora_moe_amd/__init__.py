@@ -89,6 +89,10 @@ class moe_lora_sort_shape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "E", "topk", "dtype")]
 
 
+class moe_lora_proj_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "L", "r")] + [("lora_scale", ctypes.c_float)]
+
+
 # An entry's tuned configuration applies to shapes within this distance of
 # its key (sum over rows per expert (x4), H, I, E, r, L of |log2 ratio|):
 # e.g. a shape with half or twice the entry's rows per expert and the same
@@ -197,7 +201,7 @@ def load_library(path: str = LIB_PATH):
     lib.moe_lora_profiler_destroy.argtypes = [vp]
     lib.moe_lora_profiler_destroy.restype = None
     fp, wp = ctypes.POINTER(moe_lora_ffn_shape), ctypes.POINTER(moe_lora_w4)
-    op = ctypes.POINTER(moe_lora_sort_shape)
+    op, pp = ctypes.POINTER(moe_lora_sort_shape), ctypes.POINTER(moe_lora_proj_shape)
     sz, c32 = ctypes.c_size_t, ctypes.c_int32
     for name, restype, argtypes in (
             ("moe_lora_ffn_workspace_bytes", sz, [fp, i32]),
@@ -217,7 +221,10 @@ def load_library(path: str = LIB_PATH):
             ("moe_lora_sort_backward", i32, [op] + [vp] * 4),
             ("moe_lora_unsort", i32, [op] + [vp] * 5),
             ("moe_lora_unsort_backward", i32, [op] + [vp] * 7),
-            ("moe_lora_route_backward", i32, [sp] + [vp] * 5)):
+            ("moe_lora_route_backward", i32, [sp] + [vp] * 5),
+            ("moe_lora_proj_workspace_bytes", sz, [pp, i32]),
+            ("moe_lora_proj_forward", i32, [pp] + [vp] * 8 + [sz, vp, vp]),
+            ("moe_lora_proj_backward", i32, [pp] + [vp] * 9 + [sz] + [vp] * 4)):
         f = getattr(lib, name)
         f.restype, f.argtypes = restype, argtypes
     _lib = lib
@@ -909,8 +916,92 @@ def moe_lora_route_backward(shape, topk_ids, topk_weights, dweights, dlogits, st
         _stream(stream)))
 
 
+# ------------------------------------------------------------------ a shared projection with adapters
+
+
+def make_proj_shape(T, K, N, L, r, lora_scale=1.0) -> moe_lora_proj_shape:
+    """Sizes of a projection [N, K] that all tokens share, with L adapters of
+    rank r beside it."""
+    return moe_lora_proj_shape(int(T), int(K), int(N), int(L), int(r), float(lora_scale))
+
+
+def moe_lora_proj_workspace_bytes(shape: moe_lora_proj_shape, backward: bool = True) -> int:
+    return int(load_library().moe_lora_proj_workspace_bytes(ctypes.byref(shape), int(bool(backward))))
+
+
+def alloc_proj_workspace(shape: moe_lora_proj_shape, backward: bool = True, device="cuda"):
+    """Workspace of moe_lora_proj_forward and (backward) moe_lora_proj_backward."""
+    import torch
+    n = moe_lora_proj_workspace_bytes(shape, backward)
+    if n == 0:
+        raise MoeLoraError("moe_lora_proj_workspace_bytes", MOE_LORA_EINVAL)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _proj_weights(shape, lora_ids, W, A, B, scales):
+    T, K, N, L, r = shape.T, shape.K, shape.N, shape.L, shape.r
+    specs = [("lora_ids", lora_ids, (T,), "int32"), ("W", W, (N, K), "bfloat16"), ("A", A, (L, r, K), "bfloat16"),
+             ("B", B, (L, N, r), "bfloat16")]
+    if scales is not None:
+        specs.append(("scales", scales, (L,), "float32"))
+    return specs
+
+
+def moe_lora_proj_forward(shape, x, lora_ids, W, A, B, workspace, y, z=None, scales=None, stream=None) -> None:
+    """y [T, N] = x W^T + s_l (x A_l^T) B_l^T with each token's own adapter l =
+    lora_ids[t] (-1: none), s_l = lora_scale * scales[l]; with z ([T, r] fp32)
+    x A_l^T is kept there for moe_lora_proj_backward."""
+    specs = [("x", x, (shape.T, shape.K), "bfloat16"), ("y", y, (shape.T, shape.N), "bfloat16"),
+             *_proj_weights(shape, lora_ids, W, A, B, scales),
+             _check_workspace(workspace, moe_lora_proj_workspace_bytes(shape, False), "alloc_proj_workspace")]
+    if z is not None:
+        specs.append(("z", z, (shape.T, shape.r), "float32"))
+    _check_tensors(specs)
+    _check("moe_lora_proj_forward", load_library().moe_lora_proj_forward(
+        ctypes.byref(shape), x.data_ptr(), lora_ids.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(),
+        None if scales is None else scales.data_ptr(), None if z is None else z.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), y.data_ptr(), _stream(stream)))
+
+
+def moe_lora_proj_backward(shape, dy, x, lora_ids, z, W, A, B, workspace, dx=None, dA=None, dB=None, scales=None,
+                           stream=None) -> None:
+    """Gradients of the projection from dy and the kept z into those of dx, dA
+    and dB that are given (overwritten); W is frozen."""
+    T, K, N, L, r = shape.T, shape.K, shape.N, shape.L, shape.r
+    specs = [("dy", dy, (T, N), "bfloat16"), ("x", x, (T, K), "bfloat16"), ("z", z, (T, r), "float32"),
+             *_proj_weights(shape, lora_ids, W, A, B, scales),
+             _check_workspace(workspace, moe_lora_proj_workspace_bytes(shape, True), "alloc_proj_workspace")]
+    outs = (("dx", dx, (T, K)), ("dA", dA, (L, r, K)), ("dB", dB, (L, N, r)))
+    specs += [(n, t, s, "bfloat16") for n, t, s in outs if t is not None]
+    _check_tensors(specs)
+    _check("moe_lora_proj_backward", load_library().moe_lora_proj_backward(
+        ctypes.byref(shape), dy.data_ptr(), x.data_ptr(), lora_ids.data_ptr(), z.data_ptr(), W.data_ptr(),
+        A.data_ptr(), B.data_ptr(), None if scales is None else scales.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), *[None if t is None else t.data_ptr() for _, t, _ in outs], _stream(stream)))
+
+
+def lora_projection(x, lora_ids, W, A, B, lora_scale=1.0, scales=None, workspace=None, y=None, stream=None):
+    """The projection's forward on the current stream (or ``stream``); returns
+    y [T, N] (bf16).  x [T,K], W [N,K], A [L,r,K], B [L,N,r], all bf16;
+    lora_ids [T] int32; scales [L] fp32 or None.  It records nothing for
+    autograd (see gated_ffn)."""
+    import torch
+    for name, t, nd in (("x", x, 2), ("W", W, 2), ("A", A, 3)):
+        if t.dim() != nd:
+            raise ValueError(f"{name}: {t.dim()} dimensions, expected {nd}")
+    shape = make_proj_shape(x.shape[0], x.shape[1], W.shape[0], A.shape[0], A.shape[1], lora_scale)
+    if workspace is None:
+        workspace = _allocated_on(stream, lambda: alloc_proj_workspace(shape, False, x.device))
+    if y is None:
+        y = _allocated_on(stream, lambda: torch.empty((shape.T, shape.N), dtype=torch.bfloat16, device=x.device),
+                          returned=True)
+    moe_lora_proj_forward(shape, x, lora_ids, W, A, B, workspace, y, scales=scales, stream=stream)
+    return y
+
+
 __all__ = [n for n in dir() if n.startswith("moe_lora") or n in (
     "make_shape", "alloc_workspace", "workspace_tensors", "fused_moe_lora", "load_library",
     "make_ffn_shape", "alloc_ffn_workspace", "gated_ffn",
     "W4Weight", "alloc_w4_ffn_workspace", "GradSet", "make_sort_shape", "alloc_sort_workspace",
+    "make_proj_shape", "alloc_proj_workspace", "lora_projection",
     "MoeLoraError", "Profiler", "check_operands", "layer_operand_specs")]

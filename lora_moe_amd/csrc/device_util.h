@@ -42,6 +42,21 @@ __device__ __forceinline__ void f32_to_bf16_pair(float v, uint16_t* hi, uint16_t
   *lo = finite ? __builtin_bit_cast(uint16_t, (__bf16)(v - bf16_to_f32(h))) : (uint16_t)0;
 }
 
+// 8 values as sums of two bf16
+__device__ __forceinline__ void store8_pair(uint16_t* hi, uint16_t* lo, const float* v) {
+  u32x4_t a, b;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint16_t h[2], l[2];
+    f32_to_bf16_pair(v[2 * i], h, l);
+    f32_to_bf16_pair(v[2 * i + 1], h + 1, l + 1);
+    a[i] = h[0] | (uint32_t)h[1] << 16;
+    b[i] = l[0] | (uint32_t)l[1] << 16;
+  }
+  *reinterpret_cast<u32x4_t*>(hi) = a;
+  *reinterpret_cast<u32x4_t*>(lo) = b;
+}
+
 // D(16x16, fp32) += A(16x32, bf16) * B(32x16, bf16) on one wavefront.
 // Lane l supplies A[m = l%16][k = 8*(l/16) .. +8] and B[k = 8*(l/16) .. +8][n = l%16];
 // it receives D[m = 4*(l/16) + i][n = l%16], i = 0..3.  Only the pairing of

@@ -69,6 +69,14 @@ size_t ffn_gemm_slab_bytes(int M, int N, int K, FfnProduct product, bool pair = 
 
 int launch_ffn_gemm(const FfnGemm& g, FfnProduct product, hipStream_t st);
 
+// Tile (256 x 256 or 128 x 128) and K splits (small tiles only) for a product
+// of these sizes, by the rule in ffn_gemm.hip.
+struct TilePlan {
+  bool big;
+  int splits;
+};
+TilePlan tile_plan(int M, int N, int K);
+
 // The FFN_DX and the two FFN_DW of a backward that wants all three; dx.slabs:
 // the larger of ffn_grads_slab_bytes and the products' own.
 size_t ffn_grads_slab_bytes(int T, int H, int I);

@@ -1,0 +1,105 @@
+// Internal declarations of the shared projection with the adapters of many
+// requests (proj.hip: ABI; proj_rows.hip: few tokens; proj_order.hip,
+// proj_shrink.hip, proj_gemm.hip, proj_grads.hip: the rest).  Not part of the
+// public ABI.
+//
+// Beyond a few tokens everything works on rows, the tokens sorted by adapter:
+// row m is token perm[m], the tokens of one adapter are one run, those without
+// an adapter come last.  Only indices are sorted; x, dy, y and dx stay where
+// they are and the kernels gather and scatter their rows.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "moe_lora.h"
+
+namespace moelora {
+
+// Up to this many tokens a forward streams the weights (proj_rows.hip), and no
+// order is needed.
+constexpr int kProjRows = 32;
+
+// Rows [row, row + n) of one adapter; slab: where a piece of a longer run puts
+// its sums (-1: the run's only piece).
+struct ProjItem {
+  int adapter, row, n, slab;
+};
+
+// What proj_order.hip writes for the other kernels.
+struct ProjOrder {
+  int32_t* perm;       // [T] token of a row
+  int32_t* run;        // [T] which run the row is in (runs with tokens, counted from 0)
+  int32_t* adapter;    // [L + 1] adapter of a run; L: the tokens without
+  int32_t* count;      // [4] shrink items, gradient items, runs with an adapter
+  ProjItem* shrink;    // pieces of at most shrink_rows rows of the runs with an adapter
+  ProjItem* grad;      // pieces of at most grad_rows rows
+  int32_t* slabs;      // [L][2] first slab of an adapter and how many (0: one piece, -1: no tokens)
+};
+
+struct ProjArgs {
+  int T, K, N, L, r;
+  float scale;
+  const int32_t* ids;
+  const float* scales;  // [L] or NULL
+  ProjOrder o;
+  int shrink_rows, grad_rows;
+};
+
+// s_l
+__device__ __forceinline__ float proj_scale(const ProjArgs& p, int l) {
+  return p.scales ? p.scale * p.scales[l] : p.scale;
+}
+
+// Pairs: [T rows][2r] bf16, a row's r values rounded and behind them their
+// remainders, which meet the same weights: 16 bits of each value.
+
+// z (NULL: not wanted): zeros for the tokens without an adapter are written
+// here; zs (backward; NULL else): pairs of s_l z.
+int launch_proj_order(const ProjArgs& p, float* z, const float* kept, uint16_t* zs, hipStream_t st);
+
+// pairs[m] = s_l * (weights of row m's adapter) in[perm[m]] and, on request,
+// the product without s_l by token (z).  back: in = dy, weights = B [L][N][r];
+// else in = x, weights = A [L][r][K].
+int launch_proj_shrink(const ProjArgs& p, bool back, const uint16_t* in, const uint16_t* weights, uint16_t* pairs,
+                       float* z, hipStream_t st);
+
+// out[perm[m]] = in[perm[m]] W^T + pairs[m] weights^T; back: the same with W
+// and the adapters' weights by their columns.
+struct ProjGemm {
+  const uint16_t* in;
+  const uint16_t* W;
+  const uint16_t* pairs;
+  const uint16_t* weights;
+  uint16_t* out;
+  float* slabs;
+  int splits;
+};
+size_t proj_gemm_slab_bytes(const ProjArgs& p, bool back);
+int launch_proj_gemm(const ProjArgs& p, bool back, ProjGemm g, hipStream_t st);
+
+// dA and dB (either may be NULL)
+struct ProjGrads {
+  const uint16_t* x;
+  const uint16_t* dy;
+  const uint16_t* us;  // pairs of u
+  const uint16_t* zs;  // pairs of s_l z
+  uint16_t* dA;
+  uint16_t* dB;
+  float* slabs;
+};
+int proj_grad_rows(int T, int K, int N, int r);
+size_t proj_grad_slab_bytes(int T, int K, int N, int r);
+int launch_proj_grads(const ProjArgs& p, const ProjGrads& g, hipStream_t st);
+
+// The whole forward of at most kProjRows tokens.
+size_t proj_rows_slab_bytes(int T, int K, int N, int L, int r);
+int launch_proj_rows(const ProjArgs& p, const uint16_t* x, const uint16_t* W, const uint16_t* A, const uint16_t* B,
+                     float* z, float* slabs, uint16_t* y, hipStream_t st);
+
+inline int proj_shrink_rows(int T, int r) { return T <= 4096 || r > 64 ? 16 : 32; }
+// items at most: whole pieces, and one short one for each run
+inline int64_t proj_items(int T, int L, int rows) { return T / rows + (T < L ? T : L); }
+
+}  // namespace moelora

@@ -1,0 +1,372 @@
+// The projection's products beyond a few tokens: LDS-tiled bf16 MFMA.
+//
+//   forward   y[t]  = W x[t]    + B_l (s_l z[t])
+//   backward  dx[t] = W^T dy[t] + A_l^T u[t]
+//
+// One product each, over the tokens sorted by adapter: a tile's K loop runs
+// over the shared weights first, then over the ranks of the adapters whose
+// rows the tile holds, 64 deep like the rest (a rank takes 2r: the pairs of
+// the values to 16 bits).  A row takes part in its own adapter's share and is
+// zeros in another's, so a tile of one long request has one share and a tile
+// of a decode batch as many as it has adapters, while W is met once by all.
+// The sorted order exists only in the addresses: rows of x (dy) are gathered
+// on their way into LDS, rows of y (dx) scattered from the epilogue.
+//
+// Zeros times an infinity or NaN would carry one adapter's broken weights into
+// another request's rows.  So the adapters' weights go into the products with
+// 0 in place of such values, and a tile that met one adds their terms to the
+// rows that they belong to, one by one, in its epilogue.
+//
+// The loop is that of ffn_gemm.hip: a two-stage ring filled by asynchronous
+// copies that go out between the MFMAs of the stage before.
+#include "ffn.h"
+#include "internal.h"
+#include "proj.h"
+#include "tile.h"
+
+namespace moelora {
+
+namespace {
+
+struct TileArgs {
+  ProjArgs p;
+  ProjGemm g;
+  int in_cols, out_cols;  // K and N of a forward
+  int ncol, nrow;
+};
+
+template <class C>
+constexpr int tile_lds() { return C::LDS + 3 * C::BM * 4 + 16; }
+
+// infinities and NaN of 8 bf16 to 0; whether there were any
+__device__ __forceinline__ bool only_finite(u32x4_t& v) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool lo = (v[i] & 0x7f80u) == 0x7f80u, hi = (v[i] & 0x7f800000u) == 0x7f800000u;
+    bad |= lo | hi;
+    v[i] = (lo ? 0u : v[i] & 0xffffu) | (hi ? 0u : v[i] & 0xffff0000u);
+  }
+  return bad;
+}
+
+// The terms of a row that only_finite took out, for 8 neighbouring outputs.
+// z: the row's pair; w: the adapter's weight of the first output and rank 0,
+// `rank` apart along the rank and `out` along the outputs.
+struct Eight {
+  f32x4_t v[2];
+};
+__device__ __noinline__ Eight add_not_finite(Eight e, const uint16_t* z, const uint16_t* w, int64_t rank, int64_t out,
+                                             int r) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    float s = e.v[q >> 2][q & 3];
+    for (int j = 0; j < r; ++j) {
+      const uint16_t b = w[j * rank + q * out];
+      if ((b & 0x7f80u) == 0x7f80u) s += (bf16_to_f32(z[j]) + bf16_to_f32(z[r + j])) * bf16_to_f32(b);
+    }
+    e.v[q >> 2][q & 3] = s;
+  }
+  return e;
+}
+
+template <bool BACK, class C, bool SPLIT>
+__global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
+  constexpr bool B_KC = !BACK;
+  constexpr int MI = C::MI, NI = C::NI;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  int* token = reinterpret_cast<int*>(smem + C::LDS);  // [BM] of the tile's rows, -1 past the last
+  int* share = token + C::BM;                          // [BM] which of the tile's adapters, -1: none
+  int* adapter = share + C::BM;                        // [BM] the tile's adapters
+  int* not_finite = adapter + C::BM;
+  const ProjArgs& p = a.p;
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int T = p.T, N = a.out_cols, K = a.in_cols, r = p.r, ncol = a.ncol, nrow = a.nrow;
+
+  // workgroups to tiles as in ffn_gemm.hip: each XCD a contiguous eighth, in
+  // panels of 4 row tiles
+  int t;
+  {
+    const int total = ncol * nrow * (SPLIT ? a.g.splits : 1), x = blockIdx.x & 7, j = blockIdx.x >> 3;
+    const int per = total >> 3, rest = total & 7;
+    t = x * per + min(x, rest) + j;
+  }
+  const int split = SPLIT ? t / (ncol * nrow) : 0;
+  t -= split * (ncol * nrow);
+  constexpr int GM = 4;
+  const int panel = t / (GM * ncol), in = t - panel * GM * ncol;
+  const int gm = min(GM, nrow - panel * GM);
+  const int tn = in / gm, tm = panel * GM + in - tn * gm;
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
+
+  Operand<true, C::BM, C::NCA, false> A;
+  Operand<B_KC, C::BN, C::NCB, false> B;
+  const int all = (K + BK - 1) / BK, kfirst = K - all * BK;
+  const int s0 = SPLIT ? (int)((int64_t)all * split / a.g.splits) : 0;
+  const int nst = SPLIT ? (int)((int64_t)all * (split + 1) / a.g.splits) : all;
+  A.init(a.g.in, 0, K, 0, kfirst, wave, 0);
+#pragma unroll
+  for (int i = 0; i < C::NCA; ++i) {  // its rows from anywhere
+    const int rr = (wave * C::NCA + i) * 8 + (lane >> 3), ch = (lane & 7) ^ ((rr >> 1) & 7);
+    A.off[i] = m0 + rr < T ? ((uint32_t)p.o.perm[m0 + rr] * (uint32_t)K + ch * 8u) * 2u : kBufNone;
+  }
+  const int64_t ldw = BACK ? N : K;
+  B.init(B_KC ? a.g.W + (int64_t)n0 * ldw : a.g.W + n0, 0, ldw, N - n0, kfirst, wave, 0);
+
+  f32x16_t acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+
+  const uint32_t smem_at = (uint32_t)(uintptr_t)(lds_char*)smem;
+  u32x4_t af[2][MI], bf[2][NI];
+  auto read = [&](int slot, int kk, int set, int i) __attribute__((always_inline)) {
+    const char* at = smem + slot * C::STAGE;
+    if (i == 0) af[set][0] = A.frag(at, wm * (C::BM / C::WM), 0, kk);
+    else if (i <= NI) bf[set][i - 1] = B.frag(at + C::ABYTES, wn * (C::BN / C::WN), i - 1, kk);
+    else af[set][i - NI] = A.frag(at, wm * (C::BM / C::WM), i - NI, kk);
+  };
+  constexpr int NM = MI * NI, NF = MI + NI, NC = C::NCA + C::NCB;
+  auto slice = [&](int set, int slot, int kk, auto issue_c) __attribute__((always_inline)) {
+    constexpr bool ISSUE = decltype(issue_c)::value;
+    for_each<NM>([&](auto n_c) __attribute__((always_inline)) {
+      constexpr int n = decltype(n_c)::value, i = n / NI, j = n % NI;
+      acc[i][j] = mfma_32x32x16(bf[set][j], af[set][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (n < NF) read(slot, kk, set ^ 1, n);
+      if constexpr (ISSUE) {
+        for_each<(n + 1) * NC / NM - n * NC / NM>([&](auto q_c) __attribute__((always_inline)) {
+          constexpr int q = n * NC / NM + decltype(q_c)::value;
+          const uint32_t to = smem_at + (slot ^ 1) * C::STAGE;
+          if constexpr (q < C::NCA) A.template copy<q, false>(to, wave, 0);
+          else B.template copy<q - C::NCA, false>(to + C::ABYTES, wave, 0);
+        });
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  typedef std::integral_constant<bool, true> yes;
+  typedef std::integral_constant<bool, false> no;
+  A.at(s0, s0 < nst);
+  B.at(s0, s0 < nst);
+  if (s0 == 0) {
+    for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, true>(smem_at, wave, kfirst); });
+    for_each<C::NCB>([&](auto i) { B.template copy<decltype(i)::value, true>(smem_at + C::ABYTES, wave, kfirst); });
+  } else {
+    for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, false>(smem_at, wave, 0); });
+    for_each<C::NCB>([&](auto i) { B.template copy<decltype(i)::value, false>(smem_at + C::ABYTES, wave, 0); });
+  }
+  A.at(s0 + 1, s0 + 1 < nst);
+  B.at(s0 + 1, s0 + 1 < nst);
+  for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, false>(smem_at + C::STAGE, wave, 0); });
+  for_each<C::NCB>(
+      [&](auto i) { B.template copy<decltype(i)::value, false>(smem_at + C::STAGE + C::ABYTES, wave, 0); });
+  // the tile's rows and adapters, while the first copies are on their way
+  const int last = min(m0 + C::BM, T) - 1;
+  const int run0 = p.o.run[m0], with = p.o.count[2];  // runs from `with` on: without an adapter
+  const int shares = SPLIT && split + 1 < a.g.splits ? 0 : max(0, min(p.o.run[last] + 1, with) - run0);
+  for (int i = threadIdx.x; i < C::BM; i += C::NT) {
+    const int m = m0 + i;
+    int tok = -1, sh = -1;
+    if (m < T) {
+      tok = p.o.perm[m];
+      const int run = p.o.run[m];
+      if (run < with) {
+        sh = run - run0;
+        if (i == 0 || p.o.run[m - 1] != run) adapter[sh] = p.o.adapter[run];
+      }
+    }
+    token[i] = tok;
+    share[i] = sh;
+  }
+  if (threadIdx.x == 0) *not_finite = 0;
+  __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);
+  bare_barrier();
+#pragma unroll
+  for (int i = 0; i < NF; ++i) read(0, 0, 0, i);
+  for (int s = s0; s < nst; s += 2) {
+    for_each<2>([&](auto h_c) __attribute__((always_inline)) {
+      constexpr int slot = decltype(h_c)::value;
+      slice(0, slot, 1, no());
+      slice(1, slot, 2, no());
+      A.at(s + slot + 2, s + slot + 2 < nst);
+      B.at(s + slot + 2, s + slot + 2 < nst);
+      slice(0, slot, 3, no());
+      __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);
+      bare_barrier();
+      slice(1, slot ^ 1, 0, yes());
+    });
+  }
+  __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);  // no copy outlives the loop
+  bare_barrier();
+
+  // The adapters' shares: column kx of this part of K is value kx % 2r of
+  // share kx / 2r.
+  const int r2 = 2 * r, extra = (shares * r2 + BK - 1) / BK;
+  if (extra) {
+    const u32x4_t rz = rsrc_of(a.g.pairs, 0x7fffffffu), rw = rsrc_of(a.g.weights, 0x7fffffffu);
+    auto bring = [&](int e) __attribute__((always_inline)) {
+      const uint32_t to = smem_at + (e & 1) * C::STAGE;
+      for_each<C::NCA>([&](auto i_c) __attribute__((always_inline)) {
+        constexpr int i = decltype(i_c)::value;
+        const int rr = (wave * C::NCA + i) * 8 + (lane >> 3), ch = (lane & 7) ^ ((rr >> 1) & 7);
+        const int kx = e * BK + ch * 8, q = kx / r2;
+        const uint32_t off = share[rr] == q ? ((uint32_t)(m0 + rr) * r2 + (kx - q * r2)) * 2u : kBufNone;
+        copy16<i * 1024>(rz, to + wave * (C::NCA * 1024), off, 0);
+      });
+      for_each<C::NCB>([&](auto i_c) __attribute__((always_inline)) {
+        constexpr int i = decltype(i_c)::value;
+        const int c = wave * C::NCB + i;
+        uint32_t off = kBufNone;
+        if (B_KC) {
+          const int nn = c * 8 + (lane >> 3), ch = (lane & 7) ^ ((nn >> 1) & 7);
+          const int kx = e * BK + ch * 8, q = kx / r2, w = kx - q * r2;
+          if (q < shares && n0 + nn < N)
+            off = (((uint32_t)adapter[q] * N + n0 + nn) * r + (w < r ? w : w - r)) * 2u;
+        } else {
+          constexpr int PER = 1024 / (C::BN * 2), LPR = C::BN / 8;
+          const int k = c * PER + lane / LPR, ch = (lane % LPR) ^ (4 * (k & 3));
+          const int kx = e * BK + k, q = kx / r2, w = kx - q * r2;
+          if (q < shares && n0 + ch * 8 < N)
+            off = (((uint32_t)adapter[q] * r + (w < r ? w : w - r)) * N + n0 + ch * 8) * 2u;
+        }
+        copy16<i * 1024>(rw, to + C::ABYTES + wave * (C::NCB * 1024), off, 0);
+      });
+    };
+    bool bad = false;
+    bring(0);
+#pragma unroll 1
+    for (int e = 0; e < extra; ++e) {
+      __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);
+      bare_barrier();  // this stage has landed, the other one's reads are done
+      if (e + 1 < extra) bring(e + 1);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+        for (int i = 0; i < NF; ++i) read(e & 1, kk, 0, i);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) bad |= only_finite(bf[0][j]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int j = 0; j < NI; ++j) acc[i][j] = mfma_32x32x16(bf[0][j], af[0][i], acc[i][j]);
+      }
+    }
+    if (bad) *not_finite = 1;
+    __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);
+    bare_barrier();
+  }
+  const bool mend = extra && *not_finite;
+
+  // Epilogue, 32 rows of the wavefront at a time through its own part of the
+  // LDS, so that memory sees whole lines (as in ffn_gemm.hip).
+  constexpr int WC = C::BN / C::WN, ROWF = WC + 4;
+  constexpr int LPR = WC / 8, RPI = 64 / LPR, STEPS = 32 / RPI;
+  float* mine = reinterpret_cast<float*>(smem) + wave * 32 * ROWF;
+  static_assert(C::NW * 32 * ROWF * 4 <= C::LDS, "staged rows must fit the ring");
+  const int l32 = lane & 31, kh = lane >> 5;
+  const int oc = (lane % LPR) * 8, n = n0 + wn * WC + oc;
+#pragma unroll 1
+  for (int i = 0; i < MI; ++i) {
+    for_each<MI>([&](auto b_c) __attribute__((always_inline)) {
+      constexpr int b = decltype(b_c)::value;
+      if (i != b) return;
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<f32x4_t*>(mine + l32 * ROWF + j * 32 + 8 * q + 4 * kh) =
+              f32x4_t{acc[b][j][4 * q], acc[b][j][4 * q + 1], acc[b][j][4 * q + 2], acc[b][j][4 * q + 3]};
+    });
+    asm volatile("" ::: "memory");  // a wavefront's LDS accesses run in order
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int rr = wm * (C::BM / C::WM) + i * 32 + s * RPI + lane / LPR;
+      const int tok = token[rr];
+      if (tok < 0 || n >= N) continue;
+      const f32x4_t* src = reinterpret_cast<const f32x4_t*>(mine + (s * RPI + lane / LPR) * ROWF + oc);
+      Eight e = {{src[0], src[1]}};
+      if (mend && share[rr] >= 0) {
+        const int64_t first = (int64_t)adapter[share[rr]] * N * r;
+        e = add_not_finite(e, a.g.pairs + (int64_t)(m0 + rr) * r2, a.g.weights + first + (BACK ? n : (int64_t)n * r),
+                           BACK ? N : 1, BACK ? 1 : r, r);
+      }
+      const f32x4_t* v = e.v;
+      if (SPLIT) {
+        f32x4_t* dst = reinterpret_cast<f32x4_t*>(a.g.slabs + ((int64_t)split * T + m0 + rr) * N + n);
+        dst[0] = v[0];
+        dst[1] = v[1];
+      } else {
+        const float o[8] = {v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]};
+        store8(a.g.out + (int64_t)tok * N + n, o);
+      }
+    }
+    asm volatile("" ::: "memory");
+  }
+}
+
+// Adds the slabs in their order and scatters the rows.
+__global__ __launch_bounds__(256) void proj_join_kernel(TileArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = a.out_cols / 8;
+  if (i >= per * a.p.T) return;
+  const int m = (int)(i / per), n = (int)(i % per) * 8;
+  f32x4_t s[2];
+  for (int z = 0; z < a.g.splits; ++z) {
+    const f32x4_t* src = reinterpret_cast<const f32x4_t*>(a.g.slabs + ((int64_t)z * a.p.T + m) * a.out_cols + n);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) s[h] = z ? s[h] + src[h] : src[h];
+  }
+  const float o[8] = {s[0][0], s[0][1], s[0][2], s[0][3], s[1][0], s[1][1], s[1][2], s[1][3]};
+  store8(a.g.out + (int64_t)a.p.o.perm[m] * a.out_cols + n, o);
+}
+
+typedef FfnCfg<256, 256, 2, 4> Big;
+typedef FfnCfg<128, 128, 2, 2> Small;
+
+template <bool BACK, class C, bool SPLIT>
+int launch_cfg(TileArgs a, hipStream_t st) {
+  static std::atomic<uint64_t> attr_done;
+  const int64_t ncol = (a.out_cols + C::BN - 1) / C::BN, nrow = (a.p.T + C::BM - 1) / C::BM;
+  const int64_t grid = ncol * nrow * a.g.splits;
+  if (grid * C::NT > 0xffffffff) return MOE_LORA_EUNSUPPORTED;
+  a.ncol = (int)ncol;
+  a.nrow = (int)nrow;
+  const void* fn = reinterpret_cast<const void*>(&proj_tile_kernel<BACK, C, SPLIT>);
+  const int rc = ensure_dynamic_lds(fn, tile_lds<C>(), attr_done);
+  if (rc) return rc;
+  proj_tile_kernel<BACK, C, SPLIT><<<(unsigned)grid, C::NT, tile_lds<C>(), st>>>(a);
+  if (SPLIT) {
+    const int64_t n = (int64_t)a.p.T * (a.out_cols / 8);
+    proj_join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
+  }
+  return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
+}
+
+TilePlan plan_of(const ProjArgs& p, bool back) { return tile_plan(p.T, back ? p.K : p.N, back ? p.N : p.K); }
+
+template <bool BACK>
+int launch(TileArgs a, hipStream_t st) {
+  const TilePlan f = plan_of(a.p, BACK);
+  a.g.splits = f.splits;
+  if (f.splits > 1) return launch_cfg<BACK, Small, true>(a, st);
+  return f.big ? launch_cfg<BACK, Big, false>(a, st) : launch_cfg<BACK, Small, false>(a, st);
+}
+
+}  // namespace
+
+size_t proj_gemm_slab_bytes(const ProjArgs& p, bool back) {
+  const int s = plan_of(p, back).splits;
+  return s > 1 ? (size_t)s * p.T * (back ? p.K : p.N) * sizeof(float) : 0;
+}
+
+int launch_proj_gemm(const ProjArgs& p, bool back, ProjGemm g, hipStream_t st) {
+  const TileArgs a{p, g, back ? p.N : p.K, back ? p.K : p.N, 0, 0};
+  return back ? launch<true>(a, st) : launch<false>(a, st);
+}
+
+}  // namespace moelora
