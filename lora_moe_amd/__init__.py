@@ -814,6 +814,52 @@ def moe_lora_clip_grads(grads, max_norm: float, norm, stream=None) -> None:
 # ------------------------------------------------------------------ tokens to their experts and back
 
 _ROW_TYPES = {MOE_LORA_F32: "float32", MOE_LORA_BF16: "bfloat16", MOE_LORA_F16: "float16"}
+_types = {}  # torch's types by name
+
+
+def _operands(specs, workspace=None):
+    """The device of (name, tensor, shape, dtype) that all match, are contiguous
+    and lie on the current HIP device; raises ValueError otherwise.  workspace:
+    (tensor, bytes needed as a function, what allocates it).  What is right
+    passes in one look at each tensor (a small call's time is mostly its
+    checks'; the workspace's size is looked at by the library); what is not is
+    named by the checks of the other calls."""
+    if not _types:
+        import torch
+        _types.update({n: getattr(torch, n) for n in ("bfloat16", "float16", "float32", "int32", "uint8")},
+                      device=torch._C._cuda_getDevice)
+    dev = None
+    for _, t, shape, dtype in specs:
+        if t is None or t.dtype is not _types[dtype] or t.shape != shape or not t.is_contiguous():
+            break
+        if t.get_device() != dev:
+            if dev is not None or not t.is_cuda:
+                break
+            dev = t.get_device()
+    else:
+        w = None if workspace is None else workspace[0]
+        if ((workspace is None or w is not None and w.dtype is _types["uint8"] and w.dim() == 1
+                and w.is_contiguous() and w.get_device() == dev) and dev == _types["device"]()):
+            return dev
+    if workspace is not None:
+        specs = [*specs, _check_workspace(workspace[0], workspace[1](), workspace[2])]
+    _check_tensors(specs)
+    return specs[0][1].device.index
+
+
+def _done(func, code, workspace=None):
+    if code == MOE_LORA_OK:
+        return
+    if code == MOE_LORA_EWORKSPACE and workspace is not None:
+        _check_workspace(workspace[0], workspace[1](), workspace[2])
+    _check(func, code)
+
+
+def _handle(stream, dev):
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return getattr(stream, "cuda_stream", stream)
 
 
 def make_sort_shape(T, H, E, topk, dtype="bfloat16") -> moe_lora_sort_shape:
@@ -840,9 +886,10 @@ def alloc_sort_workspace(shape: moe_lora_sort_shape, device="cuda"):
 
 
 def _row_type(shape) -> str:
-    if shape.dtype not in _ROW_TYPES:
+    name = _ROW_TYPES.get(shape.dtype)
+    if name is None:
         raise ValueError(f"shape: dtype {shape.dtype}, expected one of {sorted(_ROW_TYPES)}")
-    return _ROW_TYPES[shape.dtype]
+    return name
 
 
 def moe_lora_sort(shape, topk_ids, x, workspace, rows, expert_off, row_of_pair, pair_of_row=None,
@@ -852,41 +899,41 @@ def moe_lora_sort(shape, topk_ids, x, workspace, rows, expert_off, row_of_pair, 
     alone).  expert_off [E+1], row_of_pair [T, k] and pair_of_row [T k] are
     int32 and written."""
     T, k, dtype = shape.T, shape.topk, _row_type(shape)
-    specs = [("topk_ids", topk_ids, (T, k), "int32"),
-             _check_workspace(workspace, moe_lora_sort_workspace_bytes(shape), "alloc_sort_workspace"),
-             ("expert_off", expert_off, (shape.E + 1,), "int32"), ("row_of_pair", row_of_pair, (T, k), "int32")]
+    specs = [("topk_ids", topk_ids, (T, k), "int32"), ("expert_off", expert_off, (shape.E + 1,), "int32"),
+             ("row_of_pair", row_of_pair, (T, k), "int32")]
     if x is not None or rows is not None:
-        specs += [("x", x, (T, shape.H), dtype), ("rows", rows, (T * k, shape.H), dtype)]
+        H = shape.H
+        specs += [("x", x, (T, H), dtype), ("rows", rows, (T * k, H), dtype)]
     if pair_of_row is not None:
         specs.append(("pair_of_row", pair_of_row, (T * k,), "int32"))
-    _check_tensors(specs)
-    _check("moe_lora_sort", load_library().moe_lora_sort(
+    ws = (workspace, lambda: moe_lora_sort_workspace_bytes(shape), "alloc_sort_workspace")
+    dev = _operands(specs, ws)
+    _done("moe_lora_sort", load_library().moe_lora_sort(
         ctypes.byref(shape), topk_ids.data_ptr(), None if x is None else x.data_ptr(), workspace.data_ptr(),
         workspace.numel(), None if rows is None else rows.data_ptr(), expert_off.data_ptr(), row_of_pair.data_ptr(),
-        None if pair_of_row is None else pair_of_row.data_ptr(), _stream(stream)))
+        None if pair_of_row is None else pair_of_row.data_ptr(), _handle(stream, dev)), ws)
 
 
 def moe_lora_sort_backward(shape, drows, row_of_pair, dx, stream=None) -> None:
     """dx [T, H]: each token's sum of its pairs' rows of drows [T k, H]."""
-    T, k, dtype = shape.T, shape.topk, _row_type(shape)
-    _check_tensors([("drows", drows, (T * k, shape.H), dtype), ("row_of_pair", row_of_pair, (T, k), "int32"),
-                    ("dx", dx, (T, shape.H), dtype)])
-    _check("moe_lora_sort_backward", load_library().moe_lora_sort_backward(
-        ctypes.byref(shape), drows.data_ptr(), row_of_pair.data_ptr(), dx.data_ptr(), _stream(stream)))
+    T, H, k, dtype = shape.T, shape.H, shape.topk, _row_type(shape)
+    dev = _operands((("drows", drows, (T * k, H), dtype), ("row_of_pair", row_of_pair, (T, k), "int32"),
+                     ("dx", dx, (T, H), dtype)))
+    _done("moe_lora_sort_backward", load_library().moe_lora_sort_backward(
+        ctypes.byref(shape), drows.data_ptr(), row_of_pair.data_ptr(), dx.data_ptr(), _handle(stream, dev)))
 
 
 def moe_lora_unsort(shape, rows, row_of_pair, y, weights=None, stream=None) -> None:
     """y [T, H]: each token's sum of its pairs' rows [T k, H], times weights
     [T, k] (fp32; None: ones)."""
-    T, k, dtype = shape.T, shape.topk, _row_type(shape)
-    specs = [("rows", rows, (T * k, shape.H), dtype), ("row_of_pair", row_of_pair, (T, k), "int32"),
-             ("y", y, (T, shape.H), dtype)]
+    T, H, k, dtype = shape.T, shape.H, shape.topk, _row_type(shape)
+    specs = [("rows", rows, (T * k, H), dtype), ("row_of_pair", row_of_pair, (T, k), "int32"), ("y", y, (T, H), dtype)]
     if weights is not None:
         specs.append(("weights", weights, (T, k), "float32"))
-    _check_tensors(specs)
-    _check("moe_lora_unsort", load_library().moe_lora_unsort(
+    dev = _operands(specs)
+    _done("moe_lora_unsort", load_library().moe_lora_unsort(
         ctypes.byref(shape), rows.data_ptr(), row_of_pair.data_ptr(),
-        None if weights is None else weights.data_ptr(), y.data_ptr(), _stream(stream)))
+        None if weights is None else weights.data_ptr(), y.data_ptr(), _handle(stream, dev)))
 
 
 def moe_lora_unsort_backward(shape, dy, rows, row_of_pair, drows=None, weights=None, dweights=None,
@@ -894,26 +941,26 @@ def moe_lora_unsort_backward(shape, dy, rows, row_of_pair, drows=None, weights=N
     """Gradients of moe_lora_unsort from dy [T, H] into those of drows [T k,
     H] and dweights [T, k] (fp32) that are given; rows (as given to the
     forward) are needed for dweights alone."""
-    T, k, dtype = shape.T, shape.topk, _row_type(shape)
-    specs = [("dy", dy, (T, shape.H), dtype), ("row_of_pair", row_of_pair, (T, k), "int32")]
-    opt = (("rows", rows, (T * k, shape.H), dtype), ("weights", weights, (T, k), "float32"),
-           ("drows", drows, (T * k, shape.H), dtype), ("dweights", dweights, (T, k), "float32"))
+    T, H, k, dtype = shape.T, shape.H, shape.topk, _row_type(shape)
+    specs = [("dy", dy, (T, H), dtype), ("row_of_pair", row_of_pair, (T, k), "int32")]
+    opt = (("rows", rows, (T * k, H), dtype), ("weights", weights, (T, k), "float32"),
+           ("drows", drows, (T * k, H), dtype), ("dweights", dweights, (T, k), "float32"))
     specs += [s for s in opt if s[1] is not None]
-    _check_tensors(specs)
+    dev = _operands(specs)
     p = [None if s[1] is None else s[1].data_ptr() for s in opt]
-    _check("moe_lora_unsort_backward", load_library().moe_lora_unsort_backward(
-        ctypes.byref(shape), dy.data_ptr(), p[0], row_of_pair.data_ptr(), p[1], p[2], p[3], _stream(stream)))
+    _done("moe_lora_unsort_backward", load_library().moe_lora_unsort_backward(
+        ctypes.byref(shape), dy.data_ptr(), p[0], row_of_pair.data_ptr(), p[1], p[2], p[3], _handle(stream, dev)))
 
 
 def moe_lora_route_backward(shape, topk_ids, topk_weights, dweights, dlogits, stream=None) -> None:
     """The gradient of moe_lora_route's weights: dlogits [T, E] from dweights
     [T, k] (both fp32) and what the router wrote."""
     T, k = shape.T, shape.topk
-    _check_tensors([("topk_ids", topk_ids, (T, k), "int32"), ("topk_weights", topk_weights, (T, k), "float32"),
-                    ("dweights", dweights, (T, k), "float32"), ("dlogits", dlogits, (T, shape.E), "float32")])
-    _check("moe_lora_route_backward", load_library().moe_lora_route_backward(
+    dev = _operands((("topk_ids", topk_ids, (T, k), "int32"), ("topk_weights", topk_weights, (T, k), "float32"),
+                     ("dweights", dweights, (T, k), "float32"), ("dlogits", dlogits, (T, shape.E), "float32")))
+    _done("moe_lora_route_backward", load_library().moe_lora_route_backward(
         ctypes.byref(shape), topk_ids.data_ptr(), topk_weights.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(),
-        _stream(stream)))
+        _handle(stream, dev)))
 
 
 # ------------------------------------------------------------------ a shared projection with adapters
@@ -938,29 +985,23 @@ def alloc_proj_workspace(shape: moe_lora_proj_shape, backward: bool = True, devi
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _proj_weights(shape, lora_ids, W, A, B, scales):
-    T, K, N, L, r = shape.T, shape.K, shape.N, shape.L, shape.r
-    specs = [("lora_ids", lora_ids, (T,), "int32"), ("W", W, (N, K), "bfloat16"), ("A", A, (L, r, K), "bfloat16"),
-             ("B", B, (L, N, r), "bfloat16")]
-    if scales is not None:
-        specs.append(("scales", scales, (L,), "float32"))
-    return specs
-
-
 def moe_lora_proj_forward(shape, x, lora_ids, W, A, B, workspace, y, z=None, scales=None, stream=None) -> None:
     """y [T, N] = x W^T + s_l (x A_l^T) B_l^T with each token's own adapter l =
     lora_ids[t] (-1: none), s_l = lora_scale * scales[l]; with z ([T, r] fp32)
     x A_l^T is kept there for moe_lora_proj_backward."""
-    specs = [("x", x, (shape.T, shape.K), "bfloat16"), ("y", y, (shape.T, shape.N), "bfloat16"),
-             *_proj_weights(shape, lora_ids, W, A, B, scales),
-             _check_workspace(workspace, moe_lora_proj_workspace_bytes(shape, False), "alloc_proj_workspace")]
+    T, K, N, L, r = shape.T, shape.K, shape.N, shape.L, shape.r
+    specs = [("x", x, (T, K), "bfloat16"), ("lora_ids", lora_ids, (T,), "int32"), ("W", W, (N, K), "bfloat16"),
+             ("A", A, (L, r, K), "bfloat16"), ("B", B, (L, N, r), "bfloat16"), ("y", y, (T, N), "bfloat16")]
+    if scales is not None:
+        specs.append(("scales", scales, (L,), "float32"))
     if z is not None:
-        specs.append(("z", z, (shape.T, shape.r), "float32"))
-    _check_tensors(specs)
-    _check("moe_lora_proj_forward", load_library().moe_lora_proj_forward(
+        specs.append(("z", z, (T, r), "float32"))
+    ws = (workspace, lambda: moe_lora_proj_workspace_bytes(shape, False), "alloc_proj_workspace")
+    dev = _operands(specs, ws)
+    _done("moe_lora_proj_forward", load_library().moe_lora_proj_forward(
         ctypes.byref(shape), x.data_ptr(), lora_ids.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(),
         None if scales is None else scales.data_ptr(), None if z is None else z.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), y.data_ptr(), _stream(stream)))
+        workspace.numel(), y.data_ptr(), _handle(stream, dev)), ws)
 
 
 def moe_lora_proj_backward(shape, dy, x, lora_ids, z, W, A, B, workspace, dx=None, dA=None, dB=None, scales=None,
@@ -968,16 +1009,19 @@ def moe_lora_proj_backward(shape, dy, x, lora_ids, z, W, A, B, workspace, dx=Non
     """Gradients of the projection from dy and the kept z into those of dx, dA
     and dB that are given (overwritten); W is frozen."""
     T, K, N, L, r = shape.T, shape.K, shape.N, shape.L, shape.r
-    specs = [("dy", dy, (T, N), "bfloat16"), ("x", x, (T, K), "bfloat16"), ("z", z, (T, r), "float32"),
-             *_proj_weights(shape, lora_ids, W, A, B, scales),
-             _check_workspace(workspace, moe_lora_proj_workspace_bytes(shape, True), "alloc_proj_workspace")]
-    outs = (("dx", dx, (T, K)), ("dA", dA, (L, r, K)), ("dB", dB, (L, N, r)))
-    specs += [(n, t, s, "bfloat16") for n, t, s in outs if t is not None]
-    _check_tensors(specs)
-    _check("moe_lora_proj_backward", load_library().moe_lora_proj_backward(
+    specs = [("dy", dy, (T, N), "bfloat16"), ("x", x, (T, K), "bfloat16"), ("lora_ids", lora_ids, (T,), "int32"),
+             ("z", z, (T, r), "float32"), ("W", W, (N, K), "bfloat16"), ("A", A, (L, r, K), "bfloat16"),
+             ("B", B, (L, N, r), "bfloat16")]
+    if scales is not None:
+        specs.append(("scales", scales, (L,), "float32"))
+    outs = (("dx", dx, (T, K), "bfloat16"), ("dA", dA, (L, r, K), "bfloat16"), ("dB", dB, (L, N, r), "bfloat16"))
+    specs += [s for s in outs if s[1] is not None]
+    ws = (workspace, lambda: moe_lora_proj_workspace_bytes(shape, True), "alloc_proj_workspace")
+    dev = _operands(specs, ws)
+    _done("moe_lora_proj_backward", load_library().moe_lora_proj_backward(
         ctypes.byref(shape), dy.data_ptr(), x.data_ptr(), lora_ids.data_ptr(), z.data_ptr(), W.data_ptr(),
         A.data_ptr(), B.data_ptr(), None if scales is None else scales.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), *[None if t is None else t.data_ptr() for _, t, _ in outs], _stream(stream)))
+        workspace.numel(), *[None if s[1] is None else s[1].data_ptr() for s in outs], _handle(stream, dev)), ws)
 
 
 def lora_projection(x, lora_ids, W, A, B, lora_scale=1.0, scales=None, workspace=None, y=None, stream=None):

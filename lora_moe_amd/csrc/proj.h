@@ -93,8 +93,16 @@ int proj_grad_rows(int T, int K, int N, int r);
 size_t proj_grad_slab_bytes(int T, int K, int N, int r);
 int launch_proj_grads(const ProjArgs& p, const ProjGrads& g, hipStream_t st);
 
-// The whole forward of at most kProjRows tokens.
-size_t proj_rows_slab_bytes(int T, int K, int N, int L, int r);
+// x [W; A]^T for all adapters, fp32, into slabs [proj_both_splits][T][N + L r].
+int proj_both_splits(const ProjArgs& p);
+int launch_proj_both(const ProjArgs& p, const uint16_t* x, const uint16_t* W, const uint16_t* A, float* slabs,
+                     hipStream_t st);
+
+// Whether a forward takes the two launches of proj_rows.hip, which need no
+// order: up to kProjRows tokens, and beyond them where the adapters' A are few
+// columns beside W's and the tokens' shares of B are little to read one by one.
+bool proj_few(int T, int N, int L, int r);
+size_t proj_rows_slab_bytes(const ProjArgs& p);
 int launch_proj_rows(const ProjArgs& p, const uint16_t* x, const uint16_t* W, const uint16_t* A, const uint16_t* B,
                      float* z, float* slabs, uint16_t* y, hipStream_t st);
 

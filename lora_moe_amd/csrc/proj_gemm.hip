@@ -18,7 +18,9 @@
 // rows that they belong to, one by one, in its epilogue.
 //
 // The loop is that of ffn_gemm.hip: a two-stage ring filled by asynchronous
-// copies that go out between the MFMAs of the stage before.
+// copies that go out between the MFMAs of the stage before.  The adapters'
+// shares are further stages of the same loop, whose copies get their addresses
+// when their turn comes.
 #include "ffn.h"
 #include "internal.h"
 #include "proj.h"
@@ -33,6 +35,7 @@ struct TileArgs {
   ProjGemm g;
   int in_cols, out_cols;  // K and N of a forward
   int ncol, nrow;
+  int ncol_w;             // BOTH: column tiles of W, then those of the adapters
 };
 
 template <class C>
@@ -70,7 +73,10 @@ __device__ __noinline__ Eight add_not_finite(Eight e, const uint16_t* z, const u
   return e;
 }
 
-template <bool BACK, class C, bool SPLIT>
+// BOTH (forward, SPLIT): x [W; A]^T instead, all adapters' A behind W as further
+// columns, tokens in their own order, all of it fp32 into the slabs
+// [splits][T][N + L r].
+template <bool BACK, class C, bool SPLIT, bool BOTH>
 __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
   constexpr bool B_KC = !BACK;
   constexpr int MI = C::MI, NI = C::NI;
@@ -83,7 +89,7 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
-  const int T = p.T, N = a.out_cols, K = a.in_cols, r = p.r, ncol = a.ncol, nrow = a.nrow;
+  const int T = p.T, K = a.in_cols, r = p.r, ncol = a.ncol, nrow = a.nrow;
 
   // workgroups to tiles as in ffn_gemm.hip: each XCD a contiguous eighth, in
   // panels of 4 row tiles
@@ -99,21 +105,86 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
   const int panel = t / (GM * ncol), in = t - panel * GM * ncol;
   const int gm = min(GM, nrow - panel * GM);
   const int tn = in / gm, tm = panel * GM + in - tn * gm;
-  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  const bool is_w = !BOTH || tn < a.ncol_w;
+  const int m0 = tm * C::BM, n0 = (is_w ? tn : tn - a.ncol_w) * C::BN;
+  const int N = is_w ? a.out_cols : p.L * r;
+  auto token_of = [&](int m) { return BOTH ? m : p.o.perm[m]; };
+
+  // Stages: those of the shared weights, then those of the tile's shares;
+  // column kx of the latter's part of K is value kx % 2r of share kx / 2r.
+  const int last = min(m0 + C::BM, T) - 1, r2 = 2 * r;
+  const int run0 = BOTH ? 0 : p.o.run[m0], with = BOTH ? 0 : p.o.count[2];  // runs from `with` on: without an adapter
+  const int shares = BOTH ? 0 : max(0, min(p.o.run[last] + 1, with) - run0);
+  const int base = (K + BK - 1) / BK, kfirst = K - base * BK;
+  const int total = base + (shares * r2 + BK - 1) / BK;
+  // this split's
+  const int s0 = SPLIT ? (int)((int64_t)total * split / a.g.splits) : 0;
+  const int nst = SPLIT ? (int)((int64_t)total * (split + 1) / a.g.splits) : total;
 
   Operand<true, C::BM, C::NCA, false> A;
   Operand<B_KC, C::BN, C::NCB, false> B;
-  const int all = (K + BK - 1) / BK, kfirst = K - all * BK;
-  const int s0 = SPLIT ? (int)((int64_t)all * split / a.g.splits) : 0;
-  const int nst = SPLIT ? (int)((int64_t)all * (split + 1) / a.g.splits) : all;
   A.init(a.g.in, 0, K, 0, kfirst, wave, 0);
 #pragma unroll
   for (int i = 0; i < C::NCA; ++i) {  // its rows from anywhere
     const int rr = (wave * C::NCA + i) * 8 + (lane >> 3), ch = (lane & 7) ^ ((rr >> 1) & 7);
-    A.off[i] = m0 + rr < T ? ((uint32_t)p.o.perm[m0 + rr] * (uint32_t)K + ch * 8u) * 2u : kBufNone;
+    A.off[i] = m0 + rr < T ? ((uint32_t)token_of(m0 + rr) * (uint32_t)K + ch * 8u) * 2u : kBufNone;
   }
   const int64_t ldw = BACK ? N : K;
-  B.init(B_KC ? a.g.W + (int64_t)n0 * ldw : a.g.W + n0, 0, ldw, N - n0, kfirst, wave, 0);
+  const uint16_t* w = is_w ? a.g.W : a.g.weights;
+  B.init(B_KC ? w + (int64_t)n0 * ldw : w + n0, 0, ldw, N - n0, kfirst, wave, 0);
+
+  // the tile's rows and adapters
+  for (int i = threadIdx.x; i < C::BM; i += C::NT) {
+    const int m = m0 + i;
+    int tok = -1, sh = -1;
+    if (m < T) {
+      tok = token_of(m);
+      const int run = BOTH ? 0 : p.o.run[m];
+      if (run < with) {
+        sh = run - run0;
+        if (i == 0 || p.o.run[m - 1] != run) adapter[sh] = p.o.adapter[run];
+      }
+    }
+    token[i] = tok;
+    share[i] = sh;
+  }
+  if (threadIdx.x == 0) *not_finite = 0;
+
+  // what copy() brings next: stage s, or, behind the split's last, zeros
+  auto at = [&](int s) __attribute__((always_inline)) {
+    if (s < base || s >= nst) {
+      A.at(s, s < nst);
+      B.at(s, s < nst);
+      return;
+    }
+    A.rs = rsrc_of(a.g.pairs, 0x7fffffffu);
+    B.rs = rsrc_of(a.g.weights, 0x7fffffffu);
+    A.soff = B.soff = 0;
+    const int k0 = (s - base) * BK;
+#pragma unroll
+    for (int i = 0; i < C::NCA; ++i) {
+      const int rr = (wave * C::NCA + i) * 8 + (lane >> 3), ch = (lane & 7) ^ ((rr >> 1) & 7);
+      const int kx = k0 + ch * 8, q = kx / r2;
+      A.off[i] = share[rr] == q ? ((uint32_t)(m0 + rr) * r2 + (kx - q * r2)) * 2u : kBufNone;
+    }
+#pragma unroll
+    for (int i = 0; i < C::NCB; ++i) {
+      const int c = wave * C::NCB + i;
+      uint32_t off = kBufNone;
+      if (B_KC) {
+        const int nn = c * 8 + (lane >> 3), ch = (lane & 7) ^ ((nn >> 1) & 7);
+        const int kx = k0 + ch * 8, q = kx / r2, w = kx - q * r2;
+        if (q < shares && n0 + nn < N) off = (((uint32_t)adapter[q] * N + n0 + nn) * r + (w < r ? w : w - r)) * 2u;
+      } else {
+        constexpr int PER = 1024 / (C::BN * 2), LPR = C::BN / 8;
+        const int k = c * PER + lane / LPR, ch = (lane % LPR) ^ (4 * (k & 3));
+        const int kx = k0 + k, q = kx / r2, w = kx - q * r2;
+        if (q < shares && n0 + ch * 8 < N)
+          off = (((uint32_t)adapter[q] * r + (w < r ? w : w - r)) * N + n0 + ch * 8) * 2u;
+      }
+      B.off[i] = off;
+    }
+  };
 
   f32x16_t acc[MI][NI];
 #pragma unroll
@@ -125,15 +196,21 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
 
   const uint32_t smem_at = (uint32_t)(uintptr_t)(lds_char*)smem;
   u32x4_t af[2][MI], bf[2][NI];
+  bool bad = false;
   auto read = [&](int slot, int kk, int set, int i) __attribute__((always_inline)) {
-    const char* at = smem + slot * C::STAGE;
-    if (i == 0) af[set][0] = A.frag(at, wm * (C::BM / C::WM), 0, kk);
-    else if (i <= NI) bf[set][i - 1] = B.frag(at + C::ABYTES, wn * (C::BN / C::WN), i - 1, kk);
-    else af[set][i - NI] = A.frag(at, wm * (C::BM / C::WM), i - NI, kk);
+    const char* from = smem + slot * C::STAGE;
+    if (i == 0) af[set][0] = A.frag(from, wm * (C::BM / C::WM), 0, kk);
+    else if (i <= NI) bf[set][i - 1] = B.frag(from + C::ABYTES, wn * (C::BN / C::WN), i - 1, kk);
+    else af[set][i - NI] = A.frag(from, wm * (C::BM / C::WM), i - NI, kk);
   };
   constexpr int NM = MI * NI, NF = MI + NI, NC = C::NCA + C::NCB;
-  auto slice = [&](int set, int slot, int kk, auto issue_c) __attribute__((always_inline)) {
+  // shared: the stage is one of the shared weights'; MIXED: it need not be
+  auto slice = [&](bool shared, int set, int slot, int kk, auto issue_c, auto mixed_c) __attribute__((always_inline)) {
     constexpr bool ISSUE = decltype(issue_c)::value;
+    if (decltype(mixed_c)::value && !shared) {
+#pragma unroll
+      for (int j = 0; j < NI; ++j) bad |= only_finite(bf[set][j]);
+    }
     for_each<NM>([&](auto n_c) __attribute__((always_inline)) {
       constexpr int n = decltype(n_c)::value, i = n / NI, j = n % NI;
       acc[i][j] = mfma_32x32x16(bf[set][j], af[set][i], acc[i][j]);
@@ -152,8 +229,13 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
   };
   typedef std::integral_constant<bool, true> yes;
   typedef std::integral_constant<bool, false> no;
-  A.at(s0, s0 < nst);
-  B.at(s0, s0 < nst);
+  if (!SPLIT || s0 < base) {
+    A.at(s0, true);
+    B.at(s0, true);
+  } else {
+    lds_barrier();  // share and adapter are written
+    at(s0);
+  }
   if (s0 == 0) {
     for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, true>(smem_at, wave, kfirst); });
     for_each<C::NCB>([&](auto i) { B.template copy<decltype(i)::value, true>(smem_at + C::ABYTES, wave, kfirst); });
@@ -161,107 +243,48 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
     for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, false>(smem_at, wave, 0); });
     for_each<C::NCB>([&](auto i) { B.template copy<decltype(i)::value, false>(smem_at + C::ABYTES, wave, 0); });
   }
-  A.at(s0 + 1, s0 + 1 < nst);
-  B.at(s0 + 1, s0 + 1 < nst);
+  lds_barrier();
+  at(s0 + 1);
   for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, false>(smem_at + C::STAGE, wave, 0); });
   for_each<C::NCB>(
       [&](auto i) { B.template copy<decltype(i)::value, false>(smem_at + C::STAGE + C::ABYTES, wave, 0); });
-  // the tile's rows and adapters, while the first copies are on their way
-  const int last = min(m0 + C::BM, T) - 1;
-  const int run0 = p.o.run[m0], with = p.o.count[2];  // runs from `with` on: without an adapter
-  const int shares = SPLIT && split + 1 < a.g.splits ? 0 : max(0, min(p.o.run[last] + 1, with) - run0);
-  for (int i = threadIdx.x; i < C::BM; i += C::NT) {
-    const int m = m0 + i;
-    int tok = -1, sh = -1;
-    if (m < T) {
-      tok = p.o.perm[m];
-      const int run = p.o.run[m];
-      if (run < with) {
-        sh = run - run0;
-        if (i == 0 || p.o.run[m - 1] != run) adapter[sh] = p.o.adapter[run];
-      }
-    }
-    token[i] = tok;
-    share[i] = sh;
-  }
-  if (threadIdx.x == 0) *not_finite = 0;
   __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);
   bare_barrier();
 #pragma unroll
   for (int i = 0; i < NF; ++i) read(0, 0, 0, i);
-  for (int s = s0; s < nst; s += 2) {
+  // Two loops of the same steps: one that meets and brings nothing but the
+  // shared weights, and one for the stages around their end and behind it (as
+  // one loop with its branches 242 us where this takes 218: 8192 tokens, 4096 x
+  // 4096, rank 16).
+  auto two = [&](int s, auto mixed_c) __attribute__((always_inline)) {
+    constexpr bool MIXED = decltype(mixed_c)::value;
     for_each<2>([&](auto h_c) __attribute__((always_inline)) {
       constexpr int slot = decltype(h_c)::value;
-      slice(0, slot, 1, no());
-      slice(1, slot, 2, no());
-      A.at(s + slot + 2, s + slot + 2 < nst);
-      B.at(s + slot + 2, s + slot + 2 < nst);
-      slice(0, slot, 3, no());
+      const bool shared = s + slot < base;
+      slice(shared, 0, slot, 1, no(), mixed_c);
+      slice(shared, 1, slot, 2, no(), mixed_c);
+      if constexpr (MIXED) {
+        at(s + slot + 2);
+      } else {
+        A.at(s + slot + 2, true);
+        B.at(s + slot + 2, true);
+      }
+      slice(shared, 0, slot, 3, no(), mixed_c);
+      // own copies of the next stage have landed, own reads of this one are done
       __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);
       bare_barrier();
-      slice(1, slot ^ 1, 0, yes());
+      slice(shared, 1, slot ^ 1, 0, yes(), mixed_c);
     });
-  }
+  };
+  int s = s0;
+#pragma unroll 1
+  for (; s + 3 < min(base, nst); s += 2) two(s, no());
+#pragma unroll 1
+  for (; s < nst; s += 2) two(s, yes());
+  if (bad) *not_finite = 1;
   __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);  // no copy outlives the loop
   bare_barrier();
-
-  // The adapters' shares: column kx of this part of K is value kx % 2r of
-  // share kx / 2r.
-  const int r2 = 2 * r, extra = (shares * r2 + BK - 1) / BK;
-  if (extra) {
-    const u32x4_t rz = rsrc_of(a.g.pairs, 0x7fffffffu), rw = rsrc_of(a.g.weights, 0x7fffffffu);
-    auto bring = [&](int e) __attribute__((always_inline)) {
-      const uint32_t to = smem_at + (e & 1) * C::STAGE;
-      for_each<C::NCA>([&](auto i_c) __attribute__((always_inline)) {
-        constexpr int i = decltype(i_c)::value;
-        const int rr = (wave * C::NCA + i) * 8 + (lane >> 3), ch = (lane & 7) ^ ((rr >> 1) & 7);
-        const int kx = e * BK + ch * 8, q = kx / r2;
-        const uint32_t off = share[rr] == q ? ((uint32_t)(m0 + rr) * r2 + (kx - q * r2)) * 2u : kBufNone;
-        copy16<i * 1024>(rz, to + wave * (C::NCA * 1024), off, 0);
-      });
-      for_each<C::NCB>([&](auto i_c) __attribute__((always_inline)) {
-        constexpr int i = decltype(i_c)::value;
-        const int c = wave * C::NCB + i;
-        uint32_t off = kBufNone;
-        if (B_KC) {
-          const int nn = c * 8 + (lane >> 3), ch = (lane & 7) ^ ((nn >> 1) & 7);
-          const int kx = e * BK + ch * 8, q = kx / r2, w = kx - q * r2;
-          if (q < shares && n0 + nn < N)
-            off = (((uint32_t)adapter[q] * N + n0 + nn) * r + (w < r ? w : w - r)) * 2u;
-        } else {
-          constexpr int PER = 1024 / (C::BN * 2), LPR = C::BN / 8;
-          const int k = c * PER + lane / LPR, ch = (lane % LPR) ^ (4 * (k & 3));
-          const int kx = e * BK + k, q = kx / r2, w = kx - q * r2;
-          if (q < shares && n0 + ch * 8 < N)
-            off = (((uint32_t)adapter[q] * r + (w < r ? w : w - r)) * N + n0 + ch * 8) * 2u;
-        }
-        copy16<i * 1024>(rw, to + C::ABYTES + wave * (C::NCB * 1024), off, 0);
-      });
-    };
-    bool bad = false;
-    bring(0);
-#pragma unroll 1
-    for (int e = 0; e < extra; ++e) {
-      __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);
-      bare_barrier();  // this stage has landed, the other one's reads are done
-      if (e + 1 < extra) bring(e + 1);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-#pragma unroll
-        for (int i = 0; i < NF; ++i) read(e & 1, kk, 0, i);
-#pragma unroll
-        for (int j = 0; j < NI; ++j) bad |= only_finite(bf[0][j]);
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-          for (int j = 0; j < NI; ++j) acc[i][j] = mfma_32x32x16(bf[0][j], af[0][i], acc[i][j]);
-      }
-    }
-    if (bad) *not_finite = 1;
-    __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);
-    bare_barrier();
-  }
-  const bool mend = extra && *not_finite;
+  const bool mend = *not_finite;
 
   // Epilogue, 32 rows of the wavefront at a time through its own part of the
   // LDS, so that memory sees whole lines (as in ffn_gemm.hip).
@@ -291,6 +314,7 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
       if (tok < 0 || n >= N) continue;
       const f32x4_t* src = reinterpret_cast<const f32x4_t*>(mine + (s * RPI + lane / LPR) * ROWF + oc);
       Eight e = {{src[0], src[1]}};
+      // (with K split the shares' terms are added by the split that met them)
       if (mend && share[rr] >= 0) {
         const int64_t first = (int64_t)adapter[share[rr]] * N * r;
         e = add_not_finite(e, a.g.pairs + (int64_t)(m0 + rr) * r2, a.g.weights + first + (BACK ? n : (int64_t)n * r),
@@ -298,7 +322,8 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
       }
       const f32x4_t* v = e.v;
       if (SPLIT) {
-        f32x4_t* dst = reinterpret_cast<f32x4_t*>(a.g.slabs + ((int64_t)split * T + m0 + rr) * N + n);
+        const int cols = BOTH ? a.out_cols + p.L * r : N, c = is_w ? n : a.out_cols + n;
+        f32x4_t* dst = reinterpret_cast<f32x4_t*>(a.g.slabs + ((int64_t)split * T + m0 + rr) * cols + c);
         dst[0] = v[0];
         dst[1] = v[1];
       } else {
@@ -328,26 +353,30 @@ __global__ __launch_bounds__(256) void proj_join_kernel(TileArgs a) {
 typedef FfnCfg<256, 256, 2, 4> Big;
 typedef FfnCfg<128, 128, 2, 2> Small;
 
-template <bool BACK, class C, bool SPLIT>
+template <bool BACK, class C, bool SPLIT, bool BOTH = false>
 int launch_cfg(TileArgs a, hipStream_t st) {
   static std::atomic<uint64_t> attr_done;
-  const int64_t ncol = (a.out_cols + C::BN - 1) / C::BN, nrow = (a.p.T + C::BM - 1) / C::BM;
+  a.ncol_w = (a.out_cols + C::BN - 1) / C::BN;
+  const int64_t ncol = a.ncol_w + (BOTH ? (a.p.L * a.p.r + C::BN - 1) / C::BN : 0), nrow = (a.p.T + C::BM - 1) / C::BM;
   const int64_t grid = ncol * nrow * a.g.splits;
   if (grid * C::NT > 0xffffffff) return MOE_LORA_EUNSUPPORTED;
   a.ncol = (int)ncol;
   a.nrow = (int)nrow;
-  const void* fn = reinterpret_cast<const void*>(&proj_tile_kernel<BACK, C, SPLIT>);
+  const void* fn = reinterpret_cast<const void*>(&proj_tile_kernel<BACK, C, SPLIT, BOTH>);
   const int rc = ensure_dynamic_lds(fn, tile_lds<C>(), attr_done);
   if (rc) return rc;
-  proj_tile_kernel<BACK, C, SPLIT><<<(unsigned)grid, C::NT, tile_lds<C>(), st>>>(a);
-  if (SPLIT) {
+  proj_tile_kernel<BACK, C, SPLIT, BOTH><<<(unsigned)grid, C::NT, tile_lds<C>(), st>>>(a);
+  if (SPLIT && !BOTH) {
     const int64_t n = (int64_t)a.p.T * (a.out_cols / 8);
     proj_join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
   }
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
-TilePlan plan_of(const ProjArgs& p, bool back) { return tile_plan(p.T, back ? p.K : p.N, back ? p.N : p.K); }
+// (two shares a tile: what a tile of several requests has)
+TilePlan plan_of(const ProjArgs& p, bool back) {
+  return tile_plan(p.T, back ? p.K : p.N, (back ? p.N : p.K) + 4 * p.r);
+}
 
 template <bool BACK>
 int launch(TileArgs a, hipStream_t st) {
@@ -365,8 +394,19 @@ size_t proj_gemm_slab_bytes(const ProjArgs& p, bool back) {
 }
 
 int launch_proj_gemm(const ProjArgs& p, bool back, ProjGemm g, hipStream_t st) {
-  const TileArgs a{p, g, back ? p.N : p.K, back ? p.K : p.N, 0, 0};
+  const TileArgs a{p, g, back ? p.N : p.K, back ? p.K : p.N, 0, 0, 0};
   return back ? launch<true>(a, st) : launch<false>(a, st);
+}
+
+int proj_both_splits(const ProjArgs& p) {
+  const TilePlan f = tile_plan(p.T, p.N + p.L * p.r, p.K);
+  return f.big ? 1 : f.splits;
+}
+
+int launch_proj_both(const ProjArgs& p, const uint16_t* x, const uint16_t* W, const uint16_t* A, float* slabs,
+                     hipStream_t st) {
+  const ProjGemm g{x, W, nullptr, A, nullptr, slabs, proj_both_splits(p)};
+  return launch_cfg<false, Small, true, true>(TileArgs{p, g, p.K, p.N, 0, 0, 0}, st);
 }
 
 }  // namespace moelora

@@ -2,8 +2,8 @@
 //
 // One launch: every workgroup counts all tokens' adapters for itself (the ids
 // are a few KB in the L2 cache, and integer counts do not depend on the order
-// of the LDS atomics), then places its own tokens.  The first workgroup writes
-// the runs' tables as well.  8192 tokens, 8 adapters: 8 us.
+// of the LDS atomics), then places its own 256 tokens.  The first workgroup
+// writes the runs' tables as well.
 #include "proj.h"
 #include "sort_util.h"
 
@@ -11,27 +11,53 @@ namespace moelora {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 1024, kTokens = 256;  // of a workgroup; the tokens that it places
 
 // ids outside [0, L) have no adapter
-__device__ __forceinline__ int key_of(const ProjArgs& p, int t) {
-  const int l = p.ids[t];
-  return l >= 0 && l < p.L ? l : p.L;
+__device__ __forceinline__ int key_of(int l, int L) { return l >= 0 && l < L ? l : L; }
+
+// Counts the lanes' keys (< 0: none) into total, those with `early` into next
+// too.  A run of tokens has one adapter: lanes with the same key as the first
+// that is left are counted together, a few times, and only the rest one by
+// one (atomics on one address follow each other).
+__device__ __forceinline__ void count_keys(int key, bool early, int* total, int* next) {
+  const int lane = threadIdx.x & 63;
+  uint64_t left = __ballot(key >= 0);
+  const uint64_t before = __ballot(early);
+#pragma unroll 1
+  for (int i = 0; i < 4 && left; ++i) {
+    const int first = __builtin_ctzll(left), k = __builtin_amdgcn_readlane(key, first);
+    const uint64_t same = __ballot(key == k);
+    if (lane == first) {
+      atomicAdd(&total[k], __popcll(same));
+      if (same & before) atomicAdd(&next[k], __popcll(same & before));
+    }
+    left &= ~same;
+  }
+  if (left >> lane & 1) {
+    atomicAdd(&total[key], 1);
+    if (early) atomicAdd(&next[key], 1);
+  }
 }
 
-// Exclusive scan over the keys of f(key), to g(key, sum before); returns the
-// whole sum.  scan: 16 ints of LDS.
+// Exclusive scan over the keys of f(key), to g(key, sum before), by one
+// wavefront; returns the whole sum.
 template <class F, class G>
-__device__ __forceinline__ int scan_keys(int n, int* scan, F&& f, G&& g) {
-  const int per = (n + kThreads - 1) / kThreads, e0 = min(n, (int)threadIdx.x * per), e1 = min(n, e0 + per);
-  int mine = 0, all;
-  for (int e = e0; e < e1; ++e) mine += f(e);
-  int at = block_exclusive_scan<true>(mine, scan, &all);
-  for (int e = e0; e < e1; ++e) {
-    g(e, at);
-    at += f(e);
+__device__ __forceinline__ int scan_keys(int n, F&& f, G&& g) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int e0 = 0; e0 < n; e0 += 64) {
+    const int e = e0 + lane, v = e < n ? f(e) : 0;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(x, o, 64);
+      if (lane >= o) x += y;
+    }
+    if (e < n) g(e, before + x - v);
+    before += __shfl(x, 63, 64);
   }
-  return all;
+  return before;
 }
 
 __device__ __forceinline__ int pieces(int n, int rows) { return (n + rows - 1) / rows; }
@@ -40,66 +66,84 @@ __global__ __launch_bounds__(kThreads) void proj_order_kernel(ProjArgs p, float*
   extern __shared__ __attribute__((aligned(16))) int lds[];
   const int S = p.L + 1;
   int* wkeys = lds;               // [kThreads]
-  int* place = wkeys + kThreads;  // [kThreads]
-  int* keys = place + kThreads;   // [kThreads]
-  int* scan = keys + kThreads;    // [16]
-  int* next = scan + 16;          // [S] next row of each key
+  int* place = wkeys + kThreads;  // [kTokens]
+  int* keys = place + kTokens;    // [kTokens]
+  int* next = keys + kTokens;     // [S] next row of each key
   int* total = next + S;          // [S]
-  int* runs = total + S;          // [S] runs before the key's
-  int* slab = runs + S;           // [S] slabs before the key's
+  int* first = total + S;         // [S] first row, and how many runs, pieces and slabs lie before the key's
+  int* runs = first + S;          // [S]
+  int* shrink = runs + S;         // [S]
+  int* grad = shrink + S;         // [S]
+  int* slab = grad + S;           // [S]
   const int tid = threadIdx.x;
-  const int t0 = blockIdx.x * kThreads, mine = min(kThreads, p.T - t0);
+  const int t0 = blockIdx.x * kTokens, mine = min(kTokens, p.T - t0);
   for (int e = tid; e < S; e += kThreads) next[e] = total[e] = 0;
   lds_barrier();
-  for (int t = tid; t < p.T; t += kThreads) {
-    const int e = key_of(p, t);
-    atomicAdd(&total[e], 1);
-    if (t < t0) atomicAdd(&next[e], 1);
+  for (int base = 0; base < p.T; base += 4 * kThreads) {  // four ids a thread, in flight together
+    int id[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = base + i * kThreads + tid;
+      id[i] = t < p.T ? p.ids[t] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = base + i * kThreads + tid;
+      if (t - (tid & 63) < p.T) count_keys(t < p.T ? key_of(id[i], p.L) : -1, t < t0, total, next);
+    }
   }
   lds_barrier();
-  scan_keys(S, scan, [&](int e) { return (int)(total[e] > 0); }, [&](int e, int at) { runs[e] = at; });
-  scan_keys(S, scan, [&](int e) { return total[e]; }, [&](int e, int at) { next[e] += at; });
-  lds_barrier();
-  if (blockIdx.x == 0) {
-    // (nothing lies before this workgroup's tokens: next is a run's first row)
-    const ProjOrder& o = p.o;
-    for (int e = tid; e < S; e += kThreads)
-      if (total[e]) o.adapter[runs[e]] = e;
-    const int ns = scan_keys(p.L, scan, [&](int e) { return pieces(total[e], p.shrink_rows); },
-                             [&](int e, int at) {
-                               for (int i = 0; i < total[e]; i += p.shrink_rows)
-                                 o.shrink[at++] = ProjItem{e, next[e] + i, min(p.shrink_rows, total[e] - i), -1};
-                             });
-    int ng = 0;
-    if (p.grad_rows) {
-      auto slabs_of = [&](int e) { return total[e] > p.grad_rows ? pieces(total[e], p.grad_rows) : 0; };
-      scan_keys(p.L, scan, slabs_of, [&](int e, int at) {
-        slab[e] = at;
-        o.slabs[2 * e] = at;
-        o.slabs[2 * e + 1] = total[e] ? slabs_of(e) : -1;
-      });
-      // (a thread meets the same keys in every scan)
-      ng = scan_keys(p.L, scan, [&](int e) { return pieces(total[e], p.grad_rows); },
-                     [&](int e, int at) {
-                       const bool split = total[e] > p.grad_rows;
-                       for (int i = 0, s = slab[e]; i < total[e]; i += p.grad_rows, ++s)
-                         o.grad[at++] = ProjItem{e, next[e] + i, min(p.grad_rows, total[e] - i), split ? s : -1};
-                     });
-    }
-    if (tid == 0) {
-      o.count[0] = ns;
-      o.count[1] = ng;
-      o.count[2] = runs[p.L];
-    }
-    lds_barrier();  // before the tokens below move next
+  // The tables, a wavefront each; the first workgroup writes what belongs to
+  // no token.
+  const int wave = tid >> 6;
+  const bool writes = blockIdx.x == 0, counts = writes && (tid & 63) == 0;
+  const ProjOrder& o = p.o;
+  if (wave == 0) {
+    scan_keys(S, [&](int e) { return total[e]; }, [&](int e, int at) {
+      first[e] = at;
+      next[e] += at;
+    });
+  } else if (wave == 1) {
+    const int n = scan_keys(S, [&](int e) { return (int)(total[e] > 0); }, [&](int e, int at) {
+      runs[e] = at;
+      if (writes && total[e]) o.adapter[at] = e;
+    });
+    if (counts) o.count[2] = n - (total[p.L] > 0);
+  } else if (wave == 2) {
+    const int n = scan_keys(p.L, [&](int e) { return pieces(total[e], p.shrink_rows); },
+                            [&](int e, int at) { shrink[e] = at; });
+    if (counts) o.count[0] = n;
+  } else if (wave == 3 && p.grad_rows) {
+    const int n = scan_keys(p.L, [&](int e) { return pieces(total[e], p.grad_rows); },
+                            [&](int e, int at) { grad[e] = at; });
+    if (counts) o.count[1] = n;
+  } else if (wave == 4 && p.grad_rows) {
+    auto slabs_of = [&](int e) { return total[e] > p.grad_rows ? pieces(total[e], p.grad_rows) : 0; };
+    scan_keys(p.L, slabs_of, [&](int e, int at) {
+      slab[e] = at;
+      if (!writes) return;
+      o.slabs[2 * e] = at;
+      o.slabs[2 * e + 1] = total[e] ? slabs_of(e) : -1;
+    });
   }
-  const int key = tid < mine ? key_of(p, t0 + tid) : -1;
+  lds_barrier();
+  const int key = tid < mine ? key_of(p.ids[t0 + tid], p.L) : -1;
   const int row = ordered_rank(key, next, (mine + 63) >> 6, wkeys);
-  place[tid] = row;
-  keys[tid] = key;
   if (key >= 0) {
-    p.o.perm[row] = t0 + tid;
-    p.o.run[row] = runs[key];
+    place[tid] = row;
+    keys[tid] = key;
+    o.perm[row] = t0 + tid;
+    o.run[row] = runs[key];
+    if (key < p.L) {  // a piece is written by its first row's token
+      const int at = row - first[key], left = total[key] - at;
+      if (at % p.shrink_rows == 0)
+        o.shrink[shrink[key] + at / p.shrink_rows] = ProjItem{key, row, min(p.shrink_rows, left), -1};
+      if (p.grad_rows && at % p.grad_rows == 0) {
+        const int i = at / p.grad_rows;
+        o.grad[grad[key] + i] =
+            ProjItem{key, row, min(p.grad_rows, left), total[key] > p.grad_rows ? slab[key] + i : -1};
+      }
+    }
   }
   if (!z && !zs) return;
   lds_barrier();
@@ -127,8 +171,8 @@ __global__ __launch_bounds__(kThreads) void proj_order_kernel(ProjArgs p, float*
 }  // namespace
 
 int launch_proj_order(const ProjArgs& p, float* z, const float* kept, uint16_t* zs, hipStream_t st) {
-  const int lds = (3 * kThreads + 16 + 4 * (p.L + 1)) * 4;  // at most 36 KB
-  proj_order_kernel<<<(p.T + kThreads - 1) / kThreads, kThreads, lds, st>>>(p, z, kept, zs);
+  const int lds = (kThreads + 2 * kTokens + 7 * (p.L + 1)) * 4;  // at most 62 KB
+  proj_order_kernel<<<(p.T + kTokens - 1) / kTokens, kThreads, lds, st>>>(p, z, kept, zs);
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 

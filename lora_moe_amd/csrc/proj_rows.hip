@@ -1,22 +1,27 @@
-// The projection of a few tokens (decode): the weight stream of rows.h over
-// the shared weights and the adapters' A as one matrix.
+// The projection of a decode batch: the shared weights and the adapters' A as
+// one matrix.
 //
-//   first launch   [y0 z'] = x [W; A_l of every adapter met]^T, fp32
+//   first launch   [y0 z'] = x [W; A]^T, fp32
 //   second launch  y[t] = y0[t] + B_l (s_l z[t])
 //
-// A's rows lie like W's (k contiguous), so the adapters that the batch meets
-// are further tiles of 16 weight rows behind W's.  They meet all tokens, which
-// costs nothing beside reading them, and a token takes the columns of its own
-// adapter.  An adapter is read once, however many tokens have it: its tiles
-// are numbered by the first token that has it.  The second launch is one
-// output per lane and token, in fp32, so nothing of one adapter can reach
-// another's tokens.
+// A's rows lie like W's (k contiguous), so they are further columns behind
+// W's.  They meet all tokens, and a token takes the columns of its own adapter.
+// Up to 32 tokens this is the weight stream of rows.h: the adapters that the
+// batch meets are further tiles of 16 weight rows, read once however many
+// tokens have them (their tiles are numbered by the first token that has one),
+// and meeting all tokens costs nothing beside reading them.  Beyond it is a
+// tiled product (proj_gemm.hip) with all adapters' A.  The second launch works
+// on single outputs in fp32, so nothing of one adapter can reach another's
+// tokens.
 #include "proj.h"
 #include "rows_bf16.h"
 
 namespace moelora {
 
 namespace {
+
+// products of tokens, outputs and rank in the second launch (see proj_few)
+constexpr int64_t kProjFew = 1 << 25;
 
 // The batch's adapters, a lane a token: id of the lane's token (-1: none), and
 // a bit for the first token of each adapter.
@@ -67,58 +72,91 @@ struct ProjWeights : Bf16Stream {
 struct JoinArgs {
   ProjArgs p;
   const uint16_t* B;
-  const float* slabs;  // [splits][T][cols]: W's columns, then each met adapter's
+  const float* slabs;  // [splits][T][cols]: W's columns, then adapters'
   int splits, cols, first, per;  // first: of the adapters' columns, per: of one adapter
   float* z;
   uint16_t* y;
 };
 
-// Grid: 512 outputs, two a thread; tokens.
+// y and z from the first launch's sums.  Grid: 256 OUT outputs; tokens.  PER: r
+// / 8 at most.  MET: the adapters' columns are those met by at most 64 tokens,
+// else all adapters'.  B's rows are asked for before z is there.
+template <int PER, bool MET>
 __global__ __launch_bounds__(256) void proj_rows_join_kernel(JoinArgs a) {
+  constexpr int OUT = PER >= 8 ? 1 : 2;
   __shared__ float zs[128];
   const ProjArgs& p = a.p;
   const int t = blockIdx.y, tid = threadIdx.x, r = p.r;
-  const Met met(p.ids, p.T, p.L, tid & 63);
-  const int l = __builtin_amdgcn_readlane(met.id, t);
+  int l, place;
+  if constexpr (MET) {
+    // an adapter's place among those met is that of the first token that has it
+    const Met met(p.ids, p.T, p.L, tid & 63);
+    l = __builtin_amdgcn_readlane(met.id, t);
+    const int owner = __builtin_ctzll(__ballot(met.id == l));
+    place = __popcll(met.first & ((1ull << owner) - 1));
+  } else {
+    l = p.ids[t];
+    if (l >= p.L) l = -1;
+    place = l;
+  }
+  const int n = ((int)blockIdx.x * 256 + tid) * OUT;
+  u32x4_t b[OUT][PER];
+  if (l >= 0 && n < p.N) {
+#pragma unroll
+    for (int h = 0; h < OUT; ++h)
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (j * 8 < r) b[h][j] = ld16(a.B + ((int64_t)l * p.N + n + h) * r + j * 8);
+  }
   const float* mine = a.slabs + (int64_t)t * a.cols;
   const int64_t slab = (int64_t)p.T * a.cols;
-  // this token's z: its adapter's place among those met is that of the first
-  // token that has it
-  const int owner = __builtin_ctzll(__ballot(met.id == l));
-  const int place = __popcll(met.first & ((1ull << owner) - 1));
+  float v[OUT];
+#pragma unroll
+  for (int h = 0; h < OUT; ++h) v[h] = 0.f;
+  if (n < p.N) {
+    for (int s = 0; s < a.splits; ++s)
+#pragma unroll
+      for (int h = 0; h < OUT; ++h) v[h] += mine[s * slab + n + h];
+  }
   if (tid < r) {
-    float v = 0.f;
+    float d = 0.f;
     if (l >= 0)
-      for (int s = 0; s < a.splits; ++s) v += mine[s * slab + a.first + place * a.per + tid];
-    if (a.z && blockIdx.x == 0) a.z[(int64_t)t * r + tid] = v;
-    if (l >= 0) zs[tid] = proj_scale(p, l) * v;
+      for (int s = 0; s < a.splits; ++s) d += mine[s * slab + a.first + place * a.per + tid];
+    if (a.z && blockIdx.x == 0) a.z[(int64_t)t * r + tid] = d;
+    if (l >= 0) zs[tid] = proj_scale(p, l) * d;
   }
   __syncthreads();
-  const int n = ((int)blockIdx.x * 256 + tid) * 2;
   if (n >= p.N) return;
-  float v[2] = {0.f, 0.f};
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 q = *reinterpret_cast<const float2*>(mine + s * slab + n);
-    v[0] += q.x;
-    v[1] += q.y;
-  }
   if (l >= 0) {
-    const uint16_t* b = a.B + ((int64_t)l * p.N + n) * r;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < OUT; ++h) {
       float d = 0.f;
-      for (int j = 0; j < r; j += 8) {
-        const u32x4_t q = ld16(b + h * r + j);
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        if (j * 8 >= r) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          d = fmaf(zs[j + 2 * i], bf16_lo(q[i]), d);
-          d = fmaf(zs[j + 2 * i + 1], bf16_hi(q[i]), d);
+          d = fmaf(zs[j * 8 + 2 * i], bf16_lo(b[h][j][i]), d);
+          d = fmaf(zs[j * 8 + 2 * i + 1], bf16_hi(b[h][j][i]), d);
         }
       }
       v[h] += d;
     }
   }
-  *reinterpret_cast<uint32_t*>(a.y + (int64_t)t * p.N + n) = f32x2_to_bf16(v[0], v[1]);
+  uint16_t* y = a.y + (int64_t)t * p.N + n;
+  if constexpr (OUT == 2) *reinterpret_cast<uint32_t*>(y) = f32x2_to_bf16(v[0], v[1]);
+  else *y = __builtin_bit_cast(uint16_t, (__bf16)v[0]);
+}
+
+template <bool MET>
+void launch_join(const JoinArgs& j, hipStream_t st) {
+  const int r = j.p.r, out = r >= 40 ? 1 : 2;
+  const dim3 grid((j.p.N + 256 * out - 1) / (256 * out), j.p.T);
+  if (r <= 8) proj_rows_join_kernel<1, MET><<<grid, 256, 0, st>>>(j);
+  else if (r <= 16) proj_rows_join_kernel<2, MET><<<grid, 256, 0, st>>>(j);
+  else if (r <= 32) proj_rows_join_kernel<4, MET><<<grid, 256, 0, st>>>(j);
+  else if (r <= 64) proj_rows_join_kernel<8, MET><<<grid, 256, 0, st>>>(j);
+  else proj_rows_join_kernel<16, MET><<<grid, 256, 0, st>>>(j);
 }
 
 struct Columns {
@@ -128,14 +166,25 @@ struct Columns {
 
 }  // namespace
 
-size_t proj_rows_slab_bytes(int T, int K, int N, int L, int r) {
-  const Columns c(T, N, L, r);
-  const RowsPlan f = rows_plan(T, c.all * 16, K, Bf16Stream::LINES);
-  return (size_t)f.splits * T * c.all * 16 * sizeof(float);
+bool proj_few(int T, int N, int L, int r) {
+  return T <= kProjRows || (T <= 4096 && (int64_t)T * N * r <= kProjFew && 2 * (int64_t)L * r <= N);
+}
+
+size_t proj_rows_slab_bytes(const ProjArgs& p) {
+  if (p.T > kProjRows) return (size_t)proj_both_splits(p) * p.T * (p.N + p.L * p.r) * sizeof(float);
+  const Columns c(p.T, p.N, p.L, p.r);
+  const RowsPlan f = rows_plan(p.T, c.all * 16, p.K, Bf16Stream::LINES);
+  return (size_t)f.splits * p.T * c.all * 16 * sizeof(float);
 }
 
 int launch_proj_rows(const ProjArgs& p, const uint16_t* x, const uint16_t* W, const uint16_t* A, const uint16_t* B,
                      float* z, float* slabs, uint16_t* y, hipStream_t st) {
+  if (p.T > kProjRows) {
+    const int rc = launch_proj_both(p, x, W, A, slabs, st);
+    if (rc) return rc;
+    launch_join<false>(JoinArgs{p, B, slabs, proj_both_splits(p), p.N + p.L * p.r, p.N, p.r, z, y}, st);
+    return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
+  }
   const Columns c(p.T, p.N, p.L, p.r);
   const RowsPlan f = rows_plan(p.T, c.all * 16, p.K, Bf16Stream::LINES);
   RowsArgs a = {};
@@ -149,8 +198,7 @@ int launch_proj_rows(const ProjArgs& p, const uint16_t* x, const uint16_t* W, co
     if (p.T <= 16) rows_shared_kernel<ProjWeights, 1, false, false><<<grid, 512, 0, st>>>(a, w);
     else rows_shared_kernel<ProjWeights, 2, false, false><<<grid, 512, 0, st>>>(a, w);
   }
-  const JoinArgs j{p, B, slabs, f.splits, c.all * 16, c.base * 16, c.per * 16, z, y};
-  proj_rows_join_kernel<<<dim3((p.N + 511) / 512, p.T), 256, 0, st>>>(j);
+  launch_join<true>(JoinArgs{p, B, slabs, f.splits, c.all * 16, c.base * 16, c.per * 16, z, y}, st);
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 

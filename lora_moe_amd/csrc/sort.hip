@@ -64,19 +64,25 @@ __global__ __launch_bounds__(kThreads) void sort_count_kernel(SortArgs p) {
   for (int e = threadIdx.x; e < p.E; e += kThreads) p.table[(int64_t)e * p.chunks + blockIdx.x] = hist[e];
 }
 
-// one wavefront per expert: its counts to exclusive prefixes, and their total
+// one workgroup per expert: its counts to exclusive prefixes, and their total
+// (at most kChunks of them, kChunks / kThreads neighbouring ones a thread)
 __global__ __launch_bounds__(kThreads) void sort_scan_kernel(SortArgs p) {
-  const int lane = threadIdx.x & 63, e = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
-  if (e >= p.E) return;
+  constexpr int PER = kChunks / kThreads;
+  __shared__ int scan[16];
+  const int e = blockIdx.x, c0 = threadIdx.x * PER;
   int32_t* row = p.table + (int64_t)e * p.chunks;
-  int carry = 0;
-  for (int c0 = 0; c0 < p.chunks; c0 += 64) {
-    const int c = c0 + lane, v = c < p.chunks ? row[c] : 0;
-    const int s = wave_inclusive_scan(v);
-    if (c < p.chunks) row[c] = carry + s - v;
-    carry += __shfl(s, 63, 64);
+  int v[PER], mine = 0, all;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) v[i] = c0 + i < p.chunks ? row[c0 + i] : 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) mine += v[i];
+  int at = block_exclusive_scan<true>(mine, scan, &all);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (c0 + i < p.chunks) row[c0 + i] = at;
+    at += v[i];
   }
-  if (lane == 0) p.totals[e] = carry;
+  if (threadIdx.x == 0) p.totals[e] = all;
 }
 
 // The rows of the workgroup's tokens: pieces are loaded once, kAhead of them
@@ -190,18 +196,18 @@ __global__ __launch_bounds__(kThreads) void unsort_kernel(BackArgs p) {
     for (int j = 0; j < STEP; ++j) {
       const bool has = j0 + j < k;
       r[j] = has ? row_of(p, (int64_t)t * k + j0 + j) : -1;
-      w[j] = has && p.w ? p.w[(int64_t)t * k + j0 + j] : 1.f;
+      w[j] = r[j] >= 0 && p.w ? p.w[(int64_t)t * k + j0 + j] : 1.f;
     }
+    // a dropped pair loads row 0 and adds zeros: without branches the loads go
+    // out together (and in 32 bits 8 pairs take 46 registers, not 238)
 #pragma unroll
-    for (int j = 0; j < STEP; ++j)
-      if (r[j] >= 0) q[j] = __builtin_nontemporal_load(p.rows + (int64_t)r[j] * p.pieces + c);
+    for (int j = 0; j < STEP; ++j) q[j] = __builtin_nontemporal_load(p.rows + (int64_t)max(r[j], 0) * p.pieces + c);
 #pragma unroll
     for (int j = 0; j < STEP; ++j) {
-      if (r[j] < 0) continue;
       float v[X::N];
       X::load(q[j], v);
 #pragma unroll
-      for (int n = 0; n < X::N; ++n) s[n] = fmaf(w[j], v[n], s[n]);
+      for (int n = 0; n < X::N; ++n) s[n] = fmaf(w[j], r[j] >= 0 ? v[n] : 0.f, s[n]);
     }
   }
   p.out[i] = X::store(s);
@@ -235,7 +241,7 @@ __global__ __launch_bounds__(kThreads) void unsort_backward_kernel(BackArgs p) {
         if (p.dw) {
 #pragma unroll
           for (int j = 0; j < STEP; ++j)
-            if (r[j] >= 0) q[j] = __builtin_nontemporal_load(p.rows + (int64_t)r[j] * p.pieces + c);
+            q[j] = __builtin_nontemporal_load(p.rows + (int64_t)max(r[j], 0) * p.pieces + c);
         }
         float y[X::N], v[X::N];
         X::load(qy, y);
@@ -448,7 +454,7 @@ int moe_lora_sort(const moe_lora_sort_shape* shape, const int32_t* topk_ids, con
     return launched() ? MOE_LORA_OK : MOE_LORA_EHIP;
   }
   sort_count_kernel<<<r.chunks, kThreads, a.E * 4, st>>>(a);
-  sort_scan_kernel<<<(a.E + 3) / 4, kThreads, 0, st>>>(a);
+  sort_scan_kernel<<<a.E, kThreads, 0, st>>>(a);
   sort_place_kernel<true><<<r.chunks, kThreads, lds, st>>>(a);
   return launched() ? MOE_LORA_OK : MOE_LORA_EHIP;
 }

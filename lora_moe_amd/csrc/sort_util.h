@@ -9,16 +9,6 @@ namespace moelora {
 
 constexpr int kSortKeys = 4096;  // keys at most: their tables lie in LDS
 
-__device__ __forceinline__ int wave_inclusive_scan(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int y = __shfl_up(v, o, 64);
-    if (lane >= o) v += y;
-  }
-  return v;
-}
-
 // The place of each thread's key (>= 0) in its run: run[key] (LDS) is the next
 // free place and moves on.  The wavefronts take turns, and inside one the
 // lanes of a key follow each other, so places are in thread order.  wkeys:

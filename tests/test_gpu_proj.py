@@ -36,7 +36,9 @@ CASES = [  # T, K, N, L, r, ids, scales
     (130, 256, 512, 4, 8, "runs", True), (201, 2880, 640, 32, 16, "each", True), (257, 72, 2880, 7, 128, "mixed", True),
     (300, 264, 264, 300, 24, "each", True), (513, 512, 136, 9, 72, "runs", True), (700, 200, 1032, 2, 40, "none", True),
     (1030, 520, 392, 5, 64, "mixed", False), (1100, 136, 264, 3, 32, "one", True), (2100, 264, 640, 16, 16, "runs", True),
-    (4500, 136, 264, 6, 16, "runs", True), (4200, 264, 136, 4, 96, "mixed", True)]
+    (4500, 136, 264, 6, 16, "runs", True), (4200, 264, 136, 4, 96, "mixed", True),
+    (201, 264, 200, 32, 16, "each", True), (90, 1000, 520, 40, 128, "mixed", True), (33, 136, 2880, 500, 8, "each", True),
+    (1300, 264, 4104, 9, 72, "each", True), (600, 2880, 2880, 16, 32, "runs", True)]
 
 
 @pytest.mark.parametrize("T,K,N,L,r,ids,scales", CASES)
@@ -107,12 +109,12 @@ def test_whole_numbers_and_differences():
             assert loss(**moved) - base == float((out[n].cpu().double() * e.double()).sum()), (n, k)
 
 
-@pytest.mark.parametrize("T", [7, 20, 90, 600])
+@pytest.mark.parametrize("T,L", [(7, 4), (20, 4), (90, 4), (600, 4), (90, 10), (600, 10), (1500, 30)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
-def test_a_broken_adapter_stays_with_its_tokens(T, bad):
+def test_a_broken_adapter_stays_with_its_tokens(T, L, bad):
     """Weights that are not finite reach the rows of their own adapter, by the
     formula, and no others."""
-    K, N, L, r = 136, 264, 4, 16
+    K, N, r = 136, 264, 16
     x, W, A, B, dy, i, _ = inputs(T, K, N, L, r, 5, "each", False)
     shape = lm.make_proj_shape(T, K, N, L, r)
     ws = lm.alloc_proj_workspace(shape)
@@ -145,7 +147,7 @@ def test_a_broken_adapter_stays_with_its_tokens(T, bad):
     inner = torch.ones(K, dtype=torch.bool)
     inner[9] = False
     assert torch.equal(dx[of(1)][:, inner], want[1][of(1)][:, inner])
-    for l in (0, 3):
+    for l in (0, 3, L - 1):
         assert torch.equal(dA[l], want[2][l]) and torch.equal(dB[l], want[3][l])
 
 
