@@ -814,52 +814,55 @@ def moe_lora_clip_grads(grads, max_norm: float, norm, stream=None) -> None:
 # ------------------------------------------------------------------ tokens to their experts and back
 
 _ROW_TYPES = {MOE_LORA_F32: "float32", MOE_LORA_BF16: "bfloat16", MOE_LORA_F16: "float16"}
-_types = {}  # torch's types by name
+_addresses = {}  # of the library's functions
+_native = None   # the _operands module
 
 
-def _operands(specs, workspace=None):
-    """The device of (name, tensor, shape, dtype) that all match, are contiguous
-    and lie on the current HIP device; raises ValueError otherwise.  workspace:
-    (tensor, bytes needed as a function, what allocates it).  What is right
-    passes in one look at each tensor (a small call's time is mostly its
-    checks'; the workspace's size is looked at by the library); what is not is
-    named by the checks of the other calls."""
-    if not _types:
+def _run(func, shape, args, stream, workspace=None) -> None:
+    """Calls the library's ``func`` on the shape, args and the stream; raises
+    what is wrong.  args: None, or (name, tensor, sizes, type) for a tensor that
+    has to match, be contiguous and lie on the current HIP device; the
+    workspace has sizes None and a None behind it for its bytes.  workspace:
+    (the bytes needed, as a function; what allocates it)."""
+    global _native
+    if _native is None:
         import torch
-        _types.update({n: getattr(torch, n) for n in ("bfloat16", "float16", "float32", "int32", "uint8")},
-                      device=torch._C._cuda_getDevice)
-    dev = None
-    for _, t, shape, dtype in specs:
-        if t is None or t.dtype is not _types[dtype] or t.shape != shape or not t.is_contiguous():
-            break
-        if t.get_device() != dev:
-            if dev is not None or not t.is_cuda:
-                break
-            dev = t.get_device()
-    else:
-        w = None if workspace is None else workspace[0]
-        if ((workspace is None or w is not None and w.dtype is _types["uint8"] and w.dim() == 1
-                and w.is_contiguous() and w.get_device() == dev) and dev == _types["device"]()):
-            return dev
-    if workspace is not None:
-        specs = [*specs, _check_workspace(workspace[0], workspace[1](), workspace[2])]
-    _check_tensors(specs)
-    return specs[0][1].device.index
+        try:
+            from . import _operands
+        except ImportError as e:
+            raise RuntimeError(f"lora_moe_amd._operands: {e}; build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        _native = (_operands.call, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    call, device, raw_stream = _native
+    f = _addresses.get(func)
+    if f is None:
+        f = _addresses[func] = ctypes.cast(getattr(load_library(), func), ctypes.c_void_p).value
+    first = args[0][1]
+    code = None
+    if first is not None and first.is_cuda:
+        dev = device()
+        handle = raw_stream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
+        code = call(f, shape, (*args, handle), dev)
+    if code is None:
+        specs = [a for a in args if a is not None and a[2] is not None]
+        for a in args:
+            if a is not None and a[2] is None:
+                specs.append(_check_workspace(a[1], workspace[0](), workspace[1]))
+        _check_tensors(specs)
+        # as it should be after all (a tensor that DLPack does not take)
+        ptrs = [None if a is None else a[1].data_ptr() for a in args]
+        for i, a in enumerate(args):
+            if a is not None and a[2] is None:
+                ptrs[i + 1] = a[1].numel()
+        code = getattr(load_library(), func)(ctypes.byref(shape), *ptrs, _stream(stream))
+    if code != MOE_LORA_OK:
+        if code == MOE_LORA_EWORKSPACE:
+            _check_workspace(next(a[1] for a in args if a is not None and a[2] is None), workspace[0](), workspace[1])
+        _check(func, code)
 
 
-def _done(func, code, workspace=None):
-    if code == MOE_LORA_OK:
-        return
-    if code == MOE_LORA_EWORKSPACE and workspace is not None:
-        _check_workspace(workspace[0], workspace[1](), workspace[2])
-    _check(func, code)
-
-
-def _handle(stream, dev):
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return getattr(stream, "cuda_stream", stream)
+def _or_none(name, tensor, sizes, dtype):
+    return None if tensor is None else (name, tensor, sizes, dtype)
 
 
 def make_sort_shape(T, H, E, topk, dtype="bfloat16") -> moe_lora_sort_shape:
@@ -899,41 +902,30 @@ def moe_lora_sort(shape, topk_ids, x, workspace, rows, expert_off, row_of_pair, 
     alone).  expert_off [E+1], row_of_pair [T, k] and pair_of_row [T k] are
     int32 and written."""
     T, k, dtype = shape.T, shape.topk, _row_type(shape)
-    specs = [("topk_ids", topk_ids, (T, k), "int32"), ("expert_off", expert_off, (shape.E + 1,), "int32"),
-             ("row_of_pair", row_of_pair, (T, k), "int32")]
-    if x is not None or rows is not None:
-        H = shape.H
-        specs += [("x", x, (T, H), dtype), ("rows", rows, (T * k, H), dtype)]
-    if pair_of_row is not None:
-        specs.append(("pair_of_row", pair_of_row, (T * k,), "int32"))
-    ws = (workspace, lambda: moe_lora_sort_workspace_bytes(shape), "alloc_sort_workspace")
-    dev = _operands(specs, ws)
-    _done("moe_lora_sort", load_library().moe_lora_sort(
-        ctypes.byref(shape), topk_ids.data_ptr(), None if x is None else x.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), None if rows is None else rows.data_ptr(), expert_off.data_ptr(), row_of_pair.data_ptr(),
-        None if pair_of_row is None else pair_of_row.data_ptr(), _handle(stream, dev)), ws)
+    both = x is not None or rows is not None
+    _run("moe_lora_sort", shape, (
+        ("topk_ids", topk_ids, (T, k), "int32"), ("x", x, (T, shape.H), dtype) if both else None,
+        ("workspace", workspace, None, "uint8"), None, ("rows", rows, (T * k, shape.H), dtype) if both else None,
+        ("expert_off", expert_off, (shape.E + 1,), "int32"), ("row_of_pair", row_of_pair, (T, k), "int32"),
+        _or_none("pair_of_row", pair_of_row, (T * k,), "int32")), stream,
+        (lambda: moe_lora_sort_workspace_bytes(shape), "alloc_sort_workspace"))
 
 
 def moe_lora_sort_backward(shape, drows, row_of_pair, dx, stream=None) -> None:
     """dx [T, H]: each token's sum of its pairs' rows of drows [T k, H]."""
     T, H, k, dtype = shape.T, shape.H, shape.topk, _row_type(shape)
-    dev = _operands((("drows", drows, (T * k, H), dtype), ("row_of_pair", row_of_pair, (T, k), "int32"),
-                     ("dx", dx, (T, H), dtype)))
-    _done("moe_lora_sort_backward", load_library().moe_lora_sort_backward(
-        ctypes.byref(shape), drows.data_ptr(), row_of_pair.data_ptr(), dx.data_ptr(), _handle(stream, dev)))
+    _run("moe_lora_sort_backward", shape, (
+        ("drows", drows, (T * k, H), dtype), ("row_of_pair", row_of_pair, (T, k), "int32"),
+        ("dx", dx, (T, H), dtype)), stream)
 
 
 def moe_lora_unsort(shape, rows, row_of_pair, y, weights=None, stream=None) -> None:
     """y [T, H]: each token's sum of its pairs' rows [T k, H], times weights
     [T, k] (fp32; None: ones)."""
     T, H, k, dtype = shape.T, shape.H, shape.topk, _row_type(shape)
-    specs = [("rows", rows, (T * k, H), dtype), ("row_of_pair", row_of_pair, (T, k), "int32"), ("y", y, (T, H), dtype)]
-    if weights is not None:
-        specs.append(("weights", weights, (T, k), "float32"))
-    dev = _operands(specs)
-    _done("moe_lora_unsort", load_library().moe_lora_unsort(
-        ctypes.byref(shape), rows.data_ptr(), row_of_pair.data_ptr(),
-        None if weights is None else weights.data_ptr(), y.data_ptr(), _handle(stream, dev)))
+    _run("moe_lora_unsort", shape, (
+        ("rows", rows, (T * k, H), dtype), ("row_of_pair", row_of_pair, (T, k), "int32"),
+        _or_none("weights", weights, (T, k), "float32"), ("y", y, (T, H), dtype)), stream)
 
 
 def moe_lora_unsort_backward(shape, dy, rows, row_of_pair, drows=None, weights=None, dweights=None,
@@ -942,25 +934,19 @@ def moe_lora_unsort_backward(shape, dy, rows, row_of_pair, drows=None, weights=N
     H] and dweights [T, k] (fp32) that are given; rows (as given to the
     forward) are needed for dweights alone."""
     T, H, k, dtype = shape.T, shape.H, shape.topk, _row_type(shape)
-    specs = [("dy", dy, (T, H), dtype), ("row_of_pair", row_of_pair, (T, k), "int32")]
-    opt = (("rows", rows, (T * k, H), dtype), ("weights", weights, (T, k), "float32"),
-           ("drows", drows, (T * k, H), dtype), ("dweights", dweights, (T, k), "float32"))
-    specs += [s for s in opt if s[1] is not None]
-    dev = _operands(specs)
-    p = [None if s[1] is None else s[1].data_ptr() for s in opt]
-    _done("moe_lora_unsort_backward", load_library().moe_lora_unsort_backward(
-        ctypes.byref(shape), dy.data_ptr(), p[0], row_of_pair.data_ptr(), p[1], p[2], p[3], _handle(stream, dev)))
+    _run("moe_lora_unsort_backward", shape, (
+        ("dy", dy, (T, H), dtype), _or_none("rows", rows, (T * k, H), dtype),
+        ("row_of_pair", row_of_pair, (T, k), "int32"), _or_none("weights", weights, (T, k), "float32"),
+        _or_none("drows", drows, (T * k, H), dtype), _or_none("dweights", dweights, (T, k), "float32")), stream)
 
 
 def moe_lora_route_backward(shape, topk_ids, topk_weights, dweights, dlogits, stream=None) -> None:
     """The gradient of moe_lora_route's weights: dlogits [T, E] from dweights
     [T, k] (both fp32) and what the router wrote."""
     T, k = shape.T, shape.topk
-    dev = _operands((("topk_ids", topk_ids, (T, k), "int32"), ("topk_weights", topk_weights, (T, k), "float32"),
-                     ("dweights", dweights, (T, k), "float32"), ("dlogits", dlogits, (T, shape.E), "float32")))
-    _done("moe_lora_route_backward", load_library().moe_lora_route_backward(
-        ctypes.byref(shape), topk_ids.data_ptr(), topk_weights.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(),
-        _handle(stream, dev)))
+    _run("moe_lora_route_backward", shape, (
+        ("topk_ids", topk_ids, (T, k), "int32"), ("topk_weights", topk_weights, (T, k), "float32"),
+        ("dweights", dweights, (T, k), "float32"), ("dlogits", dlogits, (T, shape.E), "float32")), stream)
 
 
 # ------------------------------------------------------------------ a shared projection with adapters
@@ -990,18 +976,12 @@ def moe_lora_proj_forward(shape, x, lora_ids, W, A, B, workspace, y, z=None, sca
     lora_ids[t] (-1: none), s_l = lora_scale * scales[l]; with z ([T, r] fp32)
     x A_l^T is kept there for moe_lora_proj_backward."""
     T, K, N, L, r = shape.T, shape.K, shape.N, shape.L, shape.r
-    specs = [("x", x, (T, K), "bfloat16"), ("lora_ids", lora_ids, (T,), "int32"), ("W", W, (N, K), "bfloat16"),
-             ("A", A, (L, r, K), "bfloat16"), ("B", B, (L, N, r), "bfloat16"), ("y", y, (T, N), "bfloat16")]
-    if scales is not None:
-        specs.append(("scales", scales, (L,), "float32"))
-    if z is not None:
-        specs.append(("z", z, (T, r), "float32"))
-    ws = (workspace, lambda: moe_lora_proj_workspace_bytes(shape, False), "alloc_proj_workspace")
-    dev = _operands(specs, ws)
-    _done("moe_lora_proj_forward", load_library().moe_lora_proj_forward(
-        ctypes.byref(shape), x.data_ptr(), lora_ids.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(),
-        None if scales is None else scales.data_ptr(), None if z is None else z.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), y.data_ptr(), _handle(stream, dev)), ws)
+    _run("moe_lora_proj_forward", shape, (
+        ("x", x, (T, K), "bfloat16"), ("lora_ids", lora_ids, (T,), "int32"), ("W", W, (N, K), "bfloat16"),
+        ("A", A, (L, r, K), "bfloat16"), ("B", B, (L, N, r), "bfloat16"), _or_none("scales", scales, (L,), "float32"),
+        _or_none("z", z, (T, r), "float32"), ("workspace", workspace, None, "uint8"), None,
+        ("y", y, (T, N), "bfloat16")), stream,
+        (lambda: moe_lora_proj_workspace_bytes(shape, False), "alloc_proj_workspace"))
 
 
 def moe_lora_proj_backward(shape, dy, x, lora_ids, z, W, A, B, workspace, dx=None, dA=None, dB=None, scales=None,
@@ -1009,19 +989,13 @@ def moe_lora_proj_backward(shape, dy, x, lora_ids, z, W, A, B, workspace, dx=Non
     """Gradients of the projection from dy and the kept z into those of dx, dA
     and dB that are given (overwritten); W is frozen."""
     T, K, N, L, r = shape.T, shape.K, shape.N, shape.L, shape.r
-    specs = [("dy", dy, (T, N), "bfloat16"), ("x", x, (T, K), "bfloat16"), ("lora_ids", lora_ids, (T,), "int32"),
-             ("z", z, (T, r), "float32"), ("W", W, (N, K), "bfloat16"), ("A", A, (L, r, K), "bfloat16"),
-             ("B", B, (L, N, r), "bfloat16")]
-    if scales is not None:
-        specs.append(("scales", scales, (L,), "float32"))
-    outs = (("dx", dx, (T, K), "bfloat16"), ("dA", dA, (L, r, K), "bfloat16"), ("dB", dB, (L, N, r), "bfloat16"))
-    specs += [s for s in outs if s[1] is not None]
-    ws = (workspace, lambda: moe_lora_proj_workspace_bytes(shape, True), "alloc_proj_workspace")
-    dev = _operands(specs, ws)
-    _done("moe_lora_proj_backward", load_library().moe_lora_proj_backward(
-        ctypes.byref(shape), dy.data_ptr(), x.data_ptr(), lora_ids.data_ptr(), z.data_ptr(), W.data_ptr(),
-        A.data_ptr(), B.data_ptr(), None if scales is None else scales.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), *[None if s[1] is None else s[1].data_ptr() for s in outs], _handle(stream, dev)), ws)
+    _run("moe_lora_proj_backward", shape, (
+        ("dy", dy, (T, N), "bfloat16"), ("x", x, (T, K), "bfloat16"), ("lora_ids", lora_ids, (T,), "int32"),
+        ("z", z, (T, r), "float32"), ("W", W, (N, K), "bfloat16"), ("A", A, (L, r, K), "bfloat16"),
+        ("B", B, (L, N, r), "bfloat16"), _or_none("scales", scales, (L,), "float32"),
+        ("workspace", workspace, None, "uint8"), None, _or_none("dx", dx, (T, K), "bfloat16"),
+        _or_none("dA", dA, (L, r, K), "bfloat16"), _or_none("dB", dB, (L, N, r), "bfloat16")), stream,
+        (lambda: moe_lora_proj_workspace_bytes(shape, True), "alloc_proj_workspace"))
 
 
 def lora_projection(x, lora_ids, W, A, B, lora_scale=1.0, scales=None, workspace=None, y=None, stream=None):

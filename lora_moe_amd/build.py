@@ -1,19 +1,23 @@
 """Build the HIP library ``libmoe_lora.so`` for gfx950 with hipcc.
 
 Every ``csrc/*.hip`` file is compiled to an object (in parallel), then linked
-into one shared library next to this file.  Always rebuilds when called.
+into one shared library next to this file; ``csrc/operands.c``, the binding's
+look at its tensors, becomes the extension module ``_operands``.  Always
+rebuilds when called.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 SO = os.path.join(PKG, "libmoe_lora.so")
+OPERANDS = os.path.join(PKG, "_operands.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -38,8 +42,21 @@ def _compile(src: str) -> str:
     return obj
 
 
+def build_operands() -> str:
+    import torch
+    tmp = OPERANDS + ".tmp%d" % os.getpid()
+    r = subprocess.run(["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I",
+                        os.path.join(os.path.dirname(torch.__file__), "include"),
+                        os.path.join(CSRC, "operands.c"), "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for operands.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, OPERANDS)
+    return OPERANDS
+
+
 def build(jobs: int | None = None) -> str:
     os.makedirs(OBJ, exist_ok=True)
+    build_operands()
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs))) as ex:
         objs = list(ex.map(_compile, srcs))

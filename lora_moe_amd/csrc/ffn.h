@@ -74,6 +74,7 @@ int launch_ffn_gemm(const FfnGemm& g, FfnProduct product, hipStream_t st);
 struct TilePlan {
   bool big;
   int splits;
+  double us;  // what the rule expects
 };
 TilePlan tile_plan(int M, int N, int K);
 

@@ -480,7 +480,7 @@ int launch(FfnGemm g, hipStream_t st) {
 
 TilePlan tile_plan(int M, int N, int K) {
   const FfnPlan f = plan(M, N, K, FFN_DOWN);
-  return TilePlan{f.big, f.splits};
+  return TilePlan{f.big, f.splits, f.us};
 }
 
 size_t ffn_gemm_slab_bytes(int M, int N, int K, FfnProduct product, bool pair) {

@@ -38,19 +38,27 @@ struct TileArgs {
   int ncol_w;             // BOTH: column tiles of W, then those of the adapters
 };
 
-template <class C>
-constexpr int tile_lds() { return C::LDS + 3 * C::BM * 4 + 16; }
+// RING: slots of the ring, of which all but one are filled ahead.
+template <class C, int RING>
+constexpr int tile_lds() { return RING * C::STAGE + 3 * C::BM * 4 + 16; }
 
-// infinities and NaN of 8 bf16 to 0; whether there were any
-__device__ __forceinline__ bool only_finite(u32x4_t& v) {
-  bool bad = false;
+// Bits 15 and 31 of the result: whether one of the two bf16 of a word of v is an
+// infinity or NaN (the exponent's ones carry into the sign's place).
+__device__ __forceinline__ uint32_t not_finite_bits(u32x4_t v) {
+  uint32_t b = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b |= (v[i] & 0x7f807f80u) + 0x00800080u;
+  return b;
+}
+
+// such values to 0
+__device__ __forceinline__ u32x4_t only_finite(u32x4_t v) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const bool lo = (v[i] & 0x7f80u) == 0x7f80u, hi = (v[i] & 0x7f800000u) == 0x7f800000u;
-    bad |= lo | hi;
-    v[i] = (lo ? 0u : v[i] & 0xffffu) | (hi ? 0u : v[i] & 0xffff0000u);
+    if ((v[i] & 0x7f80u) == 0x7f80u) v[i] &= 0xffff0000u;
+    if ((v[i] & 0x7f800000u) == 0x7f800000u) v[i] &= 0xffffu;
   }
-  return bad;
+  return v;
 }
 
 // The terms of a row that only_finite took out, for 8 neighbouring outputs.
@@ -76,12 +84,12 @@ __device__ __noinline__ Eight add_not_finite(Eight e, const uint16_t* z, const u
 // BOTH (forward, SPLIT): x [W; A]^T instead, all adapters' A behind W as further
 // columns, tokens in their own order, all of it fp32 into the slabs
 // [splits][T][N + L r].
-template <bool BACK, class C, bool SPLIT, bool BOTH>
-__global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
+template <bool BACK, class C, int RING, bool SPLIT, bool BOTH>
+__global__ __launch_bounds__(C::NT, RING > 2 ? 1 : 2) void proj_tile_kernel(TileArgs a) {
   constexpr bool B_KC = !BACK;
   constexpr int MI = C::MI, NI = C::NI;
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  int* token = reinterpret_cast<int*>(smem + C::LDS);  // [BM] of the tile's rows, -1 past the last
+  int* token = reinterpret_cast<int*>(smem + RING * C::STAGE);  // [BM] of the tile's rows, -1 past the last
   int* share = token + C::BM;                          // [BM] which of the tile's adapters, -1: none
   int* adapter = share + C::BM;                        // [BM] the tile's adapters
   int* not_finite = adapter + C::BM;
@@ -124,9 +132,15 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
   Operand<true, C::BM, C::NCA, false> A;
   Operand<B_KC, C::BN, C::NCB, false> B;
   A.init(a.g.in, 0, K, 0, kfirst, wave, 0);
+  static_assert(C::NCA % 2 == 0 && C::NCB % 2 == 0, "a copy's parity is its index's");
+  int my_share[C::NCA];  // of this lane's rows
+  const uint32_t a_row = (uint32_t)(m0 + wave * C::NCA * 8 + (lane >> 3)) * r2 * 2u;
+  const float inv_r2 = 1.f / (float)r2;
 #pragma unroll
   for (int i = 0; i < C::NCA; ++i) {  // its rows from anywhere
     const int rr = (wave * C::NCA + i) * 8 + (lane >> 3), ch = (lane & 7) ^ ((rr >> 1) & 7);
+    const int run = !BOTH && m0 + rr < T ? p.o.run[m0 + rr] : with;
+    my_share[i] = run < with ? run - run0 : -1;
     A.off[i] = m0 + rr < T ? ((uint32_t)token_of(m0 + rr) * (uint32_t)K + ch * 8u) * 2u : kBufNone;
   }
   const int64_t ldw = BACK ? N : K;
@@ -161,28 +175,39 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
     B.rs = rsrc_of(a.g.weights, 0x7fffffffu);
     A.soff = B.soff = 0;
     const int k0 = (s - base) * BK;
+    // of column kx: its share q and value w (r2 - r.. are the remainders)
+    auto split_k = [&](int kx, int& q, int& w) {
+      q = (int)(((float)kx + 0.5f) * inv_r2);  // exact: kx < 2^16, r2 <= 2^8
+      w = kx - q * r2;
+    };
+    // a lane's 16-byte piece of an even and of an odd copy's rows
+    int q[2], w[2];
 #pragma unroll
-    for (int i = 0; i < C::NCA; ++i) {
-      const int rr = (wave * C::NCA + i) * 8 + (lane >> 3), ch = (lane & 7) ^ ((rr >> 1) & 7);
-      const int kx = k0 + ch * 8, q = kx / r2;
-      A.off[i] = share[rr] == q ? ((uint32_t)(m0 + rr) * r2 + (kx - q * r2)) * 2u : kBufNone;
-    }
+    for (int h = 0; h < 2; ++h) split_k(k0 + ((lane & 7) ^ ((lane >> 4) + 4 * h)) * 8, q[h], w[h]);
 #pragma unroll
-    for (int i = 0; i < C::NCB; ++i) {
-      const int c = wave * C::NCB + i;
-      uint32_t off = kBufNone;
-      if (B_KC) {
-        const int nn = c * 8 + (lane >> 3), ch = (lane & 7) ^ ((nn >> 1) & 7);
-        const int kx = k0 + ch * 8, q = kx / r2, w = kx - q * r2;
-        if (q < shares && n0 + nn < N) off = (((uint32_t)adapter[q] * N + n0 + nn) * r + (w < r ? w : w - r)) * 2u;
-      } else {
-        constexpr int PER = 1024 / (C::BN * 2), LPR = C::BN / 8;
-        const int k = c * PER + lane / LPR, ch = (lane % LPR) ^ (4 * (k & 3));
-        const int kx = k0 + k, q = kx / r2, w = kx - q * r2;
-        if (q < shares && n0 + ch * 8 < N)
-          off = (((uint32_t)adapter[q] * r + (w < r ? w : w - r)) * N + n0 + ch * 8) * 2u;
+    for (int i = 0; i < C::NCA; ++i)
+      A.off[i] = my_share[i] == q[i & 1] ? a_row + (uint32_t)(i * 8 * r2 + w[i & 1]) * 2u : kBufNone;
+    if (B_KC) {
+      uint32_t at_q[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        at_q[h] = kBufNone;
+        if (q[h] < shares) at_q[h] = ((uint32_t)adapter[q[h]] * N * r + (w[h] < r ? w[h] : w[h] - r)) * 2u;
       }
-      B.off[i] = off;
+#pragma unroll
+      for (int i = 0; i < C::NCB; ++i) {
+        const int nn = n0 + (wave * C::NCB + i) * 8 + (lane >> 3);
+        B.off[i] = at_q[i & 1] != kBufNone && nn < N ? at_q[i & 1] + (uint32_t)(nn * r) * 2u : kBufNone;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < C::NCB; ++i) {
+        constexpr int PER = 1024 / (C::BN * 2), LPR = C::BN / 8;
+        const int k = (wave * C::NCB + i) * PER + lane / LPR, n = n0 + ((lane % LPR) ^ (4 * (k & 3))) * 8;
+        int qk, wk;
+        split_k(k0 + k, qk, wk);
+        B.off[i] = qk < shares && n < N ? (((uint32_t)adapter[qk] * r + (wk < r ? wk : wk - r)) * N + n) * 2u : kBufNone;
+      }
     }
   };
 
@@ -205,21 +230,31 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
   };
   constexpr int NM = MI * NI, NF = MI + NI, NC = C::NCA + C::NCB;
   // shared: the stage is one of the shared weights'; MIXED: it need not be
-  auto slice = [&](bool shared, int set, int slot, int kk, auto issue_c, auto mixed_c) __attribute__((always_inline)) {
+  auto slice = [&](bool shared, int set, int slot, int kk, int to_slot, auto issue_c, auto mixed_c) __attribute__((always_inline)) {
     constexpr bool ISSUE = decltype(issue_c)::value;
     if (decltype(mixed_c)::value && !shared) {
+      uint32_t b = 0;
 #pragma unroll
-      for (int j = 0; j < NI; ++j) bad |= only_finite(bf[set][j]);
+      for (int j = 0; j < NI; ++j) b |= not_finite_bits(bf[set][j]);
+      if (__ballot(b & 0x80008000u)) {
+        bad = true;
+#pragma unroll
+        for (int j = 0; j < NI; ++j) bf[set][j] = only_finite(bf[set][j]);
+      }
     }
     for_each<NM>([&](auto n_c) __attribute__((always_inline)) {
       constexpr int n = decltype(n_c)::value, i = n / NI, j = n % NI;
       acc[i][j] = mfma_32x32x16(bf[set][j], af[set][i], acc[i][j]);
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (n < NF) read(slot, kk, set ^ 1, n);
+      constexpr int PER = (NF + NM - 1) / NM;  // all of them, also where there are more than MFMAs
+      for_each<PER>([&](auto f_c) __attribute__((always_inline)) {
+        constexpr int f = n * PER + decltype(f_c)::value;
+        if constexpr (f < NF) read(slot, kk, set ^ 1, f);
+      });
       if constexpr (ISSUE) {
         for_each<(n + 1) * NC / NM - n * NC / NM>([&](auto q_c) __attribute__((always_inline)) {
           constexpr int q = n * NC / NM + decltype(q_c)::value;
-          const uint32_t to = smem_at + (slot ^ 1) * C::STAGE;
+          const uint32_t to = smem_at + to_slot * C::STAGE;
           if constexpr (q < C::NCA) A.template copy<q, false>(to, wave, 0);
           else B.template copy<q - C::NCA, false>(to + C::ABYTES, wave, 0);
         });
@@ -244,11 +279,19 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
     for_each<C::NCB>([&](auto i) { B.template copy<decltype(i)::value, false>(smem_at + C::ABYTES, wave, 0); });
   }
   lds_barrier();
-  at(s0 + 1);
-  for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, false>(smem_at + C::STAGE, wave, 0); });
-  for_each<C::NCB>(
-      [&](auto i) { B.template copy<decltype(i)::value, false>(smem_at + C::STAGE + C::ABYTES, wave, 0); });
-  __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);
+  for_each<RING - 1>([&](auto d_c) __attribute__((always_inline)) {
+    constexpr int d = decltype(d_c)::value + 1;
+    at(s0 + d);
+    const uint32_t to = smem_at + d * C::STAGE;
+    for_each<C::NCA>([&](auto i) { A.template copy<decltype(i)::value, false>(to, wave, 0); });
+    for_each<C::NCB>([&](auto i) { B.template copy<decltype(i)::value, false>(to + C::ABYTES, wave, 0); });
+  });
+  // the next stage's copies have landed, those of the stages after it may be on
+  // their way; own LDS reads are done
+  constexpr int ON = (RING - 2) * NC;
+  static_assert(ON < 64, "six bits count them");
+  constexpr int wait_next = (ON & 15) | (ON >> 4 << 14) | (7 << 4);
+  __builtin_amdgcn_s_waitcnt((((RING - 1) * NC) & 15) | ((RING - 1) * NC >> 4 << 14) | (7 << 4));
   bare_barrier();
 #pragma unroll
   for (int i = 0; i < NF; ++i) read(0, 0, 0, i);
@@ -256,31 +299,31 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
   // shared weights, and one for the stages around their end and behind it (as
   // one loop with its branches 242 us where this takes 218: 8192 tokens, 4096 x
   // 4096, rank 16).
-  auto two = [&](int s, auto mixed_c) __attribute__((always_inline)) {
+  auto round = [&](int s, auto mixed_c) __attribute__((always_inline)) {
     constexpr bool MIXED = decltype(mixed_c)::value;
-    for_each<2>([&](auto h_c) __attribute__((always_inline)) {
-      constexpr int slot = decltype(h_c)::value;
+    for_each<RING>([&](auto h_c) __attribute__((always_inline)) {
+      constexpr int slot = decltype(h_c)::value, next = (slot + 1) % RING;
+      if (MIXED && RING > 2 && s + slot >= nst) return;
       const bool shared = s + slot < base;
-      slice(shared, 0, slot, 1, no(), mixed_c);
-      slice(shared, 1, slot, 2, no(), mixed_c);
+      slice(shared, 0, slot, 1, 0, no(), mixed_c);
+      slice(shared, 1, slot, 2, 0, no(), mixed_c);
       if constexpr (MIXED) {
-        at(s + slot + 2);
+        at(s + slot + RING);
       } else {
-        A.at(s + slot + 2, true);
-        B.at(s + slot + 2, true);
+        A.at(s + slot + RING, true);
+        B.at(s + slot + RING, true);
       }
-      slice(shared, 0, slot, 3, no(), mixed_c);
-      // own copies of the next stage have landed, own reads of this one are done
-      __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);
+      slice(shared, 0, slot, 3, 0, no(), mixed_c);
+      __builtin_amdgcn_s_waitcnt(wait_next);
       bare_barrier();
-      slice(shared, 1, slot ^ 1, 0, yes(), mixed_c);
+      slice(shared, 1, next, 0, slot, yes(), mixed_c);
     });
   };
   int s = s0;
 #pragma unroll 1
-  for (; s + 3 < min(base, nst); s += 2) two(s, no());
+  for (; s + 2 * RING - 1 < min(base, nst); s += RING) round(s, no());
 #pragma unroll 1
-  for (; s < nst; s += 2) two(s, yes());
+  for (; s < nst; s += RING) round(s, yes());
   if (bad) *not_finite = 1;
   __builtin_amdgcn_s_waitcnt(wait_vm0 & wait_lgkm0);  // no copy outlives the loop
   bare_barrier();
@@ -352,8 +395,13 @@ __global__ __launch_bounds__(256) void proj_join_kernel(TileArgs a) {
 
 typedef FfnCfg<256, 256, 2, 4> Big;
 typedef FfnCfg<128, 128, 2, 2> Small;
+// One workgroup per CU, four slots: where tiles are few, a stage is as long as
+// its copies take to come, and three on their way hide that (8 wavefronts; with
+// 4 of them 2 us more).  1001 tokens, 2880 x 2880 (184 tiles): 21 us, 30 with
+// Small.
+typedef FfnCfg<128, 128, 2, 4> Deep;
 
-template <bool BACK, class C, bool SPLIT, bool BOTH = false>
+template <bool BACK, class C, int RING, bool SPLIT, bool BOTH = false>
 int launch_cfg(TileArgs a, hipStream_t st) {
   static std::atomic<uint64_t> attr_done;
   a.ncol_w = (a.out_cols + C::BN - 1) / C::BN;
@@ -362,10 +410,10 @@ int launch_cfg(TileArgs a, hipStream_t st) {
   if (grid * C::NT > 0xffffffff) return MOE_LORA_EUNSUPPORTED;
   a.ncol = (int)ncol;
   a.nrow = (int)nrow;
-  const void* fn = reinterpret_cast<const void*>(&proj_tile_kernel<BACK, C, SPLIT, BOTH>);
-  const int rc = ensure_dynamic_lds(fn, tile_lds<C>(), attr_done);
+  const void* fn = reinterpret_cast<const void*>(&proj_tile_kernel<BACK, C, RING, SPLIT, BOTH>);
+  const int rc = ensure_dynamic_lds(fn, tile_lds<C, RING>(), attr_done);
   if (rc) return rc;
-  proj_tile_kernel<BACK, C, SPLIT, BOTH><<<(unsigned)grid, C::NT, tile_lds<C>(), st>>>(a);
+  proj_tile_kernel<BACK, C, RING, SPLIT, BOTH><<<(unsigned)grid, C::NT, tile_lds<C, RING>(), st>>>(a);
   if (SPLIT && !BOTH) {
     const int64_t n = (int64_t)a.p.T * (a.out_cols / 8);
     proj_join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
@@ -373,17 +421,46 @@ int launch_cfg(TileArgs a, hipStream_t st) {
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
-// (two shares a tile: what a tile of several requests has)
-TilePlan plan_of(const ProjArgs& p, bool back) {
-  return tile_plan(p.T, back ? p.K : p.N, (back ? p.N : p.K) + 4 * p.r);
+// Which tile, and how many K splits: the rule of ffn_gemm.hip, or Deep, up to a
+// workgroup per CU in all (0.45 us a stage; a launch for the join and the
+// slabs' way to memory and back as there).
+struct Plan {
+  bool deep, big;
+  int splits;
+};
+
+Plan plan_of(int T, int N, int K, bool joined_anyway) {
+  const TilePlan f = tile_plan(T, N, K);
+  Plan best{false, f.big, f.splits};
+  double least = f.us - (joined_anyway && f.splits > 1 ? 3.5 : 0.);
+  const int64_t tiles = (int64_t)((T + Deep::BM - 1) / Deep::BM) * ((N + Deep::BN - 1) / Deep::BN);
+  const int stages = (K + BK - 1) / BK;
+  for (int s = 1; s * tiles <= 256 && s <= 16 && s * 3 <= std::max(3, stages); ++s) {
+    const double us = 0.5 + (stages + s - 1) / s * 0.45 +
+                      (s > 1 || joined_anyway ? s * (double)T * N * 8 * 0.16e-6 + (joined_anyway ? 0. : 3.5) : 0.);
+    if (us < least) {
+      least = us;
+      best = Plan{true, false, s};
+    }
+  }
+  return best;
 }
+
+// (two shares a tile: what a tile of several requests has)
+Plan plan_of(const ProjArgs& p, bool back) {
+  return plan_of(p.T, back ? p.K : p.N, (back ? p.N : p.K) + 4 * p.r, false);
+}
+
+Plan plan_both(const ProjArgs& p) { return plan_of(p.T, p.N + p.L * p.r, p.K, true); }
 
 template <bool BACK>
 int launch(TileArgs a, hipStream_t st) {
-  const TilePlan f = plan_of(a.p, BACK);
+  const Plan f = plan_of(a.p, BACK);
   a.g.splits = f.splits;
-  if (f.splits > 1) return launch_cfg<BACK, Small, true>(a, st);
-  return f.big ? launch_cfg<BACK, Big, false>(a, st) : launch_cfg<BACK, Small, false>(a, st);
+  if (f.deep)
+    return f.splits > 1 ? launch_cfg<BACK, Deep, 4, true>(a, st) : launch_cfg<BACK, Deep, 4, false>(a, st);
+  if (f.splits > 1) return launch_cfg<BACK, Small, 2, true>(a, st);
+  return f.big ? launch_cfg<BACK, Big, 2, false>(a, st) : launch_cfg<BACK, Small, 2, false>(a, st);
 }
 
 }  // namespace
@@ -398,15 +475,13 @@ int launch_proj_gemm(const ProjArgs& p, bool back, ProjGemm g, hipStream_t st) {
   return back ? launch<true>(a, st) : launch<false>(a, st);
 }
 
-int proj_both_splits(const ProjArgs& p) {
-  const TilePlan f = tile_plan(p.T, p.N + p.L * p.r, p.K);
-  return f.big ? 1 : f.splits;
-}
+int proj_both_splits(const ProjArgs& p) { return plan_both(p).splits; }
 
 int launch_proj_both(const ProjArgs& p, const uint16_t* x, const uint16_t* W, const uint16_t* A, float* slabs,
                      hipStream_t st) {
-  const ProjGemm g{x, W, nullptr, A, nullptr, slabs, proj_both_splits(p)};
-  return launch_cfg<false, Small, true, true>(TileArgs{p, g, p.K, p.N, 0, 0, 0}, st);
+  const Plan f = plan_both(p);
+  const TileArgs a{p, ProjGemm{x, W, nullptr, A, nullptr, slabs, f.splits}, p.K, p.N, 0, 0, 0};
+  return f.deep ? launch_cfg<false, Deep, 4, true, true>(a, st) : launch_cfg<false, Small, 2, true, true>(a, st);
 }
 
 }  // namespace moelora

@@ -78,19 +78,22 @@ struct JoinArgs {
   uint16_t* y;
 };
 
-// y and z from the first launch's sums.  Grid: 256 OUT outputs; tokens.  PER: r
-// / 8 at most.  MET: the adapters' columns are those met by at most 64 tokens,
-// else all adapters'.  B's rows are asked for before z is there.
-template <int PER, bool MET>
+// y and z from the first launch's sums.  Grid: 256 outputs; tokens.  G lanes
+// (r / 8 of them with 8 ranks each) share an output's row of B and take G
+// outputs in turn, so that a wavefront reads its 64 outputs' rows as whole
+// lines, before z is there (32 tokens, 11008 outputs, rank 32: XX us so, 9.4
+// with a lane an output, whose lines drop out of the L1 cache between their
+// pieces).  MET: the adapters' columns are those met by at most 64 tokens, else
+// all adapters'.
+template <int G, bool MET>
 __global__ __launch_bounds__(256) void proj_rows_join_kernel(JoinArgs a) {
-  constexpr int OUT = PER >= 8 ? 1 : 2;
-  __shared__ float zs[128];
+  __shared__ __attribute__((aligned(16))) float zs[128];
   const ProjArgs& p = a.p;
-  const int t = blockIdx.y, tid = threadIdx.x, r = p.r;
+  const int t = blockIdx.y, tid = threadIdx.x, lane = tid & 63, r = p.r;
   int l, place;
   if constexpr (MET) {
     // an adapter's place among those met is that of the first token that has it
-    const Met met(p.ids, p.T, p.L, tid & 63);
+    const Met met(p.ids, p.T, p.L, lane);
     l = __builtin_amdgcn_readlane(met.id, t);
     const int owner = __builtin_ctzll(__ballot(met.id == l));
     place = __popcll(met.first & ((1ull << owner) - 1));
@@ -99,59 +102,58 @@ __global__ __launch_bounds__(256) void proj_rows_join_kernel(JoinArgs a) {
     if (l >= p.L) l = -1;
     place = l;
   }
-  const int n = ((int)blockIdx.x * 256 + tid) * OUT;
-  u32x4_t b[OUT][PER];
-  if (l >= 0 && n < p.N) {
+  const int n0 = (int)blockIdx.x * 256 + (tid & ~63);  // the wavefront's first output
+  const int part = lane % G, of = lane / G;            // output of + u 64 / G of load u
+  const int n = n0 + part * (64 / G) + of;             // what is left with this lane
+  const bool mine = part * 8 < r;
+  u32x4_t b[G];
+  if (l >= 0) {
 #pragma unroll
-    for (int h = 0; h < OUT; ++h)
-#pragma unroll
-      for (int j = 0; j < PER; ++j)
-        if (j * 8 < r) b[h][j] = ld16(a.B + ((int64_t)l * p.N + n + h) * r + j * 8);
+    for (int u = 0; u < G; ++u) {
+      const int o = n0 + u * (64 / G) + of;
+      b[u] = zero4();
+      if (mine && o < p.N) b[u] = ld16(a.B + ((int64_t)l * p.N + o) * r + part * 8);
+    }
   }
-  const float* mine = a.slabs + (int64_t)t * a.cols;
+  const float* sums = a.slabs + (int64_t)t * a.cols;
   const int64_t slab = (int64_t)p.T * a.cols;
-  float v[OUT];
-#pragma unroll
-  for (int h = 0; h < OUT; ++h) v[h] = 0.f;
-  if (n < p.N) {
-    for (int s = 0; s < a.splits; ++s)
-#pragma unroll
-      for (int h = 0; h < OUT; ++h) v[h] += mine[s * slab + n + h];
-  }
+  float v = 0.f;
+  if (n < p.N)
+    for (int s = 0; s < a.splits; ++s) v += sums[s * slab + n];
   if (tid < r) {
     float d = 0.f;
     if (l >= 0)
-      for (int s = 0; s < a.splits; ++s) d += mine[s * slab + a.first + place * a.per + tid];
+      for (int s = 0; s < a.splits; ++s) d += sums[s * slab + a.first + place * a.per + tid];
     if (a.z && blockIdx.x == 0) a.z[(int64_t)t * r + tid] = d;
-    if (l >= 0) zs[tid] = proj_scale(p, l) * d;
+    zs[tid] = l >= 0 ? proj_scale(p, l) * d : 0.f;
   }
   __syncthreads();
-  if (n >= p.N) return;
   if (l >= 0) {
+    float z[8];
 #pragma unroll
-    for (int h = 0; h < OUT; ++h) {
-      float d = 0.f;
+    for (int i = 0; i < 8; ++i) z[i] = mine ? zs[part * 8 + i] : 0.f;
+    float d = 0.f;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        if (j * 8 >= r) break;
+    for (int u = 0; u < G; ++u) {
+      float e = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          d = fmaf(zs[j * 8 + 2 * i], bf16_lo(b[h][j][i]), d);
-          d = fmaf(zs[j * 8 + 2 * i + 1], bf16_hi(b[h][j][i]), d);
-        }
+      for (int i = 0; i < 4; ++i) {
+        e = fmaf(z[2 * i], bf16_lo(b[u][i]), e);
+        e = fmaf(z[2 * i + 1], bf16_hi(b[u][i]), e);
       }
-      v[h] += d;
+#pragma unroll
+      for (int o = 1; o < G; o <<= 1) e += __shfl_xor(e, o, 64);
+      if (part == u) d = e;
     }
+    v += d;
   }
-  uint16_t* y = a.y + (int64_t)t * p.N + n;
-  if constexpr (OUT == 2) *reinterpret_cast<uint32_t*>(y) = f32x2_to_bf16(v[0], v[1]);
-  else *y = __builtin_bit_cast(uint16_t, (__bf16)v[0]);
+  if (n < p.N) a.y[(int64_t)t * p.N + n] = __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
 template <bool MET>
 void launch_join(const JoinArgs& j, hipStream_t st) {
-  const int r = j.p.r, out = r >= 40 ? 1 : 2;
-  const dim3 grid((j.p.N + 256 * out - 1) / (256 * out), j.p.T);
+  const int r = j.p.r;
+  const dim3 grid((j.p.N + 255) / 256, j.p.T);
   if (r <= 8) proj_rows_join_kernel<1, MET><<<grid, 256, 0, st>>>(j);
   else if (r <= 16) proj_rows_join_kernel<2, MET><<<grid, 256, 0, st>>>(j);
   else if (r <= 32) proj_rows_join_kernel<4, MET><<<grid, 256, 0, st>>>(j);

@@ -75,8 +75,12 @@ __global__ __launch_bounds__(shrink_threads(NB)) void proj_shrink_kernel(ShrinkA
     u32x4_t x[RF][2], w[C::WPL];
   } q[C::D];
   const int chunks = (K + kChunk - 1) / kChunk;
-  auto load = [&](int u, int c) __attribute__((always_inline)) {
-    const int left = c < chunks ? K - c * kChunk : 0;  // of K; behind the last chunk nothing is fetched
+  // Workgroups start at different chunks: rows lie a fixed distance apart, so
+  // in step they would all ask the same memory channels.
+  const int rot = (int)((blockIdx.x * (5u * C::NW)) % (unsigned)chunks);
+  auto load = [&](int u, int i) __attribute__((always_inline)) {
+    const int c = i + rot < chunks ? i + rot : i + rot - chunks;
+    const int left = i < chunks ? K - c * kChunk : 0;  // of K; behind the last chunk nothing is fetched
 #pragma unroll
     for (int f = 0; f < RF; ++f)
 #pragma unroll
