@@ -1,5 +1,5 @@
 // Internal declarations of the shared projection with the adapters of many
-// requests (proj.hip: ABI; proj_rows.hip: few tokens; proj_order.hip,
+// requests (proj.hip: ABI; proj_few.hip: decode batches; proj_order.hip,
 // proj_shrink.hip, proj_gemm.hip, proj_grads.hip: the rest).  Not part of the
 // public ABI.
 //
@@ -16,10 +16,6 @@
 #include "moe_lora.h"
 
 namespace moelora {
-
-// Up to this many tokens a forward streams the weights (proj_rows.hip), and no
-// order is needed.
-constexpr int kProjRows = 32;
 
 // Rows [row, row + n) of one adapter; slab: where a piece of a longer run puts
 // its sums (-1: the run's only piece).
@@ -46,6 +42,11 @@ struct ProjArgs {
   ProjOrder o;
   int shrink_rows, grad_rows;
 };
+
+// Rows of a shrink's piece.
+inline int proj_shrink_rows(int T, int r) { return T <= 4096 || r > 64 ? 16 : 32; }
+// Pieces at most: whole ones, and a short one for each run.
+inline int64_t proj_items(int T, int L, int rows) { return T / rows + (T < L ? T : L); }
 
 // s_l
 __device__ __forceinline__ float proj_scale(const ProjArgs& p, int l) {
@@ -75,6 +76,7 @@ struct ProjGemm {
   uint16_t* out;
   float* slabs;
   int splits;
+  int32_t* place;  // [64] of a token's adapter among those met (launch_proj_both)
 };
 size_t proj_gemm_slab_bytes(const ProjArgs& p, bool back);
 int launch_proj_gemm(const ProjArgs& p, bool back, ProjGemm g, hipStream_t st);
@@ -93,21 +95,20 @@ int proj_grad_rows(int T, int K, int N, int r);
 size_t proj_grad_slab_bytes(int T, int K, int N, int r);
 int launch_proj_grads(const ProjArgs& p, const ProjGrads& g, hipStream_t st);
 
-// x [W; A]^T for all adapters, fp32, into slabs [proj_both_splits][T][N + L r].
+// x [W; A]^T, fp32, into slabs [proj_both_splits][T][N + proj_slots r]: of at most
+// 64 tokens and more adapters those that are met (place: [64], which of them a
+// token's is), else of all adapters.
+int proj_slots(int T, int L);
 int proj_both_splits(const ProjArgs& p);
 int launch_proj_both(const ProjArgs& p, const uint16_t* x, const uint16_t* W, const uint16_t* A, float* slabs,
-                     hipStream_t st);
+                     int32_t* place, hipStream_t st);
 
-// Whether a forward takes the two launches of proj_rows.hip, which need no
-// order: up to kProjRows tokens, and beyond them where the adapters' A are few
-// columns beside W's and the tokens' shares of B are little to read one by one.
+// Whether a forward takes the two launches of proj_few.hip, which need no order:
+// decode batches, and more tokens where the adapters' A are few columns beside
+// W's and the tokens' shares of B are little to read one by one.
 bool proj_few(int T, int N, int L, int r);
-size_t proj_rows_slab_bytes(const ProjArgs& p);
-int launch_proj_rows(const ProjArgs& p, const uint16_t* x, const uint16_t* W, const uint16_t* A, const uint16_t* B,
-                     float* z, float* slabs, uint16_t* y, hipStream_t st);
-
-inline int proj_shrink_rows(int T, int r) { return T <= 4096 || r > 64 ? 16 : 32; }
-// items at most: whole pieces, and one short one for each run
-inline int64_t proj_items(int T, int L, int rows) { return T / rows + (T < L ? T : L); }
+size_t proj_few_slab_bytes(const ProjArgs& p);
+int launch_proj_few(const ProjArgs& p, const uint16_t* x, const uint16_t* W, const uint16_t* A, const uint16_t* B,
+                    float* z, float* scratch, uint16_t* y, hipStream_t st);
 
 }  // namespace moelora

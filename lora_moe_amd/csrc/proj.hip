@@ -82,7 +82,7 @@ struct Forward {
   Forward(ProjArgs& p, void* ws) {
     Parts w(ws);
     if (proj_few(p.T, p.N, p.L, p.r)) {
-      slabs = w.take<float>(proj_rows_slab_bytes(p) / 4);
+      slabs = w.take<float>(proj_few_slab_bytes(p) / 4);
     } else {
       take_order(p, w);
       pairs = w.take<uint16_t>((size_t)p.T * 2 * p.r);
@@ -155,7 +155,7 @@ int moe_lora_proj_forward(const moe_lora_proj_shape* shape, const uint16_t* x, c
   hipStream_t st = (hipStream_t)stream;
   ProjArgs p = args_of(*shape, lora_ids, scales, false);
   const Forward f(p, workspace);
-  if (proj_few(p.T, p.N, p.L, p.r)) return launch_proj_rows(p, x, W, A, B, z, f.slabs, y, st);
+  if (proj_few(p.T, p.N, p.L, p.r)) return launch_proj_few(p, x, W, A, B, z, f.slabs, y, st);
   int r = launch_proj_order(p, z, nullptr, nullptr, st);
   if (!r) r = launch_proj_shrink(p, false, x, A, f.pairs, z, st);
   return r ? r : launch_proj_gemm(p, false, ProjGemm{x, W, f.pairs, B, y, f.slabs, 1}, st);

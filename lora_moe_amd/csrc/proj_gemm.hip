@@ -35,12 +35,12 @@ struct TileArgs {
   ProjGemm g;
   int in_cols, out_cols;  // K and N of a forward
   int ncol, nrow;
-  int ncol_w;             // BOTH: column tiles of W, then those of the adapters
+  int ncol_w, slots;      // BOTH: column tiles of W, then those of so many adapters
 };
 
 // RING: slots of the ring, of which all but one are filled ahead.
 template <class C, int RING>
-constexpr int tile_lds() { return RING * C::STAGE + 3 * C::BM * 4 + 16; }
+constexpr int tile_lds() { return RING * C::STAGE + (2 * C::BM + std::max(C::BM, 64)) * 4 + 16; }
 
 // Bits 15 and 31 of the result: whether one of the two bf16 of a word of v is an
 // infinity or NaN (the exponent's ones carry into the sign's place).
@@ -81,18 +81,19 @@ __device__ __noinline__ Eight add_not_finite(Eight e, const uint16_t* z, const u
   return e;
 }
 
-// BOTH (forward, SPLIT): x [W; A]^T instead, all adapters' A behind W as further
-// columns, tokens in their own order, all of it fp32 into the slabs
-// [splits][T][N + L r].
+// BOTH (forward, SPLIT): x [W; A]^T instead, adapters' A behind W as further
+// columns, tokens in their own order, all of it fp32 into the slabs [splits][T][N
+// + slots r].  With fewer slots than adapters those are the ones that the batch
+// (of at most 64 tokens) meets.
 template <bool BACK, class C, int RING, bool SPLIT, bool BOTH>
-__global__ __launch_bounds__(C::NT, RING > 2 ? 1 : 2) void proj_tile_kernel(TileArgs a) {
+__global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
   constexpr bool B_KC = !BACK;
   constexpr int MI = C::MI, NI = C::NI;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   int* token = reinterpret_cast<int*>(smem + RING * C::STAGE);  // [BM] of the tile's rows, -1 past the last
   int* share = token + C::BM;                          // [BM] which of the tile's adapters, -1: none
-  int* adapter = share + C::BM;                        // [BM] the tile's adapters
-  int* not_finite = adapter + C::BM;
+  int* adapter = share + C::BM;                        // [BM, at least 64] the tile's adapters
+  int* not_finite = adapter + std::max(C::BM, 64);
   const ProjArgs& p = a.p;
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(C::NT, RING > 2 ? 1 : 2) void proj_tile_kernel(Tile
   const int tn = in / gm, tm = panel * GM + in - tn * gm;
   const bool is_w = !BOTH || tn < a.ncol_w;
   const int m0 = tm * C::BM, n0 = (is_w ? tn : tn - a.ncol_w) * C::BN;
-  const int N = is_w ? a.out_cols : p.L * r;
+  const int N = is_w ? a.out_cols : a.slots * r;
   auto token_of = [&](int m) { return BOTH ? m : p.o.perm[m]; };
 
   // Stages: those of the shared weights, then those of the tile's shares;
@@ -132,7 +133,7 @@ __global__ __launch_bounds__(C::NT, RING > 2 ? 1 : 2) void proj_tile_kernel(Tile
   Operand<true, C::BM, C::NCA, false> A;
   Operand<B_KC, C::BN, C::NCB, false> B;
   A.init(a.g.in, 0, K, 0, kfirst, wave, 0);
-  static_assert(C::NCA % 2 == 0 && C::NCB % 2 == 0, "a copy's parity is its index's");
+  static_assert(BOTH || (C::NCA % 2 == 0 && C::NCB % 2 == 0), "a copy's parity is its index's");
   int my_share[C::NCA];  // of this lane's rows
   const uint32_t a_row = (uint32_t)(m0 + wave * C::NCA * 8 + (lane >> 3)) * r2 * 2u;
   const float inv_r2 = 1.f / (float)r2;
@@ -145,7 +146,28 @@ __global__ __launch_bounds__(C::NT, RING > 2 ? 1 : 2) void proj_tile_kernel(Tile
   }
   const int64_t ldw = BACK ? N : K;
   const uint16_t* w = is_w ? a.g.W : a.g.weights;
-  B.init(B_KC ? w + (int64_t)n0 * ldw : w + n0, 0, ldw, N - n0, kfirst, wave, 0);
+  const bool met = BOTH && !is_w && a.slots < p.L;  // columns of the adapters that are met
+  const int64_t first = met ? 0 : B_KC ? n0 * ldw : n0;
+  B.init(w + first, 0, ldw, N - n0, kfirst, wave, 0);
+  if (met) {
+    // a lane a token (64 at most): adapters in the order of their first tokens
+    int id = lane < T ? p.ids[lane] : -1, place = -1, count = 0;
+    if (id >= p.L) id = -1;
+    for (uint64_t left = __ballot(id >= 0); left; ++count) {
+      const int one = __builtin_ctzll(left), l = __builtin_amdgcn_readlane(id, one);
+      if (id == l) place = count;
+      if (lane == one) adapter[count] = l;  // (every wavefront the same)
+      left &= ~__ballot(id == l);
+    }
+    if (tn == a.ncol_w && tm == 0 && split == 0 && wave == 0 && lane < T) a.g.place[lane] = place;
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < C::NCB; ++i) {
+      const int rr = (wave * C::NCB + i) * 8 + (lane >> 3), ch = (lane & 7) ^ ((rr >> 1) & 7);
+      const int q = (n0 + rr) / r, j = n0 + rr - q * r;
+      B.off[i] = q < count ? (((uint32_t)adapter[q] * r + j) * (uint32_t)K + ch * 8u) * 2u : kBufNone;
+    }
+  }
 
   // the tile's rows and adapters
   for (int i = threadIdx.x; i < C::BM; i += C::NT) {
@@ -365,7 +387,7 @@ __global__ __launch_bounds__(C::NT, RING > 2 ? 1 : 2) void proj_tile_kernel(Tile
       }
       const f32x4_t* v = e.v;
       if (SPLIT) {
-        const int cols = BOTH ? a.out_cols + p.L * r : N, c = is_w ? n : a.out_cols + n;
+        const int cols = BOTH ? a.out_cols + a.slots * r : N, c = is_w ? n : a.out_cols + n;
         f32x4_t* dst = reinterpret_cast<f32x4_t*>(a.g.slabs + ((int64_t)split * T + m0 + rr) * cols + c);
         dst[0] = v[0];
         dst[1] = v[1];
@@ -400,12 +422,17 @@ typedef FfnCfg<128, 128, 2, 2> Small;
 // 4 of them 2 us more).  1001 tokens, 2880 x 2880 (184 tiles): 21 us, 30 with
 // Small.
 typedef FfnCfg<128, 128, 2, 4> Deep;
+// Decode batches: small tiles of few wavefronts, several workgroups to a CU, so
+// that nearly all of its LDS is weights on their way (up to 32 tokens three or
+// four slots of 12 KB in three workgroups, beyond it three of 24 KB in two).
+typedef FfnCfg<64, 128, 2, 4> Few64;
+typedef FfnCfg<32, 64, 1, 2> Few32;
 
 template <bool BACK, class C, int RING, bool SPLIT, bool BOTH = false>
 int launch_cfg(TileArgs a, hipStream_t st) {
   static std::atomic<uint64_t> attr_done;
   a.ncol_w = (a.out_cols + C::BN - 1) / C::BN;
-  const int64_t ncol = a.ncol_w + (BOTH ? (a.p.L * a.p.r + C::BN - 1) / C::BN : 0), nrow = (a.p.T + C::BM - 1) / C::BM;
+  const int64_t ncol = a.ncol_w + (BOTH ? (a.slots * a.p.r + C::BN - 1) / C::BN : 0), nrow = (a.p.T + C::BM - 1) / C::BM;
   const int64_t grid = ncol * nrow * a.g.splits;
   if (grid * C::NT > 0xffffffff) return MOE_LORA_EUNSUPPORTED;
   a.ncol = (int)ncol;
@@ -426,6 +453,11 @@ int launch_cfg(TileArgs a, hipStream_t st) {
 // slabs' way to memory and back as there).
 struct Plan {
   bool deep, big;
+  int splits;
+};
+
+struct BothPlan {
+  enum { FEW32, FEW64, DEEP, SMALL } tile;
   int splits;
 };
 
@@ -451,7 +483,32 @@ Plan plan_of(const ProjArgs& p, bool back) {
   return plan_of(p.T, back ? p.K : p.N, (back ? p.N : p.K) + 4 * p.r, false);
 }
 
-Plan plan_both(const ProjArgs& p) { return plan_of(p.T, p.N + p.L * p.r, p.K, true); }
+// x [W; A]^T.  Decode batches: Few32 up to 32 tokens, Few64 up to 256 and 256
+// tiles (201 tokens, 2880 x 2880: 18.5 us, 24 with Deep; 4096 x 11008, 352
+// tiles: 59 and 52), with as many K splits as pay (0.2 us a stage; a split costs
+// its start and its slab), up to about a workgroup per CU.  Measured, us, 16
+// adapters of rank 16 with Few32 and the join, by splits 1, 2, 3, 4, 6: one
+// token, 4096 x 4096, 17.8, 13.0, 12.2, 11.7, 13.0; 11008 outputs 19.1, 20.5,
+// 23.5, 22.0, 25.1.
+BothPlan plan_both(const ProjArgs& p) {
+  const int cols = p.N + proj_slots(p.T, p.L) * p.r, stages = (p.K + BK - 1) / BK;
+  const bool few32 = p.T <= 32;
+  const int64_t tiles = few32 ? (cols + 63) / 64 : (int64_t)((p.T + 63) / 64) * ((cols + 127) / 128);
+  if (!few32 && (p.T > 256 || tiles > 256)) {
+    const Plan f = plan_of(p.T, cols, p.K, true);
+    return BothPlan{f.deep ? BothPlan::DEEP : BothPlan::SMALL, f.splits};
+  }
+  BothPlan best{few32 ? BothPlan::FEW32 : BothPlan::FEW64, 1};
+  double least = 1e9;
+  for (int s = 1; s == 1 || (s * tiles <= (few32 ? 288 : 256) && s <= 16 && 2 * s <= stages); ++s) {
+    const double us = (stages + s - 1) / s * 0.2 + s * (0.35 + 1.5e-6 * p.T * cols);
+    if (us < least) {
+      least = us;
+      best.splits = s;
+    }
+  }
+  return best;
+}
 
 template <bool BACK>
 int launch(TileArgs a, hipStream_t st) {
@@ -471,17 +528,25 @@ size_t proj_gemm_slab_bytes(const ProjArgs& p, bool back) {
 }
 
 int launch_proj_gemm(const ProjArgs& p, bool back, ProjGemm g, hipStream_t st) {
-  const TileArgs a{p, g, back ? p.N : p.K, back ? p.K : p.N, 0, 0, 0};
+  const TileArgs a{p, g, back ? p.N : p.K, back ? p.K : p.N, 0, 0, 0, 0};
   return back ? launch<true>(a, st) : launch<false>(a, st);
 }
+
+int proj_slots(int T, int L) { return T <= 64 && T < L ? T : L; }
 
 int proj_both_splits(const ProjArgs& p) { return plan_both(p).splits; }
 
 int launch_proj_both(const ProjArgs& p, const uint16_t* x, const uint16_t* W, const uint16_t* A, float* slabs,
-                     hipStream_t st) {
-  const Plan f = plan_both(p);
-  const TileArgs a{p, ProjGemm{x, W, nullptr, A, nullptr, slabs, f.splits}, p.K, p.N, 0, 0, 0};
-  return f.deep ? launch_cfg<false, Deep, 4, true, true>(a, st) : launch_cfg<false, Small, 2, true, true>(a, st);
+                     int32_t* place, hipStream_t st) {
+  const BothPlan f = plan_both(p);
+  const ProjGemm g{x, W, nullptr, A, nullptr, slabs, f.splits, place};
+  const TileArgs a{p, g, p.K, p.N, 0, 0, 0, proj_slots(p.T, p.L)};
+  switch (f.tile) {
+    case BothPlan::FEW32: return launch_cfg<false, Few32, 4, true, true>(a, st);
+    case BothPlan::FEW64: return launch_cfg<false, Few64, 3, true, true>(a, st);
+    case BothPlan::DEEP: return launch_cfg<false, Deep, 4, true, true>(a, st);
+    default: return launch_cfg<false, Small, 2, true, true>(a, st);
+  }
 }
 
 }  // namespace moelora

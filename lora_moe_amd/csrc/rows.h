@@ -28,8 +28,7 @@
 // The weights' format is a policy W (ffn_rows.hip, w4.hip): Tile, where a
 // tile lies; Buf, a chunk of it in registers; load(); operand(), the 32-deep
 // step j of a chunk as bf16; Acc, the sums.  W::DEPTH chunks are in flight;
-// a workgroup has up to W::MAX_FRAGMENTS fragments of 16 rows.  W::RAW: all
-// sums go to the slabs as they are, for the caller's own join.
+// a workgroup has up to W::MAX_FRAGMENTS fragments of 16 rows.
 #pragma once
 
 #include <algorithm>
@@ -196,10 +195,7 @@ __global__ __launch_bounds__(512, 2) void rows_direct_kernel(RowsArgs p, typenam
   const int no = tile0 * 16 + l16;
 #pragma unroll
   for (int v = 0; v < 4; ++v)
-    if (kq * 4 + v < p.M && no < p.N) {
-      if constexpr (W::RAW) p.slabs[(int64_t)(kq * 4 + v) * p.N + no] = s[0][v];
-      else rows_store(p, GATE, kq * 4 + v, no, s[0][v], s[CT - 1][v]);
-    }
+    if (kq * 4 + v < p.M && no < p.N) rows_store(p, GATE, kq * 4 + v, no, s[0][v], s[CT - 1][v]);
 }
 
 // RF: fragments of 16 rows.  Grid: groups of up to 8 tiles (an even share
@@ -332,7 +328,7 @@ __global__ __launch_bounds__(512, 2) void rows_shared_kernel(RowsArgs p, typenam
     for (int v = 0; v < 4; ++v) {
       const int m = m0 + f * 16 + kq * 4 + v;
       if (m >= p.M) continue;
-      if (!W::RAW && p.splits == 1) {
+      if (p.splits == 1) {
         rows_store(p, GATE, m, no, acc.sum(f, 0)[v], acc.sum(f, CT - 1)[v]);
       } else {
 #pragma unroll

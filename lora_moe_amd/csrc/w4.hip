@@ -83,7 +83,6 @@ struct PackedWeights {
   };
   static constexpr int GPC = 4 / SPG;  // groups of a chunk
   static constexpr int LINES = 8;
-  static constexpr bool RAW = false;
   static constexpr int MAX_FRAGMENTS = 4;
   // 4 starts later and gains nothing; 1 is up to 9 % faster in some products
   // and 9 to 15 % slower in others.  us with 1, 2 and 4,
