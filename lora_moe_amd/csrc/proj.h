@@ -30,8 +30,8 @@ struct ProjOrder {
   int32_t* adapter;    // [L + 1] adapter of a run; L: the tokens without
   int32_t* count;      // [4] shrink items, gradient items, runs with an adapter
   ProjItem* shrink;    // pieces of at most shrink_rows rows of the runs with an adapter
-  ProjItem* grad;      // pieces of at most grad_rows rows
-  int32_t* slabs;      // [L][2] first slab of an adapter and how many (0: one piece, -1: no tokens)
+  ProjItem* grad;      // pieces of at most grad_rows rows, one at least of every adapter
+  int32_t* slabs;      // [L][2] first slab of an adapter and how many (0: one piece)
 };
 
 struct ProjArgs {
@@ -92,6 +92,7 @@ struct ProjGrads {
   float* slabs;
 };
 int proj_grad_rows(int T, int K, int N, int r);
+inline int64_t proj_grad_items(const ProjArgs& p) { return p.T / p.grad_rows + p.L; }
 size_t proj_grad_slab_bytes(int T, int K, int N, int r);
 int launch_proj_grads(const ProjArgs& p, const ProjGrads& g, hipStream_t st);
 

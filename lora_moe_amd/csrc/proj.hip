@@ -71,7 +71,7 @@ void take_order(ProjArgs& p, Parts& w) {
   p.o.count = w.take<int32_t>(4);
   p.o.shrink = w.take<ProjItem>(proj_items(p.T, p.L, p.shrink_rows));
   if (!p.grad_rows) return;
-  p.o.grad = w.take<ProjItem>(proj_items(p.T, p.L, p.grad_rows));
+  p.o.grad = w.take<ProjItem>(proj_grad_items(p));
   p.o.slabs = w.take<int32_t>(2 * p.L);
 }
 

@@ -133,7 +133,6 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
   Operand<true, C::BM, C::NCA, false> A;
   Operand<B_KC, C::BN, C::NCB, false> B;
   A.init(a.g.in, 0, K, 0, kfirst, wave, 0);
-  static_assert(BOTH || (C::NCA % 2 == 0 && C::NCB % 2 == 0), "a copy's parity is its index's");
   int my_share[C::NCA];  // of this lane's rows
   const uint32_t a_row = (uint32_t)(m0 + wave * C::NCA * 8 + (lane >> 3)) * r2 * 2u;
   const float inv_r2 = 1.f / (float)r2;
@@ -207,8 +206,10 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) split_k(k0 + ((lane & 7) ^ ((lane >> 4) + 4 * h)) * 8, q[h], w[h]);
 #pragma unroll
-    for (int i = 0; i < C::NCA; ++i)
-      A.off[i] = my_share[i] == q[i & 1] ? a_row + (uint32_t)(i * 8 * r2 + w[i & 1]) * 2u : kBufNone;
+    for (int i = 0; i < C::NCA; ++i) {
+      const bool odd = (wave * C::NCA + i) & 1;
+      A.off[i] = my_share[i] == (odd ? q[1] : q[0]) ? a_row + (uint32_t)(i * 8 * r2 + (odd ? w[1] : w[0])) * 2u : kBufNone;
+    }
     if (B_KC) {
       uint32_t at_q[2];
 #pragma unroll
@@ -218,8 +219,9 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < C::NCB; ++i) {
-        const int nn = n0 + (wave * C::NCB + i) * 8 + (lane >> 3);
-        B.off[i] = at_q[i & 1] != kBufNone && nn < N ? at_q[i & 1] + (uint32_t)(nn * r) * 2u : kBufNone;
+        const int c = wave * C::NCB + i, nn = n0 + c * 8 + (lane >> 3);
+        const uint32_t of_q = c & 1 ? at_q[1] : at_q[0];
+        B.off[i] = of_q != kBufNone && nn < N ? of_q + (uint32_t)(nn * r) * 2u : kBufNone;
       }
     } else {
 #pragma unroll
@@ -448,33 +450,34 @@ int launch_cfg(TileArgs a, hipStream_t st) {
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
-// Which tile, and how many K splits: the rule of ffn_gemm.hip, or Deep, up to a
-// workgroup per CU in all (0.45 us a stage; a launch for the join and the
-// slabs' way to memory and back as there).
+// Which tile, and how many K splits: the rule of ffn_gemm.hip, or, up to a
+// workgroup per CU in all, Few64 or Deep (0.33 and 0.45 us a stage; a launch for
+// the join and the slabs' way to memory and back as there).  512 tokens, 2880 x
+// 2880, rank 64 with its order and shrink: 46 us with Few64 (184 tiles), 55 with
+// Deep; 1001 tokens, rank 32 (368 and 184 tiles): 49 and 44.
 struct Plan {
-  bool deep, big;
-  int splits;
-};
-
-struct BothPlan {
-  enum { FEW32, FEW64, DEEP, SMALL } tile;
+  enum Tile { BIG, SMALL, DEEP, FEW64, FEW32 } tile;
   int splits;
 };
 
 Plan plan_of(int T, int N, int K, bool joined_anyway) {
   const TilePlan f = tile_plan(T, N, K);
-  Plan best{false, f.big, f.splits};
+  Plan best{f.big ? Plan::BIG : Plan::SMALL, f.splits};
   double least = f.us - (joined_anyway && f.splits > 1 ? 3.5 : 0.);
-  const int64_t tiles = (int64_t)((T + Deep::BM - 1) / Deep::BM) * ((N + Deep::BN - 1) / Deep::BN);
   const int stages = (K + BK - 1) / BK;
-  for (int s = 1; s * tiles <= 256 && s <= 16 && s * 3 <= std::max(3, stages); ++s) {
-    const double us = 0.5 + (stages + s - 1) / s * 0.45 +
-                      (s > 1 || joined_anyway ? s * (double)T * N * 8 * 0.16e-6 + (joined_anyway ? 0. : 3.5) : 0.);
-    if (us < least) {
-      least = us;
-      best = Plan{true, false, s};
+  auto consider = [&](Plan::Tile tile, int bm, double stage_us) {
+    const int64_t tiles = (int64_t)((T + bm - 1) / bm) * ((N + 127) / 128);
+    for (int s = 1; s * tiles <= 256 && s <= 16 && s * 3 <= std::max(3, stages); ++s) {
+      const double us = 0.5 + (stages + s - 1) / s * stage_us +
+                        (s > 1 || joined_anyway ? s * (double)T * N * 8 * 0.16e-6 + (joined_anyway ? 0. : 3.5) : 0.);
+      if (us < least) {
+        least = us;
+        best = Plan{tile, s};
+      }
     }
-  }
+  };
+  consider(Plan::DEEP, Deep::BM, 0.45);
+  consider(Plan::FEW64, Few64::BM, 0.33);
   return best;
 }
 
@@ -490,15 +493,15 @@ Plan plan_of(const ProjArgs& p, bool back) {
 // adapters of rank 16 with Few32 and the join, by splits 1, 2, 3, 4, 6: one
 // token, 4096 x 4096, 17.8, 13.0, 12.2, 11.7, 13.0; 11008 outputs 19.1, 20.5,
 // 23.5, 22.0, 25.1.
-BothPlan plan_both(const ProjArgs& p) {
+Plan plan_both(const ProjArgs& p) {
   const int cols = p.N + proj_slots(p.T, p.L) * p.r, stages = (p.K + BK - 1) / BK;
   const bool few32 = p.T <= 32;
   const int64_t tiles = few32 ? (cols + 63) / 64 : (int64_t)((p.T + 63) / 64) * ((cols + 127) / 128);
   if (!few32 && (p.T > 256 || tiles > 256)) {
     const Plan f = plan_of(p.T, cols, p.K, true);
-    return BothPlan{f.deep ? BothPlan::DEEP : BothPlan::SMALL, f.splits};
+    return Plan{f.tile == Plan::BIG ? Plan::SMALL : f.tile, f.splits};
   }
-  BothPlan best{few32 ? BothPlan::FEW32 : BothPlan::FEW64, 1};
+  Plan best{few32 ? Plan::FEW32 : Plan::FEW64, 1};
   double least = 1e9;
   for (int s = 1; s == 1 || (s * tiles <= (few32 ? 288 : 256) && s <= 16 && 2 * s <= stages); ++s) {
     const double us = (stages + s - 1) / s * 0.2 + s * (0.35 + 1.5e-6 * p.T * cols);
@@ -514,10 +517,16 @@ template <bool BACK>
 int launch(TileArgs a, hipStream_t st) {
   const Plan f = plan_of(a.p, BACK);
   a.g.splits = f.splits;
-  if (f.deep)
-    return f.splits > 1 ? launch_cfg<BACK, Deep, 4, true>(a, st) : launch_cfg<BACK, Deep, 4, false>(a, st);
-  if (f.splits > 1) return launch_cfg<BACK, Small, 2, true>(a, st);
-  return f.big ? launch_cfg<BACK, Big, 2, false>(a, st) : launch_cfg<BACK, Small, 2, false>(a, st);
+  const bool split = f.splits > 1;
+  switch (f.tile) {
+    case Plan::DEEP:
+      return split ? launch_cfg<BACK, Deep, 4, true>(a, st) : launch_cfg<BACK, Deep, 4, false>(a, st);
+    case Plan::FEW64:
+      return split ? launch_cfg<BACK, Few64, 3, true>(a, st) : launch_cfg<BACK, Few64, 3, false>(a, st);
+    case Plan::BIG: return launch_cfg<BACK, Big, 2, false>(a, st);
+    default:
+      return split ? launch_cfg<BACK, Small, 2, true>(a, st) : launch_cfg<BACK, Small, 2, false>(a, st);
+  }
 }
 
 }  // namespace
@@ -538,13 +547,13 @@ int proj_both_splits(const ProjArgs& p) { return plan_both(p).splits; }
 
 int launch_proj_both(const ProjArgs& p, const uint16_t* x, const uint16_t* W, const uint16_t* A, float* slabs,
                      int32_t* place, hipStream_t st) {
-  const BothPlan f = plan_both(p);
+  const Plan f = plan_both(p);
   const ProjGemm g{x, W, nullptr, A, nullptr, slabs, f.splits, place};
   const TileArgs a{p, g, p.K, p.N, 0, 0, 0, proj_slots(p.T, p.L)};
   switch (f.tile) {
-    case BothPlan::FEW32: return launch_cfg<false, Few32, 4, true, true>(a, st);
-    case BothPlan::FEW64: return launch_cfg<false, Few64, 3, true, true>(a, st);
-    case BothPlan::DEEP: return launch_cfg<false, Deep, 4, true, true>(a, st);
+    case Plan::FEW32: return launch_cfg<false, Few32, 4, true, true>(a, st);
+    case Plan::FEW64: return launch_cfg<false, Few64, 3, true, true>(a, st);
+    case Plan::DEEP: return launch_cfg<false, Deep, 4, true, true>(a, st);
     default: return launch_cfg<false, Small, 2, true, true>(a, st);
   }
 }

@@ -5,9 +5,9 @@
 // and bounds the product.  A workgroup takes 128 of its columns and one piece
 // of a run, 64 rows a stage, gathered on their way into LDS; both sides have
 // their output index contiguous and are transposed on the way to registers
-// (ds_read_b64_tr_b16).  A run of several pieces puts fp32 sums into slabs,
-// which a second kernel adds in their order; it writes the zeros of adapters
-// without tokens too.
+// (ds_read_b64_tr_b16).  An adapter without tokens is an empty piece.  A run of
+// several pieces puts fp32 sums into slabs, which a second kernel adds in their
+// order.
 #include "internal.h"
 #include "proj.h"
 #include "tile.h"
@@ -156,8 +156,7 @@ __global__ __launch_bounds__(NT, NB <= 2 ? 2 : 1) void proj_grads_kernel(GradArg
   }
 }
 
-// Gradients of adapters in several pieces (their slabs added in order) and of
-// adapters without tokens.
+// Gradients of adapters in several pieces: their slabs, added in order.
 __global__ __launch_bounds__(256) void proj_grads_join_kernel(GradArgs a) {
   const ProjArgs& p = a.p;
   const int l = blockIdx.y, first = p.o.slabs[2 * l], n = p.o.slabs[2 * l + 1];
@@ -168,8 +167,6 @@ __global__ __launch_bounds__(256) void proj_grads_join_kernel(GradArgs a) {
     const int64_t size = is_a ? in_a : in_b, at = is_a ? i : i - in_a;
     const float* src = a.g.slabs + (is_a ? 0 : a.slabs * in_a) + first * size + at;
     float v[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = 0.f;
     for (int z = 0; z < n; ++z) {
       const f32x4_t* s = reinterpret_cast<const f32x4_t*>(src + z * size);
 #pragma unroll
@@ -186,7 +183,7 @@ int launch_cfg(const GradArgs& a, hipStream_t st) {
   const int rc = ensure_dynamic_lds(fn, Grad<NB>::LDS, attr_done);
   if (rc) return rc;
   const int tiles = a.tiles_a + (a.g.dB ? (a.p.N + WT - 1) / WT : 0);
-  const dim3 grid(tiles, (unsigned)proj_items(a.p.T, a.p.L, a.p.grad_rows));
+  const dim3 grid(tiles, (unsigned)proj_grad_items(a.p));
   proj_grads_kernel<NB><<<grid, NT, Grad<NB>::LDS, st>>>(a);
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
@@ -211,7 +208,7 @@ int launch_proj_grads(const ProjArgs& p, const ProjGrads& g, hipStream_t st) {
   const GradArgs a{p, g, g.dA ? (p.K + WT - 1) / WT : 0, slabs_of(p.T, p.grad_rows)};
   const int rc = p.r <= 16 ? launch_cfg<1>(a, st) : p.r <= 32 ? launch_cfg<2>(a, st)
                  : p.r <= 64 ? launch_cfg<4>(a, st) : launch_cfg<8>(a, st);
-  if (rc) return rc;
+  if (rc || p.T <= p.grad_rows) return rc;  // no run has several pieces
   const int64_t pieces = ((int64_t)(g.dA ? p.K : 0) + (g.dB ? p.N : 0)) * p.r / 8;
   const dim3 grid((unsigned)std::min<int64_t>(64, (pieces + 255) / 256), p.L);
   proj_grads_join_kernel<<<grid, 256, 0, st>>>(a);

@@ -114,8 +114,11 @@ __global__ __launch_bounds__(kThreads) void proj_order_kernel(ProjArgs p, float*
                             [&](int e, int at) { shrink[e] = at; });
     if (counts) o.count[0] = n;
   } else if (wave == 3 && p.grad_rows) {
-    const int n = scan_keys(p.L, [&](int e) { return pieces(total[e], p.grad_rows); },
-                            [&](int e, int at) { grad[e] = at; });
+    // an adapter without tokens has an empty piece, whose gradients are zeros
+    const int n = scan_keys(p.L, [&](int e) { return max(1, pieces(total[e], p.grad_rows)); }, [&](int e, int at) {
+      grad[e] = at;
+      if (writes && !total[e]) o.grad[at] = ProjItem{e, 0, 0, -1};
+    });
     if (counts) o.count[1] = n;
   } else if (wave == 4 && p.grad_rows) {
     auto slabs_of = [&](int e) { return total[e] > p.grad_rows ? pieces(total[e], p.grad_rows) : 0; };
@@ -123,7 +126,7 @@ __global__ __launch_bounds__(kThreads) void proj_order_kernel(ProjArgs p, float*
       slab[e] = at;
       if (!writes) return;
       o.slabs[2 * e] = at;
-      o.slabs[2 * e + 1] = total[e] ? slabs_of(e) : -1;
+      o.slabs[2 * e + 1] = slabs_of(e);
     });
   }
   lds_barrier();

@@ -85,18 +85,19 @@ __global__ __launch_bounds__(kThreads) void sort_scan_kernel(SortArgs p) {
   if (threadIdx.x == 0) p.totals[e] = all;
 }
 
-// The rows of the workgroup's tokens: pieces are loaded once, kAhead of them
-// per thread in flight, and stored to the token's k rows (row < 0: a pair
-// without an expert).
+// The rows of a workgroup's tokens: pieces are loaded once, kAhead of them per
+// thread in flight, and stored to the token's k rows (row < 0: a pair without an
+// expert).
 constexpr int kAhead = 4;
-__device__ __forceinline__ void copy_rows(const SortArgs& p, int t0, int tokens, const int* row) {
-  const int n = tokens * p.pieces;  // below 2^31: at most 256 tokens of 2^18 pieces
-  const u32x4_t* src = p.x + (int64_t)t0 * p.pieces;
-  for (int i0 = threadIdx.x; i0 < n; i0 += kAhead * kThreads) {
-    u32x4_t q[kAhead];
+__device__ __forceinline__ void load_pieces(u32x4_t* q, const u32x4_t* src, int i0, int n) {
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a)
-      if (i0 + a * kThreads < n) q[a] = __builtin_nontemporal_load(src + i0 + a * kThreads);
+  for (int a = 0; a < kAhead; ++a)
+    q[a] = __builtin_nontemporal_load(src + min(i0 + a * kThreads, n - 1));  // (past the last: that one again)
+}
+// q: the first ones, loaded already
+__device__ __forceinline__ void copy_rows(const SortArgs& p, const u32x4_t* src, int n, const int* row, u32x4_t* q) {
+  for (int i0 = threadIdx.x; i0 < n; i0 += kAhead * kThreads) {
+    if (i0 >= kAhead * kThreads) load_pieces(q, src, i0, n);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       const int i = i0 + a * kThreads;
@@ -122,6 +123,11 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(SortArgs p) {
   int* total = run + p.E;          // [E]
   const int tid = threadIdx.x;
   const int first = blockIdx.x * p.tokens, last = min(first + p.tokens, p.T);
+  const int step = kThreads / p.k;  // tokens at a time
+  // the first rows are on their way while the pairs are counted
+  u32x4_t q[kAhead];
+  const int ahead = p.x ? max(0, min(step, last - first)) * p.pieces : 0;
+  if (ahead) load_pieces(q, p.x + (int64_t)first * p.pieces, threadIdx.x, ahead);
   if (LARGE) {
     for (int e = tid; e < p.E; e += kThreads) {
       run[e] = p.table[(int64_t)e * p.chunks + blockIdx.x];
@@ -131,19 +137,26 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(SortArgs p) {
     for (int e = tid; e < p.E; e += kThreads) run[e] = total[e] = 0;
     lds_barrier();
     const int before = first * p.k, all = p.T * p.k;
-    for (int i = tid; i < all; i += kThreads) {
-      const int e = expert_of(p, i);
-      if (e < 0) continue;
-      atomicAdd(&total[e], 1);
-      if (i < before) atomicAdd(&run[e], 1);
+    constexpr int AHEAD = 8;  // ids of a thread in flight
+    for (int i0 = tid; i0 < all; i0 += AHEAD * kThreads) {
+      int e[AHEAD];
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q) e[q] = i0 + q * kThreads < all ? p.ids[i0 + q * kThreads] : -1;
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q) {
+        if (e[q] < 0 || e[q] >= p.E) continue;
+        atomicAdd(&total[e[q]], 1);
+        if (i0 + q * kThreads < before) atomicAdd(&run[e[q]], 1);
+      }
     }
   }
   lds_barrier();
   add_run_starts(run, total, p.E, scan, blockIdx.x == 0 ? p.off : nullptr);
 
-  const int step = kThreads / p.k;  // tokens at a time
   for (int t0 = first; t0 < last; t0 += step) {
     const int n = min(step, last - t0), pairs = n * p.k;
+    const u32x4_t* src = p.x + (int64_t)t0 * p.pieces;
+    if (t0 > first && p.x) load_pieces(q, src, tid, n * p.pieces);
     const int64_t pair = (int64_t)t0 * p.k + tid;
     const int e = tid < pairs ? expert_of(p, pair) : -1;
     const int r = ordered_rank(e, run, (pairs + 63) >> 6, wkeys);
@@ -151,7 +164,7 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(SortArgs p) {
     if (tid < pairs) p.row_of_pair[pair] = e >= 0 ? r : -1;
     if (e >= 0 && p.pair_of_row) p.pair_of_row[r] = (int32_t)pair;
     lds_barrier();
-    if (p.x) copy_rows(p, t0, n, rows);
+    if (p.x) copy_rows(p, src, n * p.pieces, rows, q);
     lds_barrier();
   }
 }
