@@ -41,28 +41,42 @@ def row_scale(ids, scales, lora_scale, L):
     adapter, and the adapter's index (0 there)."""
     has = (ids >= 0) & (ids < L)
     l = torch.where(has, ids, 0).long()
-    s = torch.tensor(lora_scale, dtype=torch.float32)
+    s = torch.tensor(lora_scale, dtype=torch.float32, device=ids.device)
     s = (s * scales if scales is not None else s.repeat(L))[l]
     return torch.where(has, s.double(), 0.0), l, has
 
 
-def _down(v, w, s, has, depth):
-    """s (w_t v_t) for each token's own w [T, r, depth], its bound, and the
-    product without s with its."""
-    p = torch.einsum("trk,tk->tr", w, v) * has[:, None]
-    e = (depth + 4) * HALF_F32 * torch.einsum("trk,tk->tr", w.abs(), v.abs()) * has[:, None]
+def _own(v, w, l, has):
+    """w[l_t] v_t of every token with an adapter, one adapter after the other
+    (zeros for the rest); w [L, out, in]."""
+    out = v.new_zeros((v.shape[0], w.shape[1]))
+    for a in range(w.shape[0]):
+        at = torch.nonzero(has & (l == a)).flatten()
+        if len(at):
+            out[at] = v[at] @ w[a].T
+    return out
+
+
+def _down(v, w, s, l, has):
+    """s (w v) of each token's own w [L, r, depth], its bound, and the product
+    without s with its."""
+    depth = w.shape[2]
+    p = _own(v, w, l, has)
+    e = (depth + 4) * HALF_F32 * _own(v.abs(), w.abs(), l, has)
     sp = s[:, None] * p
     e_sp = s.abs()[:, None] * e
     e_sp = e_sp + (PAIR + 4 * HALF_F32) * (sp.abs() + e_sp)
     return p, e, sp, e_sp
 
 
-def _join(v, w, sp, e_sp, back, depth, r):
-    """v w^T + sp back_t^T with back [T, out, r], and the bound, before the
-    rounding to bf16."""
-    y = v @ w.T + torch.einsum("tor,tr->to", back, sp)
-    size = v.abs() @ w.abs().T + torch.einsum("tor,tr->to", back.abs(), sp.abs() + e_sp)
-    return y, (depth + 2 * r + 8) * HALF_F32 * size + torch.einsum("tor,tr->to", back.abs(), e_sp)
+def _join(v, w, sp, e_sp, back, l, has):
+    """v w^T + back sp with each token's own back [L, out, r], and the bound,
+    before the rounding to bf16."""
+    depth, r = v.shape[1], sp.shape[1]
+    y = v @ w.T + _own(sp, back, l, has)
+    off = _own(e_sp, back.abs(), l, has)
+    size = v.abs() @ w.abs().T + _own(sp.abs(), back.abs(), l, has) + off
+    return y, (depth + 2 * r + 8) * HALF_F32 * size + off
 
 
 def rounded(v, e):
@@ -71,10 +85,9 @@ def rounded(v, e):
 
 def forward64(x, W, A, B, ids, scales, lora_scale=1.0):
     """(z, bound), (y, bound); everything in 64 bits."""
-    L, r, K = A.shape
-    s, l, has = row_scale(ids, scales, lora_scale, L)
-    z, e_z, sz, e_sz = _down(x, A[l], s, has.double(), K)
-    return (z, e_z), rounded(*_join(x, W, sz, e_sz, B[l], K, r))
+    s, l, has = row_scale(ids, scales, lora_scale, A.shape[0])
+    z, e_z, sz, e_sz = _down(x, A, s, l, has)
+    return (z, e_z), rounded(*_join(x, W, sz, e_sz, B, l, has))
 
 
 def backward64(dy, x, z, W, A, B, ids, scales, lora_scale=1.0):
@@ -82,11 +95,11 @@ def backward64(dy, x, z, W, A, B, ids, scales, lora_scale=1.0):
     L, r, K = A.shape
     N = W.shape[0]
     s, l, has = row_scale(ids, scales, lora_scale, L)
-    _, _, u, e_u = _down(dy, B[l].transpose(1, 2), s, has.double(), N)
-    dx = rounded(*_join(dy, W.T, u, e_u, A[l].transpose(1, 2), N, r))
+    _, _, u, e_u = _down(dy, B.transpose(1, 2), s, l, has)
+    dx = rounded(*_join(dy, W.T, u, e_u, A.transpose(1, 2), l, has))
     sz = s[:, None] * z
     e_sz = (PAIR + 4 * HALF_F32) * sz.abs()
-    dA, eA, dB, eB = (torch.zeros(s, dtype=torch.float64) for s in ((L, r, K), (L, r, K), (L, N, r), (L, N, r)))
+    dA, eA, dB, eB = (x.new_zeros(n) for n in ((L, r, K), (L, r, K), (L, N, r), (L, N, r)))
     for a in range(L):
         at = torch.nonzero(has & (l == a)).flatten()
         n = 2 * len(at) + 16  # pairs, and the slabs' additions

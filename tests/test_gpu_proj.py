@@ -38,7 +38,12 @@ CASES = [  # T, K, N, L, r, ids, scales
     (1030, 520, 392, 5, 64, "mixed", False), (1100, 136, 264, 3, 32, "one", True), (2100, 264, 640, 16, 16, "runs", True),
     (4500, 136, 264, 6, 16, "runs", True), (4200, 264, 136, 4, 96, "mixed", True),
     (201, 264, 200, 32, 16, "each", True), (90, 1000, 520, 40, 128, "mixed", True), (33, 136, 2880, 500, 8, "each", True),
-    (1300, 264, 4104, 9, 72, "each", True), (600, 2880, 2880, 16, 32, "runs", True)]
+    (1300, 264, 4104, 9, 72, "each", True), (600, 2880, 2880, 16, 32, "runs", True),
+    # every tile: small ones whole and with K split, deep ones, large ones
+    (2100, 2056, 2064, 3, 16, "each", True), (1400, 2056, 2064, 5, 24, "runs", True),
+    (1832, 16, 2216, 2, 16, "runs", True), (2423, 1368, 8, 3, 128, "mixed", True), (194, 2760, 6904, 53, 64, "each", True),
+    (260, 1032, 4104, 6, 8, "each", True), (500, 136, 6000, 40, 8, "mixed", True),
+    (8192, 1032, 4096, 3, 16, "runs", True), (8192, 1032, 4096, 37, 40, "mixed", False)]
 
 
 @pytest.mark.parametrize("T,K,N,L,r,ids,scales", CASES)
@@ -53,10 +58,11 @@ def test_forward_and_backward(T, K, N, L, r, ids, scales):
     ws, ok_ws = workspace(shape, False)
     lm.moe_lora_proj_forward(shape, d[0], d[5], d[1], d[2], d[3], ws, y, z=z, scales=ds)
     assert ok_ws() and ok_y() and ok_z()
-    f = [t.double() for t in (x, W, A, B, dy)]
-    (z64, e_z), (y64, e_y) = forward64(*f[:4], i, s, scale)
-    within(z, z64, e_z, "z")
-    within(y, y64, e_y, "y")
+    # (the 64-bit forms on the GPU, the largest case would take half a minute)
+    f = [t.double() for t in d[:5]]
+    (z64, e_z), (y64, e_y) = forward64(*f[:4], d[5], ds, scale)
+    within(z, z64.cpu(), e_z.cpu(), "z")
+    within(y, y64.cpu(), e_y.cpu(), "y")
     assert bool((z.cpu()[(i < 0) | (i >= L)] == 0).all())
     y2 = torch.empty_like(y)  # without z
     ws, ok_ws = workspace(shape)
@@ -67,9 +73,9 @@ def test_forward_and_backward(T, K, N, L, r, ids, scales):
     dB, ok_b = guarded((L, N, r))
     lm.moe_lora_proj_backward(shape, d[4], d[0], d[5], z, d[1], d[2], d[3], ws, dx=dx, dA=dA, dB=dB, scales=ds)
     assert ok_ws() and ok_x() and ok_a() and ok_b()
-    want = backward64(f[4], f[0], z.double().cpu(), *f[1:4], i, s, scale)
+    want = backward64(f[4], f[0], z.double(), *f[1:4], d[5], ds, scale)
     for n, t in (("dx", dx), ("dA", dA), ("dB", dB)):
-        within(t, *want[n], n)
+        within(t, want[n][0].cpu(), want[n][1].cpu(), n)
     # each alone, and none of them touches another's memory
     for n, t in (("dx", dx), ("dA", dA), ("dB", dB)):
         one = torch.empty_like(t)
