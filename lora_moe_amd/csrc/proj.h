@@ -91,9 +91,9 @@ struct ProjGrads {
   uint16_t* dB;
   float* slabs;
 };
-int proj_grad_rows(int T, int K, int N, int r);
+int proj_grad_rows(int T, int K, int N, int L, int r);
 inline int64_t proj_grad_items(const ProjArgs& p) { return p.T / p.grad_rows + p.L; }
-size_t proj_grad_slab_bytes(int T, int K, int N, int r);
+size_t proj_grad_slab_bytes(const ProjArgs& p);
 int launch_proj_grads(const ProjArgs& p, const ProjGrads& g, hipStream_t st);
 
 // x [W; A]^T, fp32, into slabs [proj_both_splits][T][N + proj_slots r]: of at most

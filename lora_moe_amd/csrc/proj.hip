@@ -47,7 +47,7 @@ ProjArgs args_of(const moe_lora_proj_shape& s, const int32_t* ids, const float* 
   p.T = s.T, p.K = s.K, p.N = s.N, p.L = s.L, p.r = s.r, p.scale = s.lora_scale;
   p.ids = ids, p.scales = scales;
   p.shrink_rows = proj_shrink_rows(s.T, s.r);
-  p.grad_rows = grads ? proj_grad_rows(s.T, s.K, s.N, s.r) : 0;
+  p.grad_rows = grads ? proj_grad_rows(s.T, s.K, s.N, s.L, s.r) : 0;
   return p;
 }
 
@@ -101,7 +101,7 @@ struct Backward {
     take_order(p, w);
     us = w.take<uint16_t>((size_t)p.T * 2 * p.r);
     zs = w.take<uint16_t>((size_t)p.T * 2 * p.r);
-    slabs = w.take<float>(std::max(proj_gemm_slab_bytes(p, true), proj_grad_slab_bytes(p.T, p.K, p.N, p.r)) / 4);
+    slabs = w.take<float>(std::max(proj_gemm_slab_bytes(p, true), proj_grad_slab_bytes(p)) / 4);
     bytes = w.used;
   }
 };

@@ -192,16 +192,18 @@ int slabs_of(int T, int rows) { return 2 * (T / rows); }
 
 }  // namespace
 
-// Enough pieces to fill the chip with two rounds of workgroups, but at least
-// 8r rows each (a slab of r columns costs as much as 4r rows to write and read
-// again).
-int proj_grad_rows(int T, int K, int N, int r) {
+// Enough pieces to fill the chip with four rounds of workgroups, but at least 8r
+// rows each (a slab of r columns costs as much as 4r rows to write and read
+// again).  Few tokens of several adapters are not split at all, which spares the
+// join (4 us with 1001 tokens; a single adapter's would take 10 us longer).
+int proj_grad_rows(int T, int K, int N, int L, int r) {
+  if (T <= kMostRows && L > 4) return kMostRows;
   const int64_t rows = (int64_t)T * ((K + N) / WT + 1) / 1024;
   return (int)std::min<int64_t>(kMostRows, std::max<int64_t>((rows + BK - 1) / BK * BK, std::max(256, 8 * r)));
 }
 
-size_t proj_grad_slab_bytes(int T, int K, int N, int r) {
-  return (size_t)slabs_of(T, proj_grad_rows(T, K, N, r)) * r * (K + N) * sizeof(float);
+size_t proj_grad_slab_bytes(const ProjArgs& p) {
+  return (size_t)slabs_of(p.T, p.grad_rows) * p.r * ((size_t)p.K + p.N) * sizeof(float);
 }
 
 int launch_proj_grads(const ProjArgs& p, const ProjGrads& g, hipStream_t st) {

@@ -79,15 +79,16 @@ __global__ __launch_bounds__(kThreads) void proj_order_kernel(ProjArgs p, float*
   const int t0 = blockIdx.x * kTokens, mine = min(kTokens, p.T - t0);
   for (int e = tid; e < S; e += kThreads) next[e] = total[e] = 0;
   lds_barrier();
-  for (int base = 0; base < p.T; base += 4 * kThreads) {  // four ids a thread, in flight together
-    int id[4];
+  constexpr int AHEAD = 8;  // ids of a thread in flight
+  for (int base = 0; base < p.T; base += AHEAD * kThreads) {
+    int id[AHEAD];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < AHEAD; ++i) {
       const int t = base + i * kThreads + tid;
       id[i] = t < p.T ? p.ids[t] : 0;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < AHEAD; ++i) {
       const int t = base + i * kThreads + tid;
       if (t - (tid & 63) < p.T) count_keys(t < p.T ? key_of(id[i], p.L) : -1, t < t0, total, next);
     }
