@@ -1,4 +1,4 @@
-// The projection's products beyond a few tokens: LDS-tiled bf16 MFMA.
+// The projection's products: LDS-tiled bf16 MFMA.
 //
 //   forward   y[t]  = W x[t]    + B_l (s_l z[t])
 //   backward  dx[t] = W^T dy[t] + A_l^T u[t]
@@ -17,10 +17,19 @@
 // 0 in place of such values, and a tile that met one adds their terms to the
 // rows that they belong to, one by one, in its epilogue.
 //
-// The loop is that of ffn_gemm.hip: a two-stage ring filled by asynchronous
-// copies that go out between the MFMAs of the stage before.  The adapters'
-// shares are further stages of the same loop, whose copies get their addresses
-// when their turn comes.
+// The loop is that of ffn_gemm.hip, with a ring of two to four slots: filled by
+// asynchronous copies that go out between the MFMAs of the stage before.  The
+// adapters' shares are further stages of the same loop, whose copies get their
+// addresses when their turn comes.
+//
+// What bounds it: with large tiles the matrix cores at the clock that the
+// card's power leaves them (8192 tokens, 4096 x 4096, rank 16: 219 us, 1.26
+// PFLOP/s; 7168 x 7168, rank 64: 719 us, 1.19 with the adapters' stages, of
+// which 31 us are theirs where the flops would take 17: their first touch of
+// B comes late from memory).  With a workgroup per CU the copies (0.34 us a
+// stage of 32 KB, 100 GB/s to a CU), and up to 201 tokens a first trip through
+// memory and the weights behind it.  (BOTH, a decode batch's x [W; A]^T without
+// an order, is described in proj_few.hip.)
 #include "ffn.h"
 #include "internal.h"
 #include "proj.h"
@@ -36,6 +45,16 @@ struct TileArgs {
   int in_cols, out_cols;  // K and N of a forward
   int ncol, nrow;
   int ncol_w, slots;      // BOTH: column tiles of W, then those of so many adapters
+};
+
+// A tile whose wavefronts share the stage's K slices too: KS groups of WM x WN
+// wavefronts, each with 4 / KS of the four slices, whose sums meet in LDS at the
+// end.  A wavefront's blocks are larger for it, and fewer bytes come out of LDS.
+template <int BM, int BN, int WM, int WN, int KS>
+struct SliceCfg : FfnCfg<BM, BN, WM, WN> {
+  typedef FfnCfg<BM, BN, WM, WN> Base;
+  static constexpr int NW = Base::NW * KS, NT = 64 * NW;
+  static constexpr int NCA = Base::ABYTES / 1024 / NW, NCB = Base::BBYTES / 1024 / NW;
 };
 
 // RING: slots of the ring, of which all but one are filled ahead.
@@ -97,7 +116,10 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
   const ProjArgs& p = a.p;
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / C::WN, wn = wave % C::WN;
+  constexpr int KS = C::NW / (C::WM * C::WN), KK = 4 / KS;  // groups, and slices of a stage each
+  static_assert(RING * KK % 2 == 0 && MI * NI % KS == 0, "fragments' sets alternate, blocks are shared out");
+  const int group = wave / (C::WM * C::WN), in_group = wave % (C::WM * C::WN);
+  const int wm = in_group / C::WN, wn = in_group % C::WN;
   const int T = p.T, K = a.in_cols, r = p.r, ncol = a.ncol, nrow = a.nrow;
 
   // workgroups to tiles as in ffn_gemm.hip: each XCD a contiguous eighth, in
@@ -248,6 +270,7 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
   bool bad = false;
   auto read = [&](int slot, int kk, int set, int i) __attribute__((always_inline)) {
     const char* from = smem + slot * C::STAGE;
+    kk += group * KK;
     if (i == 0) af[set][0] = A.frag(from, wm * (C::BM / C::WM), 0, kk);
     else if (i <= NI) bf[set][i - 1] = B.frag(from + C::ABYTES, wn * (C::BN / C::WN), i - 1, kk);
     else af[set][i - NI] = A.frag(from, wm * (C::BM / C::WM), i - NI, kk);
@@ -328,19 +351,22 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
     for_each<RING>([&](auto h_c) __attribute__((always_inline)) {
       constexpr int slot = decltype(h_c)::value, next = (slot + 1) % RING;
       if (MIXED && RING > 2 && s + slot >= nst) return;
+      constexpr int set = slot * KK & 1;  // of the stage's first slice
       const bool shared = s + slot < base;
-      slice(shared, 0, slot, 1, 0, no(), mixed_c);
-      slice(shared, 1, slot, 2, 0, no(), mixed_c);
+      for_each<KK - 1>([&](auto k_c) __attribute__((always_inline)) {
+        constexpr int k = decltype(k_c)::value;
+        if (k < KK - 2) slice(shared, set ^ (k & 1), slot, k + 1, 0, no(), mixed_c);
+      });
       if constexpr (MIXED) {
         at(s + slot + RING);
       } else {
         A.at(s + slot + RING, true);
         B.at(s + slot + RING, true);
       }
-      slice(shared, 0, slot, 3, 0, no(), mixed_c);
+      if (KK > 1) slice(shared, set ^ (KK & 1), slot, KK - 1, 0, no(), mixed_c);
       __builtin_amdgcn_s_waitcnt(wait_next);
       bare_barrier();
-      slice(shared, 1, next, 0, slot, yes(), mixed_c);
+      slice(shared, set ^ (KK - 1 & 1), next, 0, slot, yes(), mixed_c);
     });
   };
   int s = s0;
@@ -353,25 +379,56 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
   bare_barrier();
   const bool mend = *not_finite;
 
+  // A wavefront's blocks, by group: a group hands the others theirs and adds
+  // what it gets, in a fixed order.
+  constexpr int NB = MI * NI, PER = NB / KS;
+  if constexpr (KS > 1) {
+    static_assert(C::WM * C::WN * (KS - 1) * NB * 4096 <= RING * C::STAGE, "they must fit the ring");
+    f32x4_t* sums = reinterpret_cast<f32x4_t*>(smem) + in_group * (KS - 1) * NB * 256 + lane;
+    auto place = [&](int from, int to) { return (to * (KS - 1) + (from - to + KS) % KS - 1) * PER; };
+    for_each<NB>([&](auto f_c) __attribute__((always_inline)) {
+      constexpr int f = decltype(f_c)::value, to = f / PER;
+      if (to == group) return;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x16_t& v = acc[f / NI][f % NI];
+        sums[((place(group, to) + f % PER) * 4 + q) * 64] = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      }
+    });
+    lds_barrier();
+    for_each<NB>([&](auto f_c) __attribute__((always_inline)) {
+      constexpr int f = decltype(f_c)::value, to = f / PER;
+      if (to != group) return;
+#pragma unroll
+      for (int d = 1; d < KS; ++d)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4_t v = sums[((place((to + d) % KS, to) + f % PER) * 4 + q) * 64];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[f / NI][f % NI][4 * q + e] += v[e];
+        }
+    });
+    lds_barrier();
+  }
+
   // Epilogue, 32 rows of the wavefront at a time through its own part of the
   // LDS, so that memory sees whole lines (as in ffn_gemm.hip).
-  constexpr int WC = C::BN / C::WN, ROWF = WC + 4;
+  constexpr int EC = NI < PER ? NI : PER;  // blocks side by side
+  constexpr int WC = EC * 32, ROWF = WC + 4;
   constexpr int LPR = WC / 8, RPI = 64 / LPR, STEPS = 32 / RPI;
   float* mine = reinterpret_cast<float*>(smem) + wave * 32 * ROWF;
-  static_assert(C::NW * 32 * ROWF * 4 <= C::LDS, "staged rows must fit the ring");
+  static_assert(C::NW * 32 * ROWF * 4 <= RING * C::STAGE, "staged rows must fit the ring");
   const int l32 = lane & 31, kh = lane >> 5;
-  const int oc = (lane % LPR) * 8, n = n0 + wn * WC + oc;
+  const int oc = (lane % LPR) * 8, n = n0 + wn * (C::BN / C::WN) + group * PER % NI * 32 + oc;
 #pragma unroll 1
-  for (int i = 0; i < MI; ++i) {
-    for_each<MI>([&](auto b_c) __attribute__((always_inline)) {
-      constexpr int b = decltype(b_c)::value;
-      if (i != b) return;
+  for (int i = group * PER / NI; i < group * PER / NI + PER / EC; ++i) {
+    for_each<NB>([&](auto f_c) __attribute__((always_inline)) {
+      constexpr int f = decltype(f_c)::value, b = f / NI, j = f % NI;
+      if (i != b || f / PER != group) return;
 #pragma unroll
-      for (int j = 0; j < NI; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<f32x4_t*>(mine + l32 * ROWF + j * 32 + 8 * q + 4 * kh) =
-              f32x4_t{acc[b][j][4 * q], acc[b][j][4 * q + 1], acc[b][j][4 * q + 2], acc[b][j][4 * q + 3]};
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4_t*>(mine + l32 * ROWF + j % EC * 32 + 8 * q + 4 * kh) =
+            f32x4_t{acc[b][j][4 * q], acc[b][j][4 * q + 1], acc[b][j][4 * q + 2], acc[b][j][4 * q + 3]};
     });
     asm volatile("" ::: "memory");  // a wavefront's LDS accesses run in order
 #pragma unroll
@@ -420,10 +477,13 @@ __global__ __launch_bounds__(256) void proj_join_kernel(TileArgs a) {
 typedef FfnCfg<256, 256, 2, 4> Big;
 typedef FfnCfg<128, 128, 2, 2> Small;
 // One workgroup per CU, four slots: where tiles are few, a stage is as long as
-// its copies take to come, and three on their way hide that (8 wavefronts; with
-// 4 of them 2 us more).  1001 tokens, 2880 x 2880 (184 tiles): 21 us, 30 with
-// Small.
-typedef FfnCfg<128, 128, 2, 4> Deep;
+// its copies take to come, and three on their way hide that.  Two groups of 2 x
+// 2 wavefronts with 64 x 64 each read a third less from LDS than 2 x 4 with 64 x
+// 32 (1001 tokens with order and shrink, us: 2880 x 2880, rank 32, 44.7 and
+// 45.6, 4096 x 4096, rank 16, 52.6 and 54.1); one such group takes 2 us more than
+// 2 x 4.  2880 x 2880 (184 tiles): 24 us, of which 8.5 are launch, first trip
+// through memory and epilogue; adapters' stages 2 to 3 more.
+typedef SliceCfg<128, 128, 2, 2, 2> Deep;
 // Decode batches: small tiles of few wavefronts, several workgroups to a CU, so
 // that nearly all of its LDS is weights on their way (up to 32 tokens three or
 // four slots of 12 KB in three workgroups, beyond it three of 24 KB in two).
