@@ -303,37 +303,57 @@ __global__ __launch_bounds__(kThreads) void unsort_backward_kernel(BackArgs p) {
 
 // ---- router
 
-// One thread writes V logits' gradients of one token; the token's k pairs come
-// from the L1 cache.  A slot without an expert takes no part.
+// P lanes write P V logits' gradients of one token: lane j brings pair j, so that
+// a wavefront reads each of the three arrays once, and hands it to the others (8192
+// tokens, 256 experts, top-8: 5.8 us, 8.5 where every lane reads all pairs; the
+// 8.4 MB of logits would take 2, launch and first trip the rest).  A slot without an expert takes no part.
 template <int V>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(const int32_t* __restrict__ ids,
                                                                   const float* __restrict__ w,
-                                                                  const float* __restrict__ dw, int64_t n, int E,
-                                                                  int k, float* __restrict__ dlogits) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= n) return;
-  const int per = E / V;
-  const int64_t t = i / per;
-  const int e0 = (int)(i - t * per) * V;
-  float sum = 0.f;
-  for (int j = 0; j < k; ++j) {
-    const int e = ids[t * k + j];
-    if (e >= 0 && e < E) sum = fmaf(w[t * k + j], dw[t * k + j], sum);
+                                                                  const float* __restrict__ dw, int T, int E, int k,
+                                                                  int P, int chunks, float* __restrict__ dlogits) {
+  const int64_t group = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / P;
+  const int lane = threadIdx.x & (P - 1);
+  const int64_t t = chunks == 1 ? group : group / chunks;
+  const int e0 = ((int)(group - t * chunks) * P + lane) * V;  // (below E + 64 V)
+  int e = -1;
+  float mine = 0.f, g = 0.f;
+  if (t < T && lane < k) {  // (on their way together, an expert or not)
+    e = ids[t * k + lane];
+    mine = w[t * k + lane];
+    g = dw[t * k + lane];
   }
+  const bool has = e >= 0 && e < E;
+  float sum = has ? mine * g : 0.f;
+  for (int o = 1; o < P; o <<= 1) sum += __shfl_xor(sum, o, 64);
+  g = has ? mine * (g - sum) : 0.f;
+  if (!has) e = -1;
   float v[V];
 #pragma unroll
   for (int q = 0; q < V; ++q) v[q] = 0.f;
   for (int j = 0; j < k; ++j) {
-    const int e = ids[t * k + j] - e0;
-    if (e < 0 || e >= V) continue;
-    const float g = w[t * k + j] * (dw[t * k + j] - sum);
+    const int at = __shfl(e, j, P) - e0;
+    const float of = __shfl(g, j, P);
 #pragma unroll
     for (int q = 0; q < V; ++q)
-      if (q == e) v[q] += g;
+      if (at == q) v[q] += of;
   }
+  if (t >= T || e0 >= E) return;
   float* out = dlogits + t * E + e0;
   if constexpr (V == 4) *reinterpret_cast<f32x4_t*>(out) = f32x4_t{v[0], v[1], v[2], v[3]};
   else out[0] = v[0];
+}
+
+template <int V>
+int launch_route_backward(const int32_t* ids, const float* w, const float* dw, int T, int E, int k, float* dlogits,
+                          hipStream_t st) {
+  int P = 1;
+  while (P < 64 && (P < k || P * V < E)) P *= 2;
+  const int chunks = (E + P * V - 1) / (P * V);
+  const int64_t blocks = ((int64_t)T * chunks * P + kThreads - 1) / kThreads;
+  if (blocks * kThreads > 0xffffffff) return MOE_LORA_EUNSUPPORTED;
+  route_backward_kernel<V><<<(unsigned)blocks, kThreads, 0, st>>>(ids, w, dw, T, E, k, P, chunks, dlogits);
+  return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
 // ---- host side
@@ -522,13 +542,8 @@ int moe_lora_route_backward(const moe_lora_shape* shape, const int32_t* topk_ids
   const Range out[] = {{dlogits, (size_t)logits * 4}};
   if (any_overlap(in, 3, out, 1)) return MOE_LORA_EINVAL;
   hipStream_t st = (hipStream_t)stream;
-  if (E % 4 == 0)
-    route_backward_kernel<4><<<blocks_of(logits / 4), kThreads, 0, st>>>(topk_ids, topk_weights, dweights, logits / 4,
-                                                                         E, k, dlogits);
-  else
-    route_backward_kernel<1><<<blocks_of(logits), kThreads, 0, st>>>(topk_ids, topk_weights, dweights, logits, E, k,
-                                                                     dlogits);
-  return launched() ? MOE_LORA_OK : MOE_LORA_EHIP;
+  const auto launch = E % 4 ? launch_route_backward<1> : launch_route_backward<4>;
+  return launch(topk_ids, topk_weights, dweights, shape->T, E, k, dlogits, st);
 }
 
 }  // extern "C"
