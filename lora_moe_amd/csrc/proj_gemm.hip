@@ -25,7 +25,7 @@
 // What bounds it: with large tiles the matrix cores at the clock that the
 // card's power leaves them (8192 tokens, 4096 x 4096, rank 16: 219 us, 1.26
 // PFLOP/s; 7168 x 7168, rank 64: 719 us, 1.19 with the adapters' stages, of
-// which 31 us are theirs where the flops would take 17: their first touch of
+// which 37 us are theirs where the flops would take 17: their first touch of
 // B comes late from memory).  With a workgroup per CU the copies (0.34 us a
 // stage of 32 KB, 100 GB/s to a CU), and up to 201 tokens a first trip through
 // memory and the weights behind it.  (BOTH, a decode batch's x [W; A]^T without

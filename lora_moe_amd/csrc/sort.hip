@@ -10,7 +10,11 @@
 // All of it is bound by the rows' way through memory.  The sort reads a
 // token's row once and writes it topk times, so that what is left is the order
 // of the pairs: a stable counting sort whose counts are integers (LDS atomics,
-// the same whatever their order).
+// the same whatever their order).  8192 tokens of 7168 bf16 values, top-8: sort
+// 228 us at 4.7 TB/s and 13 for the order, back 177 at 6.0; 4096 tokens of 2048
+// fp32 values: 64 (4.9 TB/s) and 10, 54 (5.5), gradient 126 (4.8).  A large copy
+// reaches 4.4 to 4.9.  1001 tokens of 2880 fp16 values, top-4: 10.8, 6.5 and
+// 11.3 us, a third of them a kernel's start and first trip.
 #include <algorithm>
 
 #include "abi_util.h"
@@ -306,7 +310,8 @@ __global__ __launch_bounds__(kThreads) void unsort_backward_kernel(BackArgs p) {
 // P lanes write P V logits' gradients of one token: lane j brings pair j, so that
 // a wavefront reads each of the three arrays once, and hands it to the others (8192
 // tokens, 256 experts, top-8: 5.8 us, 8.5 where every lane reads all pairs; the
-// 8.4 MB of logits would take 2, launch and first trip the rest).  A slot without an expert takes no part.
+// 8.4 MB of logits would take 2, launch and first trip the rest).  A slot without
+// an expert takes no part.
 template <int V>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(const int32_t* __restrict__ ids,
                                                                   const float* __restrict__ w,
