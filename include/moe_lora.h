@@ -556,8 +556,8 @@ size_t moe_lora_proj_workspace_bytes(const moe_lora_proj_shape* shape, int backw
  *   z         device [T][r] fp32, written for the backward (zeros for tokens
  *             without an adapter); NULL where none follows
  *   y         device [T][N] bf16, overwritten
- * Sums are fp32; s_l z goes into the second product as a sum of two bf16 (16
- * bits) or in fp32; y is rounded once.  The same inputs give the same bits. */
+ * Sums are fp32; s_l z goes into the second product in fp32 or as a sum of
+ * three bf16, which is the same 24 bits; y is rounded once.  The same inputs give the same bits. */
 int moe_lora_proj_forward(const moe_lora_proj_shape* shape, const uint16_t* x, const int32_t* lora_ids,
                           const uint16_t* W, const uint16_t* A, const uint16_t* B, const float* scales, float* z,
                           void* workspace, size_t ws_bytes, uint16_t* y, void* stream);
@@ -571,7 +571,7 @@ int moe_lora_proj_forward(const moe_lora_proj_shape* shape, const uint16_t* x, c
  *            three is wanted (where T > 0)
  * Gradients are overwritten (zeros for an adapter without tokens, and for T =
  * 0), not added to.  Sums are fp32, u and s_l z enter the products as sums of
- * two bf16, each gradient is rounded once.  The same inputs give the same
+ * three bf16 (all 24 bits), each gradient is rounded once.  The same inputs give the same
  * bits. */
 int moe_lora_proj_backward(const moe_lora_proj_shape* shape, const uint16_t* dy, const uint16_t* x,
                            const int32_t* lora_ids, const float* z, const uint16_t* W, const uint16_t* A,

@@ -57,6 +57,30 @@ __device__ __forceinline__ void store8_pair(uint16_t* hi, uint16_t* lo, const fl
   *reinterpret_cast<u32x4_t*>(lo) = b;
 }
 
+// v as the sum of three bf16, all of its 24 bits (steps below 2^-133, a bf16's
+// smallest, aside): the pair's parts and what they leave.
+__device__ __forceinline__ void f32_to_bf16_three(float v, uint16_t* part) {
+  f32_to_bf16_pair(v, part, part + 1);
+  const float left = v - bf16_to_f32(part[0]) - bf16_to_f32(part[1]);
+  const bool finite = (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u;
+  part[2] = finite ? __builtin_bit_cast(uint16_t, (__bf16)left) : (uint16_t)0;
+}
+
+// 8 values as sums of three bf16, the parts `step` apart
+__device__ __forceinline__ void store8_three(uint16_t* to, int step, const float* v) {
+  u32x4_t q[3];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint16_t a[3], b[3];
+    f32_to_bf16_three(v[2 * i], a);
+    f32_to_bf16_three(v[2 * i + 1], b);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) q[k][i] = a[k] | (uint32_t)b[k] << 16;
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4_t*>(to + k * step) = q[k];
+}
+
 // D(16x16, fp32) += A(16x32, bf16) * B(32x16, bf16) on one wavefront.
 // Lane l supplies A[m = l%16][k = 8*(l/16) .. +8] and B[k = 8*(l/16) .. +8][n = l%16];
 // it receives D[m = 4*(l/16) + i][n = l%16], i = 0..3.  Only the pairing of

@@ -53,25 +53,31 @@ __device__ __forceinline__ float proj_scale(const ProjArgs& p, int l) {
   return p.scales ? p.scale * p.scales[l] : p.scale;
 }
 
-// Pairs: [T rows][2r] bf16, a row's r values rounded and behind them their
-// remainders, which meet the same weights: 16 bits of each value.
+// Parts: [T rows][3r] bf16, a row's r values rounded, behind them what is left
+// of each, rounded too, and behind those what is left then.  All three meet the
+// same weights, and their sum is the fp32 value: sums down to the rank keep all
+// of their bits on the way into the next product.  (The first two alone, 16
+// bits, show in the gradients: 1.1e-4 of their norm from sums in fp32, where the
+// order of sums makes 5e-5.  The third takes 2 us of 28 of a tile kernel with
+// 1001 tokens, 2880 x 2880, rank 32, 5 of 228 with 8192, 4096 x 4096, rank 16.)
+constexpr int kParts = 3;
 
 // z (NULL: not wanted): zeros for the tokens without an adapter are written
-// here; zs (backward; NULL else): pairs of s_l z.
+// here; zs (backward; NULL else): parts of s_l z.
 int launch_proj_order(const ProjArgs& p, float* z, const float* kept, uint16_t* zs, hipStream_t st);
 
-// pairs[m] = s_l * (weights of row m's adapter) in[perm[m]] and, on request,
+// parts[m] = s_l * (weights of row m's adapter) in[perm[m]] and, on request,
 // the product without s_l by token (z).  back: in = dy, weights = B [L][N][r];
 // else in = x, weights = A [L][r][K].
-int launch_proj_shrink(const ProjArgs& p, bool back, const uint16_t* in, const uint16_t* weights, uint16_t* pairs,
+int launch_proj_shrink(const ProjArgs& p, bool back, const uint16_t* in, const uint16_t* weights, uint16_t* parts,
                        float* z, hipStream_t st);
 
-// out[perm[m]] = in[perm[m]] W^T + pairs[m] weights^T; back: the same with W
+// out[perm[m]] = in[perm[m]] W^T + parts[m] weights^T; back: the same with W
 // and the adapters' weights by their columns.
 struct ProjGemm {
   const uint16_t* in;
   const uint16_t* W;
-  const uint16_t* pairs;
+  const uint16_t* parts;
   const uint16_t* weights;
   uint16_t* out;
   float* slabs;
@@ -79,14 +85,17 @@ struct ProjGemm {
   int32_t* place;  // [64] of a token's adapter among those met (launch_proj_both)
 };
 size_t proj_gemm_slab_bytes(const ProjArgs& p, bool back);
+// Its tile (0 to 3: 256 x 256, 128 x 128, the same in two groups, 64 x 128) times
+// 32 plus its K splits, for tests that have to meet all of them.
+int proj_gemm_plan(int T, int K, int N, int r, bool back);
 int launch_proj_gemm(const ProjArgs& p, bool back, ProjGemm g, hipStream_t st);
 
 // dA and dB (either may be NULL)
 struct ProjGrads {
   const uint16_t* x;
   const uint16_t* dy;
-  const uint16_t* us;  // pairs of u
-  const uint16_t* zs;  // pairs of s_l z
+  const uint16_t* us;  // parts of u
+  const uint16_t* zs;  // parts of s_l z
   uint16_t* dA;
   uint16_t* dB;
   float* slabs;

@@ -76,7 +76,7 @@ void take_order(ProjArgs& p, Parts& w) {
 }
 
 struct Forward {
-  uint16_t* pairs;
+  uint16_t* parts;
   float* slabs;
   size_t bytes;
   Forward(ProjArgs& p, void* ws) {
@@ -85,7 +85,7 @@ struct Forward {
       slabs = w.take<float>(proj_few_slab_bytes(p) / 4);
     } else {
       take_order(p, w);
-      pairs = w.take<uint16_t>((size_t)p.T * 2 * p.r);
+      parts = w.take<uint16_t>((size_t)p.T * kParts * p.r);
       slabs = w.take<float>(proj_gemm_slab_bytes(p, false) / 4);
     }
     bytes = w.used;
@@ -99,8 +99,8 @@ struct Backward {
   Backward(ProjArgs& p, void* ws) {
     Parts w(ws);
     take_order(p, w);
-    us = w.take<uint16_t>((size_t)p.T * 2 * p.r);
-    zs = w.take<uint16_t>((size_t)p.T * 2 * p.r);
+    us = w.take<uint16_t>((size_t)p.T * kParts * p.r);
+    zs = w.take<uint16_t>((size_t)p.T * kParts * p.r);
     slabs = w.take<float>(std::max(proj_gemm_slab_bytes(p, true), proj_grad_slab_bytes(p)) / 4);
     bytes = w.used;
   }
@@ -157,8 +157,8 @@ int moe_lora_proj_forward(const moe_lora_proj_shape* shape, const uint16_t* x, c
   const Forward f(p, workspace);
   if (proj_few(p.T, p.N, p.L, p.r)) return launch_proj_few(p, x, W, A, B, z, f.slabs, y, st);
   int r = launch_proj_order(p, z, nullptr, nullptr, st);
-  if (!r) r = launch_proj_shrink(p, false, x, A, f.pairs, z, st);
-  return r ? r : launch_proj_gemm(p, false, ProjGemm{x, W, f.pairs, B, y, f.slabs, 1}, st);
+  if (!r) r = launch_proj_shrink(p, false, x, A, f.parts, z, st);
+  return r ? r : launch_proj_gemm(p, false, ProjGemm{x, W, f.parts, B, y, f.slabs, 1}, st);
 }
 
 int moe_lora_proj_backward(const moe_lora_proj_shape* shape, const uint16_t* dy, const uint16_t* x,

@@ -5,8 +5,8 @@
 //
 // One product each, over the tokens sorted by adapter: a tile's K loop runs
 // over the shared weights first, then over the ranks of the adapters whose
-// rows the tile holds, 64 deep like the rest (a rank takes 2r: the pairs of
-// the values to 16 bits).  A row takes part in its own adapter's share and is
+// rows the tile holds, 64 deep like the rest (a rank takes 3r: a value is the
+// sum of three bf16).  A row takes part in its own adapter's share and is
 // zeros in another's, so a tile of one long request has one share and a tile
 // of a decode batch as many as it has adapters, while W is met once by all.
 // The sorted order exists only in the addresses: rows of x (dy) are gathered
@@ -81,7 +81,7 @@ __device__ __forceinline__ u32x4_t only_finite(u32x4_t v) {
 }
 
 // The terms of a row that only_finite took out, for 8 neighbouring outputs.
-// z: the row's pair; w: the adapter's weight of the first output and rank 0,
+// z: the row's parts; w: the adapter's weight of the first output and rank 0,
 // `rank` apart along the rank and `out` along the outputs.
 struct Eight {
   f32x4_t v[2];
@@ -93,7 +93,7 @@ __device__ __noinline__ Eight add_not_finite(Eight e, const uint16_t* z, const u
     float s = e.v[q >> 2][q & 3];
     for (int j = 0; j < r; ++j) {
       const uint16_t b = w[j * rank + q * out];
-      if ((b & 0x7f80u) == 0x7f80u) s += (bf16_to_f32(z[j]) + bf16_to_f32(z[r + j])) * bf16_to_f32(b);
+      if ((b & 0x7f80u) == 0x7f80u) s += (bf16_to_f32(z[j]) + bf16_to_f32(z[r + j]) + bf16_to_f32(z[2 * r + j])) * bf16_to_f32(b);
     }
     e.v[q >> 2][q & 3] = s;
   }
@@ -142,12 +142,12 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
   auto token_of = [&](int m) { return BOTH ? m : p.o.perm[m]; };
 
   // Stages: those of the shared weights, then those of the tile's shares;
-  // column kx of the latter's part of K is value kx % 2r of share kx / 2r.
-  const int last = min(m0 + C::BM, T) - 1, r2 = 2 * r;
+  // column kx of the latter's part of K is value kx % 3r of share kx / 3r.
+  const int last = min(m0 + C::BM, T) - 1, deep = kParts * r;
   const int run0 = BOTH ? 0 : p.o.run[m0], with = BOTH ? 0 : p.o.count[2];  // runs from `with` on: without an adapter
   const int shares = BOTH ? 0 : max(0, min(p.o.run[last] + 1, with) - run0);
   const int base = (K + BK - 1) / BK, kfirst = K - base * BK;
-  const int total = base + (shares * r2 + BK - 1) / BK;
+  const int total = base + (shares * deep + BK - 1) / BK;
   // this split's
   const int s0 = SPLIT ? (int)((int64_t)total * split / a.g.splits) : 0;
   const int nst = SPLIT ? (int)((int64_t)total * (split + 1) / a.g.splits) : total;
@@ -156,8 +156,8 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
   Operand<B_KC, C::BN, C::NCB, false> B;
   A.init(a.g.in, 0, K, 0, kfirst, wave, 0);
   int my_share[C::NCA];  // of this lane's rows
-  const uint32_t a_row = (uint32_t)(m0 + wave * C::NCA * 8 + (lane >> 3)) * r2 * 2u;
-  const float inv_r2 = 1.f / (float)r2;
+  const uint32_t a_row = (uint32_t)(m0 + wave * C::NCA * 8 + (lane >> 3)) * deep * 2u;
+  const float inv_deep = 1.f / (float)deep;
 #pragma unroll
   for (int i = 0; i < C::NCA; ++i) {  // its rows from anywhere
     const int rr = (wave * C::NCA + i) * 8 + (lane >> 3), ch = (lane & 7) ^ ((rr >> 1) & 7);
@@ -214,15 +214,18 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
       B.at(s, s < nst);
       return;
     }
-    A.rs = rsrc_of(a.g.pairs, 0x7fffffffu);
+    A.rs = rsrc_of(a.g.parts, 0x7fffffffu);
     B.rs = rsrc_of(a.g.weights, 0x7fffffffu);
     A.soff = B.soff = 0;
     const int k0 = (s - base) * BK;
-    // of column kx: its share q and value w (r2 - r.. are the remainders)
+    // of column kx: its share q and value w
     auto split_k = [&](int kx, int& q, int& w) {
-      q = (int)(((float)kx + 0.5f) * inv_r2);  // exact: kx < 2^16, r2 <= 2^8
-      w = kx - q * r2;
+      // exact: with kx < 2^17, deep < 2^9 and q <= 2^8 the product is off by less
+      // than 2^-14, its distance from a whole number at least 2^-10
+      q = (int)(((float)kx + 0.5f) * inv_deep);
+      w = kx - q * deep;
     };
+    auto rank_of = [&](int w) { return w < r ? w : w < 2 * r ? w - r : w - 2 * r; };
     // a lane's 16-byte piece of an even and of an odd copy's rows
     int q[2], w[2];
 #pragma unroll
@@ -230,14 +233,14 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
 #pragma unroll
     for (int i = 0; i < C::NCA; ++i) {
       const bool odd = (wave * C::NCA + i) & 1;
-      A.off[i] = my_share[i] == (odd ? q[1] : q[0]) ? a_row + (uint32_t)(i * 8 * r2 + (odd ? w[1] : w[0])) * 2u : kBufNone;
+      A.off[i] = my_share[i] == (odd ? q[1] : q[0]) ? a_row + (uint32_t)(i * 8 * deep + (odd ? w[1] : w[0])) * 2u : kBufNone;
     }
     if (B_KC) {
       uint32_t at_q[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         at_q[h] = kBufNone;
-        if (q[h] < shares) at_q[h] = ((uint32_t)adapter[q[h]] * N * r + (w[h] < r ? w[h] : w[h] - r)) * 2u;
+        if (q[h] < shares) at_q[h] = ((uint32_t)adapter[q[h]] * N * r + rank_of(w[h])) * 2u;
       }
 #pragma unroll
       for (int i = 0; i < C::NCB; ++i) {
@@ -252,7 +255,7 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
         const int k = (wave * C::NCB + i) * PER + lane / LPR, n = n0 + ((lane % LPR) ^ (4 * (k & 3))) * 8;
         int qk, wk;
         split_k(k0 + k, qk, wk);
-        B.off[i] = qk < shares && n < N ? (((uint32_t)adapter[qk] * r + (wk < r ? wk : wk - r)) * N + n) * 2u : kBufNone;
+        B.off[i] = qk < shares && n < N ? (((uint32_t)adapter[qk] * r + rank_of(wk)) * N + n) * 2u : kBufNone;
       }
     }
   };
@@ -441,7 +444,7 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
       // (with K split the shares' terms are added by the split that met them)
       if (mend && share[rr] >= 0) {
         const int64_t first = (int64_t)adapter[share[rr]] * N * r;
-        e = add_not_finite(e, a.g.pairs + (int64_t)(m0 + rr) * r2, a.g.weights + first + (BACK ? n : (int64_t)n * r),
+        e = add_not_finite(e, a.g.parts + (int64_t)(m0 + rr) * deep, a.g.weights + first + (BACK ? n : (int64_t)n * r),
                            BACK ? N : 1, BACK ? 1 : r, r);
       }
       const f32x4_t* v = e.v;
@@ -543,7 +546,7 @@ Plan plan_of(int T, int N, int K, bool joined_anyway) {
 
 // (two shares a tile: what a tile of several requests has)
 Plan plan_of(const ProjArgs& p, bool back) {
-  return plan_of(p.T, back ? p.K : p.N, (back ? p.N : p.K) + 4 * p.r, false);
+  return plan_of(p.T, back ? p.K : p.N, (back ? p.N : p.K) + 2 * kParts * p.r, false);
 }
 
 // x [W; A]^T.  Decode batches: Few32 up to 32 tokens, Few64 up to 256 and 256
@@ -590,6 +593,13 @@ int launch(TileArgs a, hipStream_t st) {
 }
 
 }  // namespace
+
+int proj_gemm_plan(int T, int K, int N, int r, bool back) {
+  ProjArgs p = {};
+  p.T = T, p.K = K, p.N = N, p.r = r;
+  const Plan f = plan_of(p, back);
+  return f.tile * 32 + f.splits;
+}
 
 size_t proj_gemm_slab_bytes(const ProjArgs& p, bool back) {
   const int s = plan_of(p, back).splits;

@@ -1,6 +1,6 @@
 // The adapters' gradients: dA_l = sum u[t] x[t]^T, dB_l = s_l sum dy[t] z[t]^T.
 //
-// Both are a few columns (u's or z's, as pairs 2r of them) against all columns
+// Both are a few columns (u's or z's, 3r of them as parts) against all columns
 // of x or dy, summed over the rows of one adapter: the wide side is read once
 // and bounds the product.  A workgroup takes 128 of its columns and one piece
 // of a run, 64 rows a stage, gathered on their way into LDS; both sides have
@@ -28,20 +28,25 @@ struct GradArgs {
   int slabs;            // at most
 };
 
-// NB: blocks of 32 narrow columns, the values in the first half, the
-// remainders in the second.
-template <int NB>
+// PW: columns of a narrow row's part, 16 or a multiple of 32.
+template <int PW>
 struct Grad {
+  // Blocks of 32 narrow columns.  The values rounded have blocks of their own,
+  // half of one with PW = 16, where the other two parts share the next.
+  static constexpr int NB = PW == 16 ? 2 : 3 * PW / 32;
   static constexpr int ROWB = NB * 64;                      // bytes of a narrow LDS row
   static constexpr int WIDE = BK * WT * 2, STAGE = WIDE + BK * ROWB;
-  static constexpr int RING = NB <= 2 ? 3 : 2;
+  static constexpr int RING = NB <= 2 ? 3 : 2;              // (two workgroups on a CU up to PW = 32)
   static constexpr int NC = WIDE / 1024 / NW + NB;          // copies of a wavefront and stage
   static constexpr int LDS = RING * STAGE + kMostRows * 4;
   // 64-byte parts of a narrow row are swizzled so that the four rows that a
   // transposing read takes side by side lie in different banks
   static __device__ __forceinline__ int swizzle(int k) {
-    return NB >= 4 ? 64 * (k & 3) : NB == 2 ? 64 * ((k >> 1) & 1) : 0;
+    return ROWB % 256 == 0 ? 64 * (k & 3) : ROWB % 128 == 0 ? 64 * ((k >> 1) & 1) : 0;
   }
+  // of an LDS row's column: its part, and which of the part's; a part's first
+  static __device__ __forceinline__ int part_of(int col) { return PW == 16 ? (col + 16) / 32 : col / PW; }
+  static constexpr int first(int part) { return PW == 16 ? part * 16 + (part > 0) * 16 : part * PW; }
 };
 
 __device__ __forceinline__ u32x4_t transposed(const char* p, int four_rows) {
@@ -51,9 +56,10 @@ __device__ __forceinline__ u32x4_t transposed(const char* p, int four_rows) {
   return u32x4_t{a.x, a.y, b.x, b.y};
 }
 
-template <int NB>
-__global__ __launch_bounds__(NT, NB <= 2 ? 2 : 1) void proj_grads_kernel(GradArgs a) {
-  typedef Grad<NB> C;
+template <int PW>
+__global__ __launch_bounds__(NT, PW <= 32 ? 2 : 1) void proj_grads_kernel(GradArgs a) {
+  typedef Grad<PW> C;
+  constexpr int NB = C::NB;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   int* token = reinterpret_cast<int*>(smem + C::RING * C::STAGE);
   const ProjArgs& p = a.p;
@@ -63,7 +69,7 @@ __global__ __launch_bounds__(NT, NB <= 2 ? 2 : 1) void proj_grads_kernel(GradArg
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool is_a = (int)blockIdx.x < a.tiles_a;
   const int w0 = ((int)blockIdx.x - (is_a ? 0 : a.tiles_a)) * WT;
-  const int width = is_a ? p.K : p.N, r = p.r, r2 = 2 * r;
+  const int width = is_a ? p.K : p.N, r = p.r;
   const u32x4_t rw = rsrc_of(is_a ? a.g.x : a.g.dy, 0x7fffffffu);
   const u32x4_t rn = rsrc_of(is_a ? a.g.us : a.g.zs, 0x7fffffffu);
   for (int i = threadIdx.x; i < item.n; i += NT) token[i] = p.o.perm[item.row + i];
@@ -85,9 +91,9 @@ __global__ __launch_bounds__(NT, NB <= 2 ? 2 : 1) void proj_grads_kernel(GradArg
       constexpr int i = decltype(i_c)::value;
       const int at = (wave * NB + i) * 1024 + lane * 16, k = at / C::ROWB;
       const int col = ((at % C::ROWB) ^ C::swizzle(k)) / 2;       // of the LDS row
-      const int j = col < NB * 16 ? col : col - NB * 16, m = s * BK + k;
-      const uint32_t off = m < item.n && j < r
-                               ? ((uint32_t)(item.row + m) * r2 + j + (col < NB * 16 ? 0 : r)) * 2u : kBufNone;
+      const int part = C::part_of(col), j = col - C::first(part), m = s * BK + k;
+      const uint32_t off = m < item.n && j >= 0 && j < r
+                               ? ((uint32_t)((item.row + m) * kParts + part) * (uint32_t)r + j) * 2u : kBufNone;
       copy16<i * 1024>(rn, to + C::WIDE + wave * (NB * 1024), off, 0);
     });
   };
@@ -127,16 +133,19 @@ __global__ __launch_bounds__(NT, NB <= 2 ? 2 : 1) void proj_grads_kernel(GradArg
   __builtin_amdgcn_s_waitcnt(wait_vm0);  // no copy outlives the workgroup
 
   // element 4 q + i of the blocks: narrow column 8 q + 4 (l / 32) + i, wide
-  // column l % 32; a value's remainder lies 2 NB groups on
+  // column l % 32; of a value its three parts' sums
   const int c = w0 + wave * 32 + (lane & 31), kh = lane >> 5;
   if (c >= width) return;
 #pragma unroll
-  for (int q = 0; q < 2 * NB; ++q) {
+  for (int q = 0; q < PW / 8; ++q) {
     const int j = 8 * q + 4 * kh;
     if (8 * q >= r) break;
+    constexpr int MID = C::first(1) / 8, LOW = C::first(2) / 8;
     f32x4_t v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = acc[q / 4][q % 4 * 4 + i] + acc[(q + 2 * NB) / 4][(q + 2 * NB) % 4 * 4 + i];
+    for (int i = 0; i < 4; ++i)
+      v[i] = acc[q / 4][q % 4 * 4 + i] +
+             (acc[(q + MID) / 4][(q + MID) % 4 * 4 + i] + acc[(q + LOW) / 4][(q + LOW) % 4 * 4 + i]);
     if (item.slab >= 0) {
       if (is_a) {
         float* to = a.g.slabs + ((int64_t)item.slab * r + j) * width + c;
@@ -177,15 +186,15 @@ __global__ __launch_bounds__(256) void proj_grads_join_kernel(GradArgs a) {
   }
 }
 
-template <int NB>
+template <int PW>
 int launch_cfg(const GradArgs& a, hipStream_t st) {
   static std::atomic<uint64_t> attr_done;
-  const void* fn = reinterpret_cast<const void*>(&proj_grads_kernel<NB>);
-  const int rc = ensure_dynamic_lds(fn, Grad<NB>::LDS, attr_done);
+  const void* fn = reinterpret_cast<const void*>(&proj_grads_kernel<PW>);
+  const int rc = ensure_dynamic_lds(fn, Grad<PW>::LDS, attr_done);
   if (rc) return rc;
   const int tiles = a.tiles_a + (a.g.dB ? (a.p.N + WT - 1) / WT : 0);
   const dim3 grid(tiles, (unsigned)proj_grad_items(a.p));
-  proj_grads_kernel<NB><<<grid, NT, Grad<NB>::LDS, st>>>(a);
+  proj_grads_kernel<PW><<<grid, NT, Grad<PW>::LDS, st>>>(a);
   return hipGetLastError() == hipSuccess ? MOE_LORA_OK : MOE_LORA_EHIP;
 }
 
@@ -209,8 +218,8 @@ size_t proj_grad_slab_bytes(const ProjArgs& p) {
 
 int launch_proj_grads(const ProjArgs& p, const ProjGrads& g, hipStream_t st) {
   const GradArgs a{p, g, g.dA ? (p.K + WT - 1) / WT : 0, slabs_of(p.T, p.grad_rows)};
-  const int rc = p.r <= 16 ? launch_cfg<1>(a, st) : p.r <= 32 ? launch_cfg<2>(a, st)
-                 : p.r <= 64 ? launch_cfg<4>(a, st) : launch_cfg<8>(a, st);
+  const int rc = p.r <= 16 ? launch_cfg<16>(a, st) : p.r <= 32 ? launch_cfg<32>(a, st)
+                 : p.r <= 64 ? launch_cfg<64>(a, st) : launch_cfg<128>(a, st);
   if (rc || p.T <= p.grad_rows) return rc;  // no run has several pieces
   const int64_t pieces = ((int64_t)(g.dA ? p.K : 0) + (g.dB ? p.N : 0)) * p.r / 8;
   const dim3 grid((unsigned)std::min<int64_t>(64, (pieces + 255) / 256), p.L);

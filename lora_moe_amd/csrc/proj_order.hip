@@ -168,8 +168,7 @@ __global__ __launch_bounds__(kThreads) void proj_order_kernel(ProjArgs p, float*
       float v[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) v[q] = s * (q < 4 ? a[q & 3] : b[q & 3]);
-      uint16_t* to = zs + (int64_t)place[t] * 2 * p.r + j;
-      store8_pair(to, to + p.r, v);
+      store8_three(zs + (int64_t)place[t] * kParts * p.r + j, p.r, v);
     }
   }
 }

@@ -26,7 +26,7 @@ struct ShrinkArgs {
   ProjArgs p;
   const uint16_t* in;  // [T][K]
   const uint16_t* w;   // KC: [L][r][K], else [L][K][r]
-  uint16_t* pairs;
+  uint16_t* parts;
   float* z;
   int K;
 };
@@ -163,8 +163,10 @@ __global__ __launch_bounds__(shrink_threads(NB)) void proj_shrink_kernel(ShrinkA
       if (m0 + e >= item.n) continue;
       const int64_t row = item.row + m0 + e;
       if (a.z) a.z[(int64_t)p.o.perm[row] * r + j] = v[e];
-      uint16_t* to = a.pairs + row * 2 * r + j;
-      f32_to_bf16_pair(s * v[e], to, to + r);
+      uint16_t part[kParts];
+      f32_to_bf16_three(s * v[e], part);
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) a.parts[(row * kParts + k) * r + j] = part[k];
     }
   }
 }
@@ -198,9 +200,9 @@ int launch(const ShrinkArgs& a, hipStream_t st) {
 
 }  // namespace
 
-int launch_proj_shrink(const ProjArgs& p, bool back, const uint16_t* in, const uint16_t* weights, uint16_t* pairs,
+int launch_proj_shrink(const ProjArgs& p, bool back, const uint16_t* in, const uint16_t* weights, uint16_t* parts,
                        float* z, hipStream_t st) {
-  const ShrinkArgs a{p, in, weights, pairs, z, back ? p.N : p.K};
+  const ShrinkArgs a{p, in, weights, parts, z, back ? p.N : p.K};
   return back ? launch<false>(a, st) : launch<true>(a, st);
 }
 
