@@ -61,25 +61,6 @@ struct SliceCfg : FfnCfg<BM, BN, WM, WN> {
 template <class C, int RING>
 constexpr int tile_lds() { return RING * C::STAGE + (2 * C::BM + std::max(C::BM, 64)) * 4 + 16; }
 
-// Bits 15 and 31 of the result: whether one of the two bf16 of a word of v is an
-// infinity or NaN (the exponent's ones carry into the sign's place).
-__device__ __forceinline__ uint32_t not_finite_bits(u32x4_t v) {
-  uint32_t b = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) b |= (v[i] & 0x7f807f80u) + 0x00800080u;
-  return b;
-}
-
-// such values to 0
-__device__ __forceinline__ u32x4_t only_finite(u32x4_t v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if ((v[i] & 0x7f80u) == 0x7f80u) v[i] &= 0xffff0000u;
-    if ((v[i] & 0x7f800000u) == 0x7f800000u) v[i] &= 0xffffu;
-  }
-  return v;
-}
-
 // The terms of a row that only_finite took out, for 8 neighbouring outputs.
 // z: the row's parts; w: the adapter's weight of the first output and rank 0,
 // `rank` apart along the rank and `out` along the outputs.

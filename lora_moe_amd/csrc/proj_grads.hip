@@ -7,7 +7,9 @@
 // their output index contiguous and are transposed on the way to registers
 // (ds_read_b64_tr_b16).  An adapter without tokens is an empty piece.  A run of
 // several pieces puts fp32 sums into slabs, which a second kernel adds in their
-// order.  8192 tokens, 4096 x 4096, rank 16: 27 us (152 MB at 5.4 TB/s) and 5 for
+// order.  What is left of a value behind its first part may be 0 or of the other
+// sign, so an infinity or NaN of x or dy meets the first part alone, whose
+// product with it is the value's; the others meet 0 there.  8192 tokens, 4096 x 4096, rank 16: 27 us (152 MB at 5.4 TB/s) and 5 for
 // the slabs; 1001 tokens, 2880 x 2880, rank 32: 8 us.
 #include "internal.h"
 #include "proj.h"
@@ -33,7 +35,7 @@ template <int PW>
 struct Grad {
   // Blocks of 32 narrow columns.  The values rounded have blocks of their own,
   // half of one with PW = 16, where the other two parts share the next.
-  static constexpr int NB = PW == 16 ? 2 : 3 * PW / 32;
+  static constexpr int NB = PW == 16 ? 2 : 3 * PW / 32, FIRST = PW == 16 ? 1 : PW / 32;
   static constexpr int ROWB = NB * 64;                      // bytes of a narrow LDS row
   static constexpr int WIDE = BK * WT * 2, STAGE = WIDE + BK * ROWB;
   static constexpr int RING = NB <= 2 ? 3 : 2;              // (two workgroups on a CU up to PW = 32)
@@ -120,11 +122,14 @@ __global__ __launch_bounds__(NT, PW <= 32 ? 2 : 1) void proj_grads_kernel(GradAr
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       const u32x4_t wide = Operand<false, WT, 1, false>::frag(at, wave * 32, 0, kk);
+      u32x4_t finite = wide;
+      if (__ballot(not_finite_bits(wide) & 0x80008000u)) finite = only_finite(wide);
       const int k = kk * 16 + 8 * (g >> 1) + sub;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int col = ((b * 32 + (g & 1) * 16) * 2 + (lane & 3) * 8) ^ C::swizzle(k);
-        acc[b] = mfma_32x32x16(transposed(at + C::WIDE + k * C::ROWB + col, 4 * C::ROWB), wide, acc[b]);
+        acc[b] = mfma_32x32x16(transposed(at + C::WIDE + k * C::ROWB + col, 4 * C::ROWB), b < C::FIRST ? wide : finite,
+                              acc[b]);
       }
     }
     __builtin_amdgcn_s_waitcnt(wait_lgkm0);

@@ -172,6 +172,25 @@ __device__ __forceinline__ void bare_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// Bits 15 and 31 of the result: whether one of the two bf16 of a word of v is an
+// infinity or NaN (the exponent's ones carry into the sign's place).
+__device__ __forceinline__ uint32_t not_finite_bits(u32x4_t v) {
+  uint32_t b = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b |= (v[i] & 0x7f807f80u) + 0x00800080u;
+  return b;
+}
+
+// such values to 0
+__device__ __forceinline__ u32x4_t only_finite(u32x4_t v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((v[i] & 0x7f80u) == 0x7f80u) v[i] &= 0xffff0000u;
+    if ((v[i] & 0x7f800000u) == 0x7f800000u) v[i] &= 0xffffu;
+  }
+  return v;
+}
+
 __device__ __forceinline__ void store8(uint16_t* p, const float* v) {
   u32x4_t o;
 #pragma unroll

@@ -119,3 +119,49 @@ def test_backward_keeps_all_bits_of_u_and_z(T, N, K, L, r):
         same(dA[l], u[at].T @ x[at], f"dA {l}")
         # (the large values of dy are not for here)
         same(dB[l, 4:], dy[at][:, 4:].T @ (s * z)[at], f"dB {l}")
+
+
+@pytest.mark.parametrize("T,L", [(90, 6), (1500, 2)])
+@pytest.mark.parametrize("r", [8, 24, 64, 128])
+def test_gradients_of_rows_that_are_not_finite(T, L, r):
+    """An infinity of x or dy is in the gradients what the formula makes of it,
+    whether the values that it meets take one bf16 or three."""
+    K, N, inf = 72, 136, float("inf")
+    g = torch.Generator().manual_seed(r)
+    r16 = lambda *s: torch.randn(s, generator=g).bfloat16()  # noqa: E731
+    x, dy, W, A, B = r16(T, K), r16(T, N), r16(N, K), r16(L, r, K), r16(L, N, r)
+    z = torch.randn((T, r), generator=g)
+    z[:, ::2] = (4 * z[:, ::2]).round() + 0.5  # (a bf16 each, and no 0)
+    ids = (torch.arange(T) % L).int()
+    shape = lm.make_proj_shape(T, K, N, L, r)
+    ws = lm.alloc_proj_workspace(shape)
+
+    def run(x, dy, **want):
+        out = {n: torch.empty_like(t, device="cuda") for n, t in want.items()}
+        lm.moe_lora_proj_backward(shape, dy.cuda(), x.cuda(), ids.cuda(), z.cuda(), W.cuda(), A.cuda(), B.cuda(), ws, **out)
+        return [t.cpu() for t in out.values()]
+
+    dA, dB = run(x, dy, dA=A, dB=B)
+    u = own(dy.double(), B.double().transpose(1, 2), ids)
+    sure = u.abs() > 1e-2  # (its sum in fp32 has this one's sign)
+    x2, dy2 = x.clone(), dy.clone()
+    a, b, c = L, 3 * L + 1, 4 * L + 1  # tokens of adapters 0 and 1
+    x2[a, 5], x2[b, 7], x2[c, 7], x2[b, 11] = inf, -inf, -inf, float("nan")
+    dA2, = run(x2, dy, dA=A)
+    assert torch.equal(dA2[0][sure[a], 5], u[a][sure[a]].sign().float().mul(inf).bfloat16())
+    two = sure[b] & sure[c]
+    for j in torch.nonzero(two).flatten().tolist():
+        want = float(-inf * u[b, j].sign() - inf * u[c, j].sign())
+        assert torch.equal(dA2[1][j, 7].float(), torch.tensor(want)) or (want != want and bool(dA2[1][j, 7].isnan()))
+    assert bool(dA2[1][:, 11].isnan().all())
+    dA2[0][:, 5], dA2[1][:, 7], dA2[1][:, 11] = dA[0][:, 5], dA[1][:, 7], dA[1][:, 11]
+    assert torch.equal(dA2, dA)
+    dy2[a, 9], dy2[b, 100] = -inf, inf
+    dB2, = run(x, dy2, dB=B)
+    assert torch.equal(dB2[0][9], z[a].sign().mul(-inf).bfloat16())
+    assert torch.equal(dB2[1][100], z[b].sign().mul(inf).bfloat16())
+    dB2[0][9], dB2[1][100] = dB[0][9], dB[1][100]
+    assert torch.equal(dB2, dB)
+    z[a] = inf  # and infinities of both
+    dB3, = run(x, dy2, dB=B)
+    assert torch.equal(dB3[0][9], torch.full((r,), -inf, dtype=torch.bfloat16))
