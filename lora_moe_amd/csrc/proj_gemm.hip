@@ -14,8 +14,9 @@
 //
 // Zeros times an infinity or NaN would carry one adapter's broken weights into
 // another request's rows.  So the adapters' weights go into the products with
-// 0 in place of such values, and a tile that met one adds their terms to the
-// rows that they belong to, one by one, in its epilogue.
+// 0 in place of such values, and so do the rows' own in that slice of K, and a
+// tile that met one adds the terms of both to the rows that they belong to, one
+// by one, in its epilogue.
 //
 // The loop is that of ffn_gemm.hip, with a ring of two to four slots: filled by
 // asynchronous copies that go out between the MFMAs of the stage before.  The
@@ -61,7 +62,10 @@ struct SliceCfg : FfnCfg<BM, BN, WM, WN> {
 template <class C, int RING>
 constexpr int tile_lds() { return RING * C::STAGE + (2 * C::BM + std::max(C::BM, 64)) * 4 + 16; }
 
-// The terms of a row that only_finite took out, for 8 neighbouring outputs.
+// The terms of a row that only_finite took out, for 8 neighbouring outputs: those
+// of which a factor is not finite.  Some may be in the sum already (a tile's
+// wavefronts and K splits take out what they meet themselves); such a term is an
+// infinity or NaN, and once more of it changes nothing.
 // z: the row's parts; w: the adapter's weight of the first output and rank 0,
 // `rank` apart along the rank and `out` along the outputs.
 struct Eight {
@@ -74,7 +78,8 @@ __device__ __noinline__ Eight add_not_finite(Eight e, const uint16_t* z, const u
     float s = e.v[q >> 2][q & 3];
     for (int j = 0; j < r; ++j) {
       const uint16_t b = w[j * rank + q * out];
-      if ((b & 0x7f80u) == 0x7f80u) s += (bf16_to_f32(z[j]) + bf16_to_f32(z[r + j]) + bf16_to_f32(z[2 * r + j])) * bf16_to_f32(b);
+      if ((b & 0x7f80u) == 0x7f80u || (z[j] & 0x7f80u) == 0x7f80u)
+        s += (bf16_to_f32(z[j]) + bf16_to_f32(z[r + j]) + bf16_to_f32(z[2 * r + j])) * bf16_to_f32(b);
     }
     e.v[q >> 2][q & 3] = s;
   }
@@ -271,6 +276,8 @@ __global__ __launch_bounds__(C::NT, 2) void proj_tile_kernel(TileArgs a) {
         bad = true;
 #pragma unroll
         for (int j = 0; j < NI; ++j) bf[set][j] = only_finite(bf[set][j]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) af[set][i] = only_finite(af[set][i]);  // (an infinity times the 0 would be NaN)
       }
     }
     for_each<NM>([&](auto n_c) __attribute__((always_inline)) {
