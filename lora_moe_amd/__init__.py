@@ -553,6 +553,18 @@ def _check_tensors(specs) -> None:
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
+def _address(name, t):
+    """Device address of an operand that may be left out (None).  One without
+    memory (a fake tensor, torch's zeros that are none) has the address 0 and
+    would pass for left out."""
+    if t is None:
+        return None
+    p = t.data_ptr()
+    if not p and t.numel():
+        raise ValueError(f"{name} has no memory")
+    return p
+
+
 def _allocated_on(stream, make, returned=False):
     """What make() allocates, as memory of ``stream``: the allocator hands a
     block of one stream to the next user in that stream's order alone, so
@@ -614,7 +626,7 @@ def moe_lora_ffn_forward(shape, x, W_gu, W_down, workspace, y, gu=None, stream=N
     _check_tensors(specs)
     _check("moe_lora_ffn_forward", load_library().moe_lora_ffn_forward(
         ctypes.byref(shape), x.data_ptr(), W_gu.data_ptr(), W_down.data_ptr(),
-        None if gu is None else gu.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _address("gu", gu), workspace.data_ptr(), workspace.numel(),
         y.data_ptr(), _stream(stream)))
 
 
@@ -634,7 +646,7 @@ def moe_lora_ffn_backward(shape, dy, x, gu, W_gu, W_down, workspace, dx=None, dW
     _check("moe_lora_ffn_backward", load_library().moe_lora_ffn_backward(
         ctypes.byref(shape), dy.data_ptr(), x.data_ptr(), gu.data_ptr(), W_gu.data_ptr(),
         W_down.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        *[None if t is None else t.data_ptr() for _, t, _ in outs], _stream(stream)))
+        *[_address(n, t) for n, t, _ in outs], _stream(stream)))
 
 
 def gated_ffn(x, W_gu, W_down, act="silu", workspace=None, y=None, stream=None):
@@ -699,7 +711,7 @@ def moe_lora_w4_pack(q, scales, zeros=None, group=128, stream=None) -> W4Weight:
     w.desc.data = w.packed.data_ptr()
     _check("moe_lora_w4_pack", load_library().moe_lora_w4_pack(
         ctypes.byref(w.desc), q.data_ptr(), scales.data_ptr(),
-        None if zeros is None else zeros.data_ptr(), w.packed.data_ptr(), n, _stream(stream)))
+        _address("zeros", zeros), w.packed.data_ptr(), n, _stream(stream)))
     return w
 
 
@@ -853,7 +865,7 @@ def _run(func, shape, args, stream, workspace=None) -> None:
                 specs.append(_check_workspace(a[1], workspace[0](), workspace[1]))
         _check_tensors(specs)
         # as it should be after all (a tensor that DLPack does not take)
-        ptrs = [None if a is None else a[1].data_ptr() for a in args]
+        ptrs = [None if a is None else _address(a[0], a[1]) for a in args]
         for i, a in enumerate(args):
             if a is not None and a[2] is None:
                 ptrs[i + 1] = a[1].numel()

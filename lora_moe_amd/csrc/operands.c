@@ -4,7 +4,7 @@
  * the shape structure (a buffer) and the function's further arguments: None
  * (a null pointer), an int, or a tuple (name, tensor, sizes, type) for a
  * tensor's address.  Every tensor has to have those sizes and that type (torch's
- * name of it), to be contiguous and to lie on the given HIP device.  Sizes None:
+ * name of it), to be contiguous and to lie in memory of the given HIP device.  Sizes None:
  * a workspace, one-dimensional, whose bytes are the next argument.  It returns
  * the function's status, or None, without having called it, when something is
  * not so: the caller then finds out what, at leisure, and says it.
@@ -49,16 +49,16 @@ static int address_of(PyObject* spec, int device, uintptr_t* out) {
     for (int i = 0; i < t.ndim; ++i)
       if (PyLong_AsLongLong(PyTuple_GET_ITEM(sizes, i)) != t.shape[i]) return 0;
   }
-  if (t.strides) {
-    int64_t n = 1;
-    int empty = 0, dense = 1;
-    for (int i = t.ndim - 1; i >= 0; --i) {
-      if (t.shape[i] == 0) empty = 1;
-      if (t.shape[i] != 1 && t.strides[i] != n) dense = 0;
-      n *= t.shape[i];
-    }
-    if (!dense && !empty) return 0;
+  int64_t n = 1;
+  int empty = 0, dense = 1;
+  for (int i = t.ndim - 1; i >= 0; --i) {
+    if (t.shape[i] == 0) empty = 1;
+    if (t.strides && t.shape[i] != 1 && t.strides[i] != n) dense = 0;
+    n *= t.shape[i];
   }
+  /* a tensor without memory (torch's zeros that are none, fake tensors) would
+   * pass for an argument that is not given */
+  if (!empty && (!dense || !t.data)) return 0;
   *out = (uintptr_t)t.data + t.byte_offset;
   return 1;
 }
