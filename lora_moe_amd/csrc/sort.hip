@@ -271,9 +271,15 @@ __global__ __launch_bounds__(kThreads) void unsort_backward_kernel(BackArgs p) {
             __builtin_nontemporal_store(X::store(v), p.out + (int64_t)r[j] * p.pieces + c);
           }
           if (p.dw) {
+            // a piece's products in pairs, so that few sums follow one another
             X::load(q[j], v);
 #pragma unroll
-            for (int n = 0; n < X::N; ++n) dot[j] = fmaf(y[n], v[n], dot[j]);
+            for (int n = 0; n < X::N; n += 2) v[n] = fmaf(y[n + 1], v[n + 1], y[n] * v[n]);
+#pragma unroll
+            for (int h = 2; h < X::N; h *= 2)
+#pragma unroll
+              for (int n = 0; n < X::N; n += 2 * h) v[n] += v[n + h];
+            dot[j] += v[0];
           }
         }
       }
