@@ -826,7 +826,7 @@ def moe_lora_clip_grads(grads, max_norm: float, norm, stream=None) -> None:
 # ------------------------------------------------------------------ tokens to their experts and back
 
 _ROW_TYPES = {MOE_LORA_F32: "float32", MOE_LORA_BF16: "bfloat16", MOE_LORA_F16: "float16"}
-_functions = {}  # the library's: address and type of the shape
+_functions = {}  # the library's: address, type of the shape, kind
 _native = None   # the _operands module
 
 
@@ -844,12 +844,12 @@ def _run(func, shape, args, stream, workspace=None) -> None:
         except ImportError as e:
             raise RuntimeError(f"lora_moe_amd._operands: {e}; build it first "
                                "(python -c 'import __graft_entry__ as g; g.build()')") from e
-        _native = (_operands.call, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
-    call, device, raw_stream = _native
+        _native = (_operands.call, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, _operands.kinds)
+    call, device, raw_stream, kinds = _native
     f = _functions.get(func)
     if f is None:
         c = getattr(load_library(), func)
-        f = _functions[func] = (ctypes.cast(c, ctypes.c_void_p).value, c.argtypes[0]._type_)
+        f = _functions[func] = (ctypes.cast(c, ctypes.c_void_p).value, c.argtypes[0]._type_, kinds[func])
     if not isinstance(shape, f[1]):  # (others have fields of the same names)
         raise TypeError(f"shape: {type(shape).__name__}, expected {f[1].__name__}")
     first = args[0][1]
@@ -857,7 +857,7 @@ def _run(func, shape, args, stream, workspace=None) -> None:
     if first is not None and first.is_cuda:
         dev = device()
         handle = raw_stream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
-        code = call(f[0], shape, (*args, handle), dev)
+        code = call(f[0], shape, (*args, handle), dev, f[2])
     if code is None:
         specs = [a for a in args if a is not None and a[2] is not None]
         for a in args:

@@ -54,7 +54,8 @@ def build_operands() -> str:
     if cc is None:
         raise RuntimeError("no C compiler for operands.c")
     tmp = OPERANDS + ".tmp%d" % os.getpid()
-    r = subprocess.run([cc, "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I",
+    r = subprocess.run([cc, "-O2", "-Wall", "-shared", "-fPIC", "-I", os.path.join(ROOT, "include"), "-I",
+                        sysconfig.get_paths()["include"], "-I",
                         os.path.join(os.path.dirname(torch.__file__), "include"),
                         os.path.join(CSRC, "operands.c"), "-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:

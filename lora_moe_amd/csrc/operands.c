@@ -1,7 +1,8 @@
 /* A library call from Python with its tensors looked at on the way.
  *
- * call(function, shape, args, device) takes the address of a library function,
- * the shape structure (a buffer) and the function's further arguments: None
+ * call(function, shape, args, device, kind) takes the address of a library
+ * function, the shape structure (a buffer), which function it is (kinds[name];
+ * left out: one that takes 17 pointers) and its further arguments: None
  * (a null pointer), an int, or a tuple (name, tensor, sizes, type) for a
  * tensor's address.  Every tensor has to have those sizes and that type (torch's
  * name of it), to be contiguous and to lie in memory of the given HIP device.  Sizes None:
@@ -19,7 +20,43 @@
 
 #include <ATen/dlpack.h>
 
+#include "moe_lora.h"
+
 enum { MOST = 16 };
+
+/* The functions by kind, and their arguments behind the shape: each is called
+ * through its own type. */
+enum { SORT, SORT_BACKWARD, UNSORT, UNSORT_BACKWARD, ROUTE_BACKWARD, PROJ_FORWARD, PROJ_BACKWARD, KINDS };
+static const struct {
+  const char* name;
+  int args;
+} functions[KINDS] = {{"moe_lora_sort", 9},           {"moe_lora_sort_backward", 4},  {"moe_lora_unsort", 5},
+                      {"moe_lora_unsort_backward", 7}, {"moe_lora_route_backward", 5}, {"moe_lora_proj_forward", 11},
+                      {"moe_lora_proj_backward", 14}};
+
+typedef int (*pointers17)(const void*, void*, void*, void*, void*, void*, void*, void*, void*, void*, void*, void*,
+                          void*, void*, void*, void*, void*);
+
+static int run(int kind, uintptr_t f, const void* s, const uintptr_t* a) {
+#define P(i) ((void*)a[i])
+#define F(name) ((__typeof__(&name))f)
+  switch (kind) {
+    case SORT: return F(moe_lora_sort)(s, P(0), P(1), P(2), a[3], P(4), P(5), P(6), P(7), P(8));
+    case SORT_BACKWARD: return F(moe_lora_sort_backward)(s, P(0), P(1), P(2), P(3));
+    case UNSORT: return F(moe_lora_unsort)(s, P(0), P(1), P(2), P(3), P(4));
+    case UNSORT_BACKWARD: return F(moe_lora_unsort_backward)(s, P(0), P(1), P(2), P(3), P(4), P(5), P(6));
+    case ROUTE_BACKWARD: return F(moe_lora_route_backward)(s, P(0), P(1), P(2), P(3), P(4));
+    case PROJ_FORWARD:
+      return F(moe_lora_proj_forward)(s, P(0), P(1), P(2), P(3), P(4), P(5), P(6), P(7), a[8], P(9), P(10));
+    case PROJ_BACKWARD:
+      return F(moe_lora_proj_backward)(s, P(0), P(1), P(2), P(3), P(4), P(5), P(6), P(7), P(8), a[9], P(10), P(11),
+                                       P(12), P(13));
+  }
+  return ((pointers17)f)(s, P(0), P(1), P(2), P(3), P(4), P(5), P(6), P(7), P(8), P(9), P(10), P(11), P(12), P(13),
+                         P(14), P(15));
+#undef F
+#undef P
+}
 
 static const DLPackExchangeAPI* api;
 
@@ -65,16 +102,17 @@ static int address_of(PyObject* spec, int device, uintptr_t* out) {
 
 static PyObject* call(PyObject* self, PyObject* const* argv, Py_ssize_t argc) {
   (void)self;
-  if (argc != 4 || !PyTuple_Check(argv[2])) {
-    PyErr_SetString(PyExc_TypeError, "call(function, shape, args, device)");
+  if ((argc != 4 && argc != 5) || !PyTuple_Check(argv[2])) {
+    PyErr_SetString(PyExc_TypeError, "call(function, shape, args, device, kind)");
     return NULL;
   }
   const uintptr_t f = (uintptr_t)PyLong_AsUnsignedLongLong(argv[0]);
   const long device = PyLong_AsLong(argv[3]);
   const Py_ssize_t n = PyTuple_GET_SIZE(argv[2]);
+  const long kind = argc == 5 ? PyLong_AsLong(argv[4]) : KINDS;
   if (PyErr_Occurred()) return NULL;
-  if (n >= MOST) {
-    PyErr_SetString(PyExc_TypeError, "call: too many arguments");
+  if (kind < 0 || kind > KINDS || (kind < KINDS ? n != functions[kind].args : n >= MOST)) {
+    PyErr_SetString(PyExc_TypeError, "call: no such function, or not as many arguments as it takes");
     return NULL;
   }
   uintptr_t a[MOST] = {0};
@@ -96,11 +134,7 @@ static PyObject* call(PyObject* self, PyObject* const* argv, Py_ssize_t argc) {
   if (PyObject_GetBuffer(argv[1], &shape, PyBUF_SIMPLE)) return NULL;
   int rc;
   Py_BEGIN_ALLOW_THREADS
-  /* all of a function's arguments are pointers or sizes; those behind its own
-   * are not looked at */
-  rc = ((int (*)(const void*, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t,
-                 uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t, uintptr_t))f)(
-      shape.buf, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10], a[11], a[12], a[13], a[14], a[15]);
+  rc = run((int)kind, f, shape.buf, a);
   Py_END_ALLOW_THREADS
   PyBuffer_Release(&shape);
   return PyLong_FromLong(rc);
@@ -122,5 +156,16 @@ PyMODINIT_FUNC PyInit__operands(void) {
     PyErr_SetString(PyExc_ImportError, "torch's DLPack exchange functions are of another version");
     return NULL;
   }
-  return PyModule_Create(&module);
+  PyObject *m = PyModule_Create(&module), *kinds = PyDict_New();
+  for (int i = 0; kinds && i < KINDS; ++i) {
+    PyObject* v = PyLong_FromLong(i);
+    if (!v || PyDict_SetItemString(kinds, functions[i].name, v)) Py_CLEAR(kinds);
+    Py_XDECREF(v);
+  }
+  if (!m || !kinds || PyModule_AddObject(m, "kinds", kinds)) {  /* (takes kinds over where it succeeds) */
+    Py_XDECREF(kinds);
+    Py_XDECREF(m);
+    return NULL;
+  }
+  return m;
 }
