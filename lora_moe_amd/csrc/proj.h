@@ -85,9 +85,11 @@ struct ProjGemm {
   int32_t* place;  // [64] of a token's adapter among those met (launch_proj_both)
 };
 size_t proj_gemm_slab_bytes(const ProjArgs& p, bool back);
-// Its tile (0 to 3: 256 x 256, 128 x 128, the same in two groups, 64 x 128) times
-// 32 plus its K splits, for tests that have to meet all of them.
+// Its tile (0 to 4: 256 x 256, 128 x 128, the same in two groups, 64 x 128, 32 x
+// 64) times 32 plus its K splits, for tests that have to meet all of them; and
+// those of launch_proj_both.
 int proj_gemm_plan(int T, int K, int N, int r, bool back);
+int proj_both_plan(int T, int K, int N, int L, int r);
 int launch_proj_gemm(const ProjArgs& p, bool back, ProjGemm g, hipStream_t st);
 
 // dA and dB (either may be NULL)

@@ -589,6 +589,13 @@ int proj_gemm_plan(int T, int K, int N, int r, bool back) {
   return f.tile * 32 + f.splits;
 }
 
+int proj_both_plan(int T, int K, int N, int L, int r) {
+  ProjArgs p = {};
+  p.T = T, p.K = K, p.N = N, p.L = L, p.r = r;
+  const Plan f = plan_both(p);
+  return f.tile * 32 + f.splits;
+}
+
 size_t proj_gemm_slab_bytes(const ProjArgs& p, bool back) {
   const int s = plan_of(p, back).splits;
   return s > 1 ? (size_t)s * p.T * (back ? p.K : p.N) * sizeof(float) : 0;
