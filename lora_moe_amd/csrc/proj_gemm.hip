@@ -540,10 +540,14 @@ Plan plan_of(const ProjArgs& p, bool back) {
 // x [W; A]^T.  Decode batches: Few32 up to 32 tokens, Few64 up to 256 and 256
 // tiles (201 tokens, 2880 x 2880: 18.5 us, 24 with Deep; 4096 x 11008, 352
 // tiles: 59 and 52), with as many K splits as pay (0.2 us a stage; a split costs
-// its start and its slab), up to about a workgroup per CU.  Measured, us, 16
-// adapters of rank 16 with Few32 and the join, by splits 1, 2, 3, 4, 6: one
-// token, 4096 x 4096, 17.8, 13.0, 12.2, 11.7, 13.0; 11008 outputs 19.1, 20.5,
-// 23.5, 22.0, 25.1.
+// its start and its slab), up to a workgroup per CU: with a few more, some CUs
+// have two and the rest wait for them.  Forward, us, weights from memory, 8
+// adapters of rank 16, up to 256 and up to 288: one token, 4096 x 4096, 13.6
+// (195 workgroups) and 15.0 (260); 2048 x 4096, 10.5 and 11.3; 8192 x 4096, 19.4
+// and 24.6; 32 tokens, 5120 x 4096, 15.8 and 20.0; up to as many as are resident
+// (three to a CU) 15.0, 16.8 for 32 tokens, 4096 x 4096 (14.7).  Few64, where two
+// to a CU are resident, up to 256 and up to 512: 100 tokens, 2880 x 5120, 19.9
+// and 21.7; 201, 29.0 and 29.1; 256, 4096 x 4096, 38.6 and 35.9.
 Plan plan_both(const ProjArgs& p) {
   const int cols = p.N + proj_slots(p.T, p.L) * p.r, stages = (p.K + BK - 1) / BK;
   const bool few32 = p.T <= 32;
@@ -554,7 +558,7 @@ Plan plan_both(const ProjArgs& p) {
   }
   Plan best{few32 ? Plan::FEW32 : Plan::FEW64, 1};
   double least = 1e9;
-  for (int s = 1; s == 1 || (s * tiles <= (few32 ? 288 : 256) && s <= 16 && 2 * s <= stages); ++s) {
+  for (int s = 1; s == 1 || (s * tiles <= 256 && s <= 16 && 2 * s <= stages); ++s) {
     const double us = (stages + s - 1) / s * 0.2 + s * (0.35 + 1.5e-6 * p.T * cols);
     if (us < least) {
       least = us;

@@ -33,8 +33,14 @@ def sorted_forward(T, N, L, r):
     return not f(T, N, L, r)
 
 
-def few_form(T, K, N, L, r):
+def few_plan(T, K, N, L, r):
+    """The tile and the K splits of a batch without an order."""
     f = lm.load_library()._ZN7moelora14proj_both_planEiiiii
     f.argtypes, f.restype = [ctypes.c_int] * 5, ctypes.c_int
     plan = f(T, K, N, L, r)
-    return TILES[plan // 32], plan % 32 > 1
+    return TILES[plan // 32], plan % 32
+
+
+def few_form(T, K, N, L, r):
+    tile, splits = few_plan(T, K, N, L, r)
+    return tile, splits > 1
