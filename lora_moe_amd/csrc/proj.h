@@ -109,7 +109,8 @@ int launch_proj_grads(const ProjArgs& p, const ProjGrads& g, hipStream_t st);
 
 // x [W; A]^T, fp32, into slabs [proj_both_splits][T][N + proj_slots r]: of at most
 // 64 tokens and more adapters those that are met (place: [64], which of them a
-// token's is), else of all adapters.
+// token's is), else of all adapters, met or not: their A are L r columns beside N,
+// no more than the tokens have at most.
 int proj_slots(int T, int L);
 int proj_both_splits(const ProjArgs& p);
 int launch_proj_both(const ProjArgs& p, const uint16_t* x, const uint16_t* W, const uint16_t* A, float* slabs,

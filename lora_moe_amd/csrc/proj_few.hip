@@ -10,9 +10,10 @@
 // splits up and works on single outputs in fp32, so nothing of one adapter can
 // reach another's tokens.
 //
-// What bounds it: the weights' stream from memory at 4.9 TB/s (32 tokens, 4096 x
-// 11008, rank 32: 17.6 us for 98 MB, and 5.5 for the second launch); with a single
-// token, 4096 x 4096, 7.5 and 3.7 us, a kernel's start and first trip each.
+// What bounds it: the weights' stream from memory at 4.1 TB/s (32 tokens, 4096 x
+// 11008, rank 32: 24 us for 98 MB, and 6 for the second launch; weights that are
+// in the cache already take 18 and 5.5); with a single token, 4096 x 4096, 10.6
+// and 3.9 us, a kernel's start and first trip each.
 #include <algorithm>
 
 #include "device_util.h"
@@ -36,7 +37,7 @@ struct JoinArgs {
 // (r / 8 of them with 8 ranks each) share an output's row of B and take G
 // outputs in turn, so that a wavefront reads its 64 outputs' rows as whole
 // lines, and before z is there.  32 tokens, 11008 outputs, rank 32 (11 MB of B,
-// a few of sums): 5.5 us, the chain of id, place, z and barrier most of it.
+// a few of sums): 6.2 us, the chain of id, place, z and barrier most of it.
 template <int G>
 __global__ __launch_bounds__(256) void proj_few_join_kernel(JoinArgs a) {
   __shared__ __attribute__((aligned(16))) float zs[128];
@@ -95,10 +96,10 @@ __global__ __launch_bounds__(256) void proj_few_join_kernel(JoinArgs a) {
 
 // Products of tokens, outputs and rank in the second launch, at most, and tokens
 // (those beyond take 16 KB of B's rows and more for a tile's worth of outputs).
-// Measured, us, so and sorted: 400 tokens, 2048 x 4096, rank 64 (105 M) 35 and
-// 46; 256, 4096 x 11008, 32 (90 M) 54 and 57; 400, 4096 x 11008, 32 (141 M) 84
-// and 80; 1001, 4096 x 4096, 16 (66 M) 66 and 52; 100, 2880 x 2880, 16 (5 M) 14
-// and 33.
+// Measured, us, so and sorted, inputs from memory: 400 tokens, 2048 x 4096, rank
+// 64 (105 M) 35 and 42; 256, 4096 x 11008, 32 (90 M) 61 and 73; 400, 4096 x 11008,
+// 32 (141 M) 87 and 94, from the cache 84 and 80; 1001, 4096 x 4096, 16 (66 M) 76
+// and 58; 100, 2880 x 2880, 16 (5 M) 14 and 30.
 constexpr int64_t kProjFew = 96 << 20;
 constexpr int kProjFewTokens = 512;
 

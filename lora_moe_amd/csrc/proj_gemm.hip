@@ -24,10 +24,10 @@
 // addresses when their turn comes.
 //
 // What bounds it: with large tiles the matrix cores at the clock that the
-// card's power leaves them (8192 tokens, 4096 x 4096, rank 16: 219 us, 1.26
-// PFLOP/s; 7168 x 7168, rank 64: 719 us, 1.19 with the adapters' stages, of
-// which 37 us are theirs where the flops would take 17: their first touch of
-// B comes late from memory).  With a workgroup per CU the copies (0.34 us a
+// card's power leaves them (8192 tokens, 4096 x 4096, rank 16: 219 us, 1.29
+// PFLOP/s with the adapters' stages; 7168 x 7168, rank 64: 743 us, 1.17, of
+// which 50 to 60 us are theirs where the flops would take 25: their first touch
+// of B comes late from memory).  With a workgroup per CU the copies (0.34 us a
 // stage of 32 KB, 100 GB/s to a CU), and up to 201 tokens a first trip through
 // memory and the weights behind it.  (BOTH, a decode batch's x [W; A]^T without
 // an order, is described in proj_few.hip.)
@@ -472,8 +472,9 @@ typedef FfnCfg<128, 128, 2, 2> Small;
 // 2 wavefronts with 64 x 64 each read a third less from LDS than 2 x 4 with 64 x
 // 32 (1001 tokens with order and shrink, us: 2880 x 2880, rank 32, 44.7 and
 // 45.6, 4096 x 4096, rank 16, 52.6 and 54.1); one such group takes 2 us more than
-// 2 x 4.  2880 x 2880 (184 tiles): 24 us, of which 8.5 are launch, first trip
-// through memory and epilogue; adapters' stages 2 to 3 more.
+// 2 x 4.  2880 x 2880 (184 tiles): 24 us with inputs from the cache, 30
+// from memory, of which 8.5 are launch, first trip through memory and epilogue;
+// adapters' stages 4 more.
 typedef SliceCfg<128, 128, 2, 2, 2> Deep;
 // Decode batches: small tiles of few wavefronts, several workgroups to a CU, so
 // that nearly all of its LDS is weights on their way (up to 32 tokens three or
@@ -503,9 +504,10 @@ int launch_cfg(TileArgs a, hipStream_t st) {
 
 // Which tile, and how many K splits: the rule of ffn_gemm.hip, or, up to a
 // workgroup per CU in all, Few64 or Deep (0.33 and 0.45 us a stage; a launch for
-// the join and the slabs' way to memory and back as there).  512 tokens, 2880 x
-// 2880, rank 64 with its order and shrink: 46 us with Few64 (184 tiles), 55 with
-// Deep; 1001 tokens, rank 32 (368 and 184 tiles): 49 and 44.
+// the join and the slabs' way to memory and back as there).  520 tokens, 2880 x
+// 2880, rank 64 with its order and shrink: 50 us with Few64 (207 tiles), 60 with
+// Deep; 513 tokens, rank 16, 35 and 41; 1001 tokens, rank 32 (368 and 184 tiles),
+// 51 with Deep, 64 without; 4096 x 4096, rank 16, 58 and 76.
 struct Plan {
   enum Tile { BIG, SMALL, DEEP, FEW64, FEW32 } tile;
   int splits;

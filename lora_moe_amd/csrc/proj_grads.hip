@@ -9,8 +9,9 @@
 // several pieces puts fp32 sums into slabs, which a second kernel adds in their
 // order.  What is left of a value behind its first part may be 0 or of the other
 // sign, so an infinity or NaN of x or dy meets the first part alone, whose
-// product with it is the value's; the others meet 0 there.  8192 tokens, 4096 x 4096, rank 16: 27 us (152 MB at 5.4 TB/s) and 5 for
-// the slabs; 1001 tokens, 2880 x 2880, rank 32: 8 us.
+// product with it is the value's; the others meet 0 there.  8192
+// tokens, 4096 x 4096, rank 16: 30 us (156 MB at 5.3 TB/s) and 5 for the slabs;
+// 1001 tokens, 2880 x 2880, rank 32: 9.6 us.
 #include "internal.h"
 #include "proj.h"
 #include "tile.h"
@@ -209,8 +210,12 @@ int slabs_of(int T, int rows) { return 2 * (T / rows); }
 
 // Enough pieces to fill the chip with four rounds of workgroups, but at least 8r
 // rows each (a slab of r columns costs as much as 4r rows to write and read
-// again).  Few tokens of several adapters are not split at all, which spares the
-// join (4 us with 1001 tokens; a single adapter's would take 10 us longer).
+// again).  Few tokens beside a stack of more than four adapters are not split at
+// all, which spares the join where the batch has several of them.  L counts those
+// of the stack: how many are met is known on the device alone.  A backward for dA
+// and dB, us, unsplit and split, 16 adapters of rank 32, 2880 x 2880, 1001 tokens
+// of 16, 5, 2 and 1 of them: 24.3 and 25.9, 23.4 and 25.1, 26.5 and 27.0, 33.1 and
+// 28.1; 500 tokens of 16, 5 and 1: 23.8 and 25.3, 21.5 and 23.3, 26.2 and 26.3.
 int proj_grad_rows(int T, int K, int N, int L, int r) {
   if (T <= kMostRows && L > 4) return kMostRows;
   const int64_t rows = (int64_t)T * ((K + N) / WT + 1) / 1024;

@@ -4,8 +4,8 @@
 // are a few KB in the L2 cache, and integer counts do not depend on the order
 // of the LDS atomics), then places its own 256 tokens.  The first workgroup
 // writes the runs' tables as well.  What bounds it is the chain of its steps
-// (ids, counts, scans, ranks, tables), one after another: 6 to 8 us with 130 to
-// 1001 tokens, 9 with 8192 of 32 workgroups, at a few hundred KB in and out.
+// (ids, counts, scans, ranks, tables), one after another: 7 to 8 us with 130 to
+// 1001 tokens, 10 with 8192 of 32 workgroups, at a few hundred KB in and out.
 #include "proj.h"
 #include "sort_util.h"
 

@@ -7,10 +7,10 @@
 // as a stream of rows from anywhere: a row's 128 bytes of a chunk are whole
 // lines.  A's rows (k contiguous) come straight into registers; B [N][r] is
 // transposed on the way, through the wavefront's own LDS
-// (ds_read_b64_tr_b16).  8192 tokens, 4096 wide, rank 16: 28 us forward, 24
-// backward (2.6 and 3.1 TB/s); 7168 wide, rank 64: 44 us, 177 MB from memory for
-// 117 MB of x, since every piece reads its adapter's A again; 1001 tokens, 2880
-// wide, rank 32: 12 and 8 us, most of it the order's tables, the first rows and
+// (ds_read_b64_tr_b16).  8192 tokens, 4096 wide, rank 16: 35 us forward, 28
+// backward (2.2 and 2.7 TB/s; 28 and 24 where x and dy are in the cache); 7168
+// wide, rank 64: 50 us, 171 MB from memory for 117 MB of x, since every piece
+// reads its adapter's A again; 1001 tokens, 2880 wide, rank 32: 12 and 10 us, most of it the order's tables, the first rows and
 // the sums, one after another.
 #include "internal.h"
 #include "proj.h"

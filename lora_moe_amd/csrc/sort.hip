@@ -13,8 +13,8 @@
 // the same whatever their order).  8192 tokens of 7168 bf16 values, top-8: sort
 // 228 us at 4.7 TB/s and 13 for the order, back 177 at 6.0; 4096 tokens of 2048
 // fp32 values: 64 (4.9 TB/s) and 10, 54 (5.5), gradient 126 (4.8).  A large copy
-// reaches 4.4 to 4.9.  1001 tokens of 2880 fp16 values, top-4: 10.8, 6.5 and
-// 11.3 us, a third of them a kernel's start and first trip.
+// reaches 4.4 to 4.9.  1001 tokens of 2880 fp16 values, top-4: 11, 7 and 13
+// us, a third of them a kernel's start and first trip.
 #include <algorithm>
 
 #include "abi_util.h"
