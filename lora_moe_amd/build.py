@@ -75,11 +75,11 @@ def build(jobs: int | None = None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, SO)
-    if os.path.exists(OPERANDS):
-        os.remove(OPERANDS)  # none rather than one of another build
     try:
         build_operands()
     except (ImportError, RuntimeError) as e:
+        if os.path.exists(OPERANDS):
+            os.remove(OPERANDS)  # none rather than an older one
         warnings.warn(f"{SO} is built, lora_moe_amd._operands is not: {e}")
     return SO
 
